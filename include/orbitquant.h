@@ -79,13 +79,17 @@ enum {
                                      Method 5: INT4 weight-only RTN, no
                                      rotation, 16-bit activations); see
                                      oq_layer_create                         */
-  OQ_FLAG_FP8_CONTRACTION = 8     /* lower-precision contraction mode: both
+  OQ_FLAG_FP8_CONTRACTION = 8,    /* lower-precision contraction mode: both
                                      operands' 4-bit codes decode to e4m3 and
                                      multiply on kind::f8f6f4 tensor cores
                                      (twice the fp16 rate).  Same codes, but y
                                      carries the e4m3 rounding of the levels
                                      and does not meet the 1e-3 bound of the
                                      default mode; see oq_layer_create       */
+  OQ_FLAG_MICROSCALED = 16        /* block-scaled operands (e2m1 or e4m3
+                                     elements, one power-of-two scale per 32)
+                                     in place of rotation and codebooks; see
+                                     oq_layer_create and oq_linear_mx        */
 };
 
 /*
@@ -154,6 +158,13 @@ oq_status oq_rotation_build(int32_t d, uint64_t seed, int32_t flags, uint32_t* p
  * decode both operands' levels to e4m3 (each codebook scaled so its levels
  * land closest to e4m3 values) and accumulate in fp32.  The fp16-level calls
  * (oq_rotate_quantize_levels, oq_linear_levels) return OQ_ERR_UNSUPPORTED.
+ *
+ * With OQ_FLAG_MICROSCALED (alone in `flags`) the layer multiplies microscaled
+ * operands (oq_linear_mx): a_bits 4 or 8, w_bits 4, d_in % 32 == 0,
+ * d_in < 65536, d_out % 16 == 0; `seed` is not used.  Its operands come from
+ * oq_mx_quantize and oq_rms_norm_mx; every call that takes a rotation,
+ * codebooks, norms or prepared weights returns OQ_ERR_UNSUPPORTED on it, and
+ * the workspace sizes are 0.
  */
 typedef struct oq_layer oq_layer;
 
@@ -432,6 +443,83 @@ size_t oq_linear_fused_host_workspace_size(const oq_layer* layer, int32_t x_dtyp
 oq_status oq_linear_fused_host(const oq_layer* layer, const void* x_host, int32_t x_dtype, int64_t T,
                                const uint32_t* Wcodes, const float* r, void* y_host, int32_t y_dtype,
                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Microscaled operands (OCP Microscaling Formats v1.0; the pages have no
+ * counterpart: these are the block-scaled formats that sm_100a's tensor cores
+ * multiply as stored, for layers that take no rotation).  Blocks of 32
+ * neighbouring elements of a row share one scale.
+ *   element  bits = 4: e2m1, +-{0, .5, 1, 1.5, 2, 3, 4, 6}; bits = 8: e4m3, up
+ *            to 448
+ *   scale    E8M0: code c stands for 2^(c - 127), 255 for NaN
+ *   codes    [rows, row bytes], a row padded with zero codes to a multiple of
+ *            128 elements; of two 4-bit codes in a byte the even element is
+ *            the low half
+ *   scales   tiles of 128 rows x 4 blocks, the order the tensor cores take:
+ *            byte [row / 128][block / 4][row % 32][row / 32 % 4][block % 4].
+ *            Places of a tile that belong to no row or no block hold code 0.
+ * oq_mx_codes_size and oq_mx_scales_size give the bytes of both arrays (0 for
+ * arguments out of range).  Every call takes d % 32 == 0, d < 65536, bits 4
+ * or 8 (else OQ_ERR_UNSUPPORTED), codes 32-byte and scales 16-byte aligned,
+ * and no overlap between inputs and outputs except where stated.  rows = 0 is
+ * a no-op.  No call holds state, allocates or waits on the host; calls may
+ * overlap and be captured into graphs.
+ *
+ * oq_mx_quantize -- rows of bf16 or fp32 to codes and scales:
+ *   E = floor(log2(max_i |x_i|)) - (2 for e2m1, 8 for e4m3), at least -127
+ *   code of x_i 2^-E, rounded to nearest even, saturating; scale code E + 127
+ * A block of zeros gets scale code 0.  A block that holds an infinity or a NaN
+ * gets scale code 255 and zero codes: all of it reads as NaN.  Activations and
+ * weight rows are quantized by the same call.
+ *
+ * oq_mx_dequantize -- codes and scales back to x [rows, d] (bf16 or fp32,
+ * 16-byte aligned): the values, exact in fp32, and in bf16 but for results
+ * below its least normal number.
+ */
+size_t oq_mx_codes_size(int64_t rows, int32_t d, int32_t bits);
+size_t oq_mx_scales_size(int64_t rows, int32_t d);
+oq_status oq_mx_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t d, int32_t bits, uint8_t* codes,
+                         uint8_t* scales, void* stream);
+oq_status oq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t d, int32_t bits, void* x,
+                           int32_t x_dtype, void* stream);
+
+/*
+ * oq_rms_norm_mx -- the residual's addition, a root-mean-square norm and its
+ * quantization in one pass over the rows:
+ *   h = x + residual,  n_i = h_i g_i / sqrt(mean(h^2) + eps),  codes of n
+ * in fp32 throughout, the norm from the unrounded h.
+ *   x, residual   device [rows, d], bf16 or fp32 (x_dtype for both); residual
+ *                 may be NULL (h = x).
+ *   gain          device [d], bf16 or fp32 (gain_dtype), or NULL (ones).
+ *   residual_out  device [rows, d] of x_dtype: h rounded to nearest even, or
+ *                 NULL (not kept); it may be x or residual itself.
+ *   codes, scales of n, as oq_mx_quantize writes them (bits 8, or 4).
+ * A row of zeros gives zeros (eps > 0).  A NaN or an infinity in a row makes
+ * the whole row's norm NaN or 0 by the formula.  The sum of squares is fp32:
+ * rows whose squares overflow it are outside the supported range.
+ * Errors: OQ_ERR_INVALID_ARG for a negative or non-finite eps, a residual_out
+ * without a residual, a null or misaligned (16 bytes) pointer.
+ */
+oq_status oq_rms_norm_mx(const void* x, const void* residual, int32_t x_dtype, const void* gain, int32_t gain_dtype,
+                         float eps, int64_t rows, int32_t d, int32_t bits, void* residual_out, uint8_t* codes,
+                         uint8_t* scales, void* stream);
+
+/*
+ * oq_linear_mx -- the product of microscaled operands on a layer created with
+ * OQ_FLAG_MICROSCALED:
+ *   y[t, o] = sum_k a[t, k] w[o, k]
+ *   codes, scales    activations [T, d_in] in a_bits, from oq_mx_quantize or
+ *                    oq_rms_norm_mx.
+ *   Wcodes, Wscales  weights [d_out, d_in] in 4 bits, from oq_mx_quantize.
+ *   y                device [T, d_out], fp32 or bf16 as y_dtype says (the fp32
+ *                    sum rounded to nearest even), 16-byte aligned.
+ * The tensor cores multiply the codes and apply the scales; sums are fp32 in
+ * tensor memory.  Results repeat bit for bit.  A NaN block makes the rows (or
+ * columns) of y that it enters NaN.  The layer must belong to the current
+ * device.  A bounded wait that runs out is reported by oq_poll_error.
+ */
+oq_status oq_linear_mx(const oq_layer* layer, const uint8_t* codes, const uint8_t* scales, int64_t T,
+                       const uint8_t* Wcodes, const uint8_t* Wscales, void* y, int32_t y_dtype, void* stream);
 
 /* Reads and clears the layer's device error word.  Synchronizes the device.
  * Returns OQ_OK or OQ_ERR_TIMEOUT (OQ_ERR_DEVICE for a bit this version does

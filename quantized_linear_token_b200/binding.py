@@ -8,6 +8,7 @@ if the library is missing or no GPU is present the calls raise.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -23,6 +24,7 @@ OQ_FLAG_SIGNS = 1
 OQ_FLAG_GAUSSIAN_MARGINAL = 2
 OQ_FLAG_WEIGHT_ONLY_INT4 = 4
 OQ_FLAG_FP8_CONTRACTION = 8
+OQ_FLAG_MICROSCALED = 16
 # oq_linear_fused decodes the weight codes once per call from this many tokens
 # on (bf16 x, d_out % 256 == 0, a workspace of oq_linear_fused_workspace_size)
 W16_MIN_T = 1024
@@ -35,6 +37,7 @@ EXPORTS = (
     "oq_linear_fused", "oq_linear_fused_decoded_workspace_size", "oq_linear_fused_decoded",
     "oq_rotate_quantize_levels", "oq_linear_levels", "oq_weight_levels", "oq_linear_decoded",
     "oq_linear_fused_static", "oq_linear_fused_host_workspace_size", "oq_linear_fused_host",
+    "oq_mx_codes_size", "oq_mx_scales_size", "oq_mx_quantize", "oq_mx_dequantize", "oq_rms_norm_mx", "oq_linear_mx",
     "oq_poll_error", "oq_check_wait_timeout", "oq_last_error", "oq_status_string",
 )
 
@@ -99,6 +102,12 @@ def load_library(path: str = LIB_PATH):
         "oq_linear_fused_static": (i32, [vp, vp, i32, i64, vp, vp, vp, vp]),
         "oq_weight_save": (i32, [vp, vp, vp, ctypes.c_char_p]),
         "oq_weight_load": (i32, [vp, ctypes.c_char_p, vp, vp]),
+        "oq_mx_codes_size": (sz, [i64, i32, i32]),
+        "oq_mx_scales_size": (sz, [i64, i32]),
+        "oq_mx_quantize": (i32, [vp, i32, i64, i32, i32, vp, vp, vp]),
+        "oq_mx_dequantize": (i32, [vp, vp, i64, i32, i32, vp, i32, vp]),
+        "oq_rms_norm_mx": (i32, [vp, vp, i32, vp, i32, ctypes.c_float, i64, i32, i32, vp, vp, vp, vp]),
+        "oq_linear_mx": (i32, [vp, vp, vp, i64, vp, vp, vp, i32, vp]),
         "oq_poll_error": (i32, [vp]),
         "oq_check_wait_timeout": (i32, [vp, ctypes.c_uint32, vp]),
         "oq_last_error": (ctypes.c_char_p, []),
@@ -412,6 +421,127 @@ def oq_weight_load(layer: Layer, path: str, Wcodes=None, r=None):
     _check(load_library().oq_weight_load(layer.handle, os.fsencode(path), _dev(Wcodes, "Wcodes"), _dev(r, "r")),
            "oq_weight_load")
     return Wcodes, r
+
+
+# ------------------------------------------------------------------ microscaled operators
+def oq_mx_codes_size(rows: int, d: int, bits: int) -> int:
+    return int(load_library().oq_mx_codes_size(rows, d, bits))
+
+
+def oq_mx_scales_size(rows: int, d: int) -> int:
+    return int(load_library().oq_mx_scales_size(rows, d))
+
+
+def _on_device(device):
+    """A context in which `device` is the current one (the C calls work on the current device)."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _mx_arrays(codes, scales, rows: int, d: int, bits: int, device, name: str):
+    """Codes [rows, row bytes] and scale tiles [row tiles, column tiles, 32, 4, 4]
+    of a [rows, d] operand: new ones, or the given ones checked."""
+    torch = _torch()
+    ct = (d + 127) // 128
+    for t, shape, what in ((codes, (rows, ct * 16 * bits), "codes"), (scales, ((rows + 127) // 128, ct, 32, 4, 4), "scales")):
+        if t is not None and (t.dtype != torch.uint8 or tuple(t.shape) != shape or t.device != device):
+            raise ValueError(f"{name}{what} must be uint8 {list(shape)} on {device}")
+    if codes is None:
+        codes = torch.empty((rows, ct * 16 * bits), dtype=torch.uint8, device=device)
+    if scales is None:
+        scales = torch.empty(((rows + 127) // 128, ct, 32, 4, 4), dtype=torch.uint8, device=device)
+    return codes, scales
+
+
+def _mx_shape(t, name: str, bits: int):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    if bits not in (4, 8) or t.shape[1] == 0 or t.shape[1] % 32:
+        raise ValueError(f"bits must be 4 or 8 and {name}'s width a positive multiple of 32")
+
+
+def oq_mx_quantize(x, bits: int, codes=None, scales=None):
+    """x [rows, d] (bf16/fp32, CUDA) -> (codes [rows, row bytes] uint8, scales
+    [row tiles, column tiles, 32, 4, 4] uint8): microscaled e2m1 (bits = 4) or
+    e4m3 (bits = 8) elements, one E8M0 scale per 32 (include/orbitquant.h)."""
+    _mx_shape(x, "x", bits)
+    rows, d = x.shape
+    px, dt = _dev(x, "x"), _dtype_code(x)
+    codes, scales = _mx_arrays(codes, scales, rows, d, bits, x.device, "")
+    with _on_device(x.device):
+        _check(load_library().oq_mx_quantize(px, dt, rows, d, bits, _dev(codes, "codes"), _dev(scales, "scales"),
+                                             _stream(x)), "oq_mx_quantize")
+    return codes, scales
+
+
+def oq_mx_dequantize(codes, scales, d: int, bits: int, dtype=None, x=None):
+    """Codes and scales of a [rows, d] operand -> its values [rows, d] (fp32 by
+    default, or bf16)."""
+    torch = _torch()
+    if codes.dim() != 2 or bits not in (4, 8) or d <= 0 or d % 32:
+        raise ValueError("codes must be a matrix, bits 4 or 8 and d a positive multiple of 32")
+    rows = codes.shape[0]
+    codes, scales = _mx_arrays(codes, scales, rows, d, bits, codes.device, "")
+    if x is None:
+        x = torch.empty((rows, d), dtype=torch.float32 if dtype is None else dtype, device=codes.device)
+    elif tuple(x.shape) != (rows, d) or x.device != codes.device or (dtype is not None and x.dtype != dtype):
+        raise ValueError(f"x must be [{rows}, {d}] on {codes.device}")
+    with _on_device(codes.device):
+        _check(load_library().oq_mx_dequantize(_dev(codes, "codes"), _dev(scales, "scales"), rows, d, bits,
+                                               _dev(x, "x"), _dtype_code(x), _stream(codes)), "oq_mx_dequantize")
+    return x
+
+
+def oq_rms_norm_mx(x, gain=None, residual=None, eps: float = 1e-6, bits: int = 8, residual_out=None, codes=None,
+                   scales=None):
+    """h = x + residual, its root-mean-square norm times gain, quantized: x,
+    residual [rows, d] (bf16/fp32, CUDA), gain [d] -> (codes, scales, h rounded
+    to x's type, or None without a residual).  residual_out may be x or
+    residual itself."""
+    torch = _torch()
+    _mx_shape(x, "x", bits)
+    rows, d = x.shape
+    px, dt = _dev(x, "x"), _dtype_code(x)
+    if gain is not None and (tuple(gain.shape) != (d,) or gain.device != x.device):
+        raise ValueError(f"gain must be [{d}] on {x.device}")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != x.device):
+            raise ValueError(f"{name} must have x's shape, type and device")
+    codes, scales = _mx_arrays(codes, scales, rows, d, bits, x.device, "")
+    with _on_device(x.device):
+        _check(load_library().oq_rms_norm_mx(
+            px, None if residual is None else _dev(residual, "residual"), dt,
+            None if gain is None else _dev(gain, "gain"), OQ_DTYPE_F32 if gain is None else _dtype_code(gain), eps,
+            rows, d, bits, None if residual_out is None else _dev(residual_out, "residual_out"),
+            _dev(codes, "codes"), _dev(scales, "scales"), _stream(x)), "oq_rms_norm_mx")
+    return codes, scales, residual_out
+
+
+def oq_linear_mx(layer: Layer, codes, scales, Wcodes, Wscales, y=None, y_dtype=None):
+    """Microscaled activations (codes, scales of layer.a_bits) times 4-bit
+    microscaled weights -> y [T, d_out] fp32 (or bf16), on a layer created with
+    OQ_FLAG_MICROSCALED."""
+    if not layer.flags & OQ_FLAG_MICROSCALED:
+        raise ValueError("the layer was not created with OQ_FLAG_MICROSCALED")
+    if codes.dim() != 2:
+        raise ValueError("codes must be a matrix")
+    T, device = codes.shape[0], codes.device
+    _mx_arrays(codes, scales, T, layer.d_in, layer.a_bits, device, "")
+    _mx_arrays(Wcodes, Wscales, layer.d_out, layer.d_in, 4, device, "W")
+    y, ycode = _y_out(y, T, layer.d_out, y_dtype, device)
+    if tuple(y.shape) != (T, layer.d_out) or y.device != device:
+        raise ValueError(f"y must be [{T}, {layer.d_out}] on {device}")
+    with _on_device(device):
+        _check(load_library().oq_linear_mx(layer.handle, _dev(codes, "codes"), _dev(scales, "scales"), T,
+                                           _dev(Wcodes, "Wcodes"), _dev(Wscales, "Wscales"), _dev(y, "y"), ycode,
+                                           _stream(codes)), "oq_linear_mx")
+    return y
 
 
 def oq_poll_error(layer: Layer) -> None:

@@ -153,8 +153,12 @@ static oq_status create_int4_layer(int32_t d_in, int32_t d_out, uint64_t seed, i
   return OQ_OK;
 }
 
-static oq_status not_for_int4(const oq_layer* L, const char* who) {
-  return fail(OQ_ERR_UNSUPPORTED, std::string(who) + ": not available on an INT4 weight-only layer");
+// the calls that need a rotation and codebooks
+static bool no_codebooks(const oq_layer* L) { return L->int4_only || L->mx; }
+
+static oq_status not_for_these(const oq_layer* L, const char* who) {
+  return fail(OQ_ERR_UNSUPPORTED, std::string(who) + (L->mx ? ": not available on a microscaled layer"
+                                                            : ": not available on an INT4 weight-only layer"));
 }
 
 oq_status oq_layer_create(int32_t d_in, int32_t d_out, uint64_t seed, int32_t a_bits, int32_t w_bits,
@@ -162,6 +166,7 @@ oq_status oq_layer_create(int32_t d_in, int32_t d_out, uint64_t seed, int32_t a_
   if (!out) return fail(OQ_ERR_INVALID_ARG, "oq_layer_create: out is null");
   *out = nullptr;
   if (flags & OQ_FLAG_WEIGHT_ONLY_INT4) return create_int4_layer(d_in, d_out, seed, a_bits, w_bits, flags, out);
+  if (flags & OQ_FLAG_MICROSCALED) return create_mx_layer(d_in, d_out, seed, a_bits, w_bits, flags, out);
   oq_status st = check_shape(d_in, d_out, a_bits, w_bits);
   if (st != OQ_OK) return st;
   if (flags & ~(OQ_FLAG_SIGNS | OQ_FLAG_GAUSSIAN_MARGINAL | OQ_FLAG_FP8_CONTRACTION))
@@ -314,7 +319,7 @@ oq_status oq_layer_get_info(const oq_layer* L, oq_layer_info* out) {
 
 oq_status oq_layer_get_perm(const oq_layer* L, uint32_t* perm) {
   if (!L || !perm) return fail(OQ_ERR_INVALID_ARG, "oq_layer_get_perm: null argument");
-  if (L->int4_only) return not_for_int4(L, "oq_layer_get_perm");
+  if (no_codebooks(L)) return not_for_these(L, "oq_layer_get_perm");
   std::memcpy(perm, L->perm_host.data(), L->perm_host.size() * sizeof(uint32_t));
   return OQ_OK;
 }
@@ -364,7 +369,7 @@ static oq_status rq(const oq_layer* L, const void* x, int32_t dtype, int64_t row
 oq_status oq_rotate_quantize(const oq_layer* L, const void* x, int32_t x_dtype, int64_t T, uint32_t* codes,
                              float* s, void* stream) {
   if (!L) return fail(OQ_ERR_INVALID_ARG, "oq_rotate_quantize: layer is null");
-  if (L->int4_only) return not_for_int4(L, "oq_rotate_quantize");
+  if (no_codebooks(L)) return not_for_these(L, "oq_rotate_quantize");
   if (T < 0) return fail(OQ_ERR_INVALID_ARG, "oq_rotate_quantize: T < 0");
   if (T == 0) return OQ_OK;
   oq_status st = check_rows_input(x, x_dtype, "oq_rotate_quantize");
@@ -381,6 +386,7 @@ oq_status oq_weight_prepare(const oq_layer* L, const void* W, int32_t W_dtype, u
   if (st != OQ_OK) return st;
   if (!Wcodes || !r || !aligned(Wcodes, 16) || !aligned(r, 4))
     return fail(OQ_ERR_INVALID_ARG, "oq_weight_prepare: Wcodes (16-byte) / r (4-byte) pointers invalid");
+  if (L->mx) return not_for_these(L, "oq_weight_prepare");
   if (L->int4_only) return rtn4_prepare_launch(W, W_dtype, L->d_out, L->d_in, Wcodes, r, stream);
   return rq(L, W, W_dtype, L->d_out, L->w_bits, L->bins_w, Wcodes, r, stream);
 }
@@ -441,7 +447,7 @@ static oq_status check_y_dtype(int32_t y_dtype, const char* who) {
 oq_status oq_linear(const oq_layer* L, const uint32_t* codes, const float* s, int64_t T, const uint32_t* Wcodes,
                     const float* r, void* y, int32_t y_dtype, void* stream) {
   if (!L) return fail(OQ_ERR_INVALID_ARG, "oq_linear: layer is null");
-  if (L->int4_only) return not_for_int4(L, "oq_linear");
+  if (no_codebooks(L)) return not_for_these(L, "oq_linear");
   if (check_y_dtype(y_dtype, "oq_linear") != OQ_OK) return OQ_ERR_INVALID_ARG;
   if (T < 0) return fail(OQ_ERR_INVALID_ARG, "oq_linear: T < 0");
   if (T == 0) return OQ_OK;
@@ -485,7 +491,7 @@ static size_t full_workspace(const oq_layer* L, int64_t T, size_t base) {
 
 // the least workspace oq_linear_fused accepts (without the decoded weights)
 static size_t min_workspace(const oq_layer* L, int64_t T) {
-  if (!L || T <= 0 || L->int4_only) return 0;
+  if (!L || T <= 0 || no_codebooks(L)) return 0;
   size_t a = fused_codes_bytes(L, T);
   if (L->d_out % 256 == 0) a = std::max(a, fused_f16_bytes(L, T));
   return round256(a) + (size_t)T * 4;
@@ -542,7 +548,7 @@ static oq_status rq_levels(const oq_layer* L, const void* x, int32_t x_dtype, in
 oq_status oq_rotate_quantize_levels(const oq_layer* L, const void* x, int32_t x_dtype, int64_t T, uint16_t* a16,
                                     float* s, void* stream) {
   if (!L) return fail(OQ_ERR_INVALID_ARG, "oq_rotate_quantize_levels: layer is null");
-  if (L->int4_only) return not_for_int4(L, "oq_rotate_quantize_levels");
+  if (no_codebooks(L)) return not_for_these(L, "oq_rotate_quantize_levels");
   if (L->fp8) return fail(OQ_ERR_UNSUPPORTED, "oq_rotate_quantize_levels: the fp16-level route is not used in the FP8 mode");
   if (T < 0) return fail(OQ_ERR_INVALID_ARG, "oq_rotate_quantize_levels: T < 0");
   if (T == 0) return OQ_OK;
@@ -558,7 +564,7 @@ oq_status oq_linear_levels(const oq_layer* L, const uint16_t* a16, const float* 
                            const float* r, void* y, int32_t y_dtype, void* stream) {
   if (!L) return fail(OQ_ERR_INVALID_ARG, "oq_linear_levels: layer is null");
   if (check_y_dtype(y_dtype, "oq_linear_levels") != OQ_OK) return OQ_ERR_INVALID_ARG;
-  if (L->int4_only) return not_for_int4(L, "oq_linear_levels");
+  if (no_codebooks(L)) return not_for_these(L, "oq_linear_levels");
   if (L->fp8) return fail(OQ_ERR_UNSUPPORTED, "oq_linear_levels: the fp16-level route is not used in the FP8 mode");
   if (T < 0) return fail(OQ_ERR_INVALID_ARG, "oq_linear_levels: T < 0");
   if (T == 0) return OQ_OK;
@@ -571,7 +577,7 @@ oq_status oq_linear_levels(const oq_layer* L, const uint16_t* a16, const float* 
 
 oq_status oq_weight_levels(const oq_layer* L, const uint32_t* Wcodes, uint16_t* w16, void* stream) {
   if (!L) return fail(OQ_ERR_INVALID_ARG, "oq_weight_levels: layer is null");
-  if (L->int4_only) return not_for_int4(L, "oq_weight_levels");
+  if (no_codebooks(L)) return not_for_these(L, "oq_weight_levels");
   if (L->fp8) return fail(OQ_ERR_UNSUPPORTED, "oq_weight_levels: the fp16-level route is not used in the FP8 mode");
   if (!Wcodes || !w16 || !aligned(Wcodes, 16) || !aligned(w16, 16))
     return fail(OQ_ERR_INVALID_ARG, "oq_weight_levels: Wcodes / w16 must be 16-byte aligned device pointers");
@@ -609,7 +615,7 @@ oq_status oq_linear_decoded(const oq_layer* L, const uint16_t* a16, const float*
                             const float* r, void* y, int32_t y_dtype, void* stream) {
   if (!L) return fail(OQ_ERR_INVALID_ARG, "oq_linear_decoded: layer is null");
   if (check_y_dtype(y_dtype, "oq_linear_decoded") != OQ_OK) return OQ_ERR_INVALID_ARG;
-  if (L->int4_only) return not_for_int4(L, "oq_linear_decoded");
+  if (no_codebooks(L)) return not_for_these(L, "oq_linear_decoded");
   if (L->fp8) return fail(OQ_ERR_UNSUPPORTED, "oq_linear_decoded: the fp16-level route is not used in the FP8 mode");
   if (T < 0) return fail(OQ_ERR_INVALID_ARG, "oq_linear_decoded: T < 0");
   if (T == 0) return OQ_OK;
@@ -729,6 +735,7 @@ static oq_status fused_checks(const oq_layer* L, const void* x, int32_t x_dtype,
                               const char* who) {
   const std::string w(who);
   if (!L) return fail(OQ_ERR_INVALID_ARG, w + ": layer is null");
+  if (L->mx) return not_for_these(L, who);
   if (T < 0) return fail(OQ_ERR_INVALID_ARG, w + ": T < 0");
   if (T == 0) return OQ_OK;
   oq_status st = check_rows_input(x, x_dtype, who);
@@ -756,7 +763,7 @@ oq_status oq_linear_fused(const oq_layer* L, const void* x, int32_t x_dtype, int
 }
 
 size_t oq_linear_fused_decoded_workspace_size(const oq_layer* L, int64_t T) {
-  if (!L || T <= 0 || L->int4_only || L->fp8 || L->d_out % 256) return 0;
+  if (!L || T <= 0 || no_codebooks(L) || L->fp8 || L->d_out % 256) return 0;
   return decoded_workspace(L, T);
 }
 
@@ -765,7 +772,7 @@ oq_status oq_linear_fused_decoded(const oq_layer* L, const void* x, int32_t x_dt
                                   void* stream) {
   const char* who = "oq_linear_fused_decoded";
   if (!L) return fail(OQ_ERR_INVALID_ARG, "oq_linear_fused_decoded: layer is null");
-  if (L->int4_only) return not_for_int4(L, who);
+  if (no_codebooks(L)) return not_for_these(L, who);
   if (L->fp8) return fail(OQ_ERR_UNSUPPORTED, "oq_linear_fused_decoded: the fp16-level route is not used in the FP8 mode");
   if (L->d_out % 256 != 0) return fail(OQ_ERR_UNSUPPORTED, "oq_linear_fused_decoded: needs d_out % 256 == 0");
   oq_status st = fused_checks(L, x, x_dtype, T, reinterpret_cast<const uint32_t*>(w16), r, y, y_dtype, workspace, who);

@@ -120,7 +120,7 @@ using namespace oq;
 extern "C" {
 
 size_t oq_linear_fused_host_workspace_size(const oq_layer* L, int32_t x_dtype, int64_t T) {
-  if (!L || T <= 0 || L->int4_only || (x_dtype != OQ_DTYPE_BF16 && x_dtype != OQ_DTYPE_F32)) return 0;
+  if (!L || T <= 0 || L->int4_only || L->mx || (x_dtype != OQ_DTYPE_BF16 && x_dtype != OQ_DTYPE_F32)) return 0;
   return io_layout(L, x_dtype, T).total;
 }
 

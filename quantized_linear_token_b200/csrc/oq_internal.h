@@ -25,6 +25,7 @@ struct oq_bin_table {
 struct oq_layer {
   int d_in, d_out, h, k, log_h, a_bits, w_bits, flags;
   bool int4_only;                     // OQ_FLAG_WEIGHT_ONLY_INT4: AdaLN path (no rotation or codebooks)
+  bool mx;                            // OQ_FLAG_MICROSCALED: block-scaled operands (no rotation or codebooks)
   bool fp8;                           // OQ_FLAG_FP8_CONTRACTION: levels decoded to e4m3, kind::f8f6f4 MMAs
   double a8_scale, w8_scale;          // e4m3 decode scale per codebook (fp8 mode)
   double a8_err, w8_err;              // their worst relative level rounding
@@ -58,6 +59,9 @@ namespace oq {
 
 void set_error(const std::string& msg);
 
+// the microscaled layer (oq_mx_api.cu)
+oq_status create_mx_layer(int32_t d_in, int32_t d_out, uint64_t seed, int32_t a_bits, int32_t w_bits, int32_t flags,
+                          oq_layer** out);
 // host math (oq_host.cpp)
 void make_permutation(int d, uint64_t seed, std::vector<uint32_t>& perm, std::vector<int8_t>* signs);
 oq_status design_codebook(int d, int bits, int flags, oq_codebook* out);

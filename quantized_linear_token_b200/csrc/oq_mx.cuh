@@ -1,0 +1,171 @@
+// Microscaled formats (OCP Microscaling Formats v1.0): blocks of 32 elements
+// along a row share one power-of-two scale.
+//   element  e2m1 (4 bits: +-{0, .5, 1, 1.5, 2, 3, 4, 6}) or e4m3 (8 bits, to 448)
+//   scale    E8M0: code c stands for 2^(c - 127), 255 for NaN
+// Rows are padded with zero codes to a multiple of 128 elements.  Scales are
+// stored in tiles of 128 rows x 4 blocks (512 bytes), the order in which the
+// tensor cores take them: byte [row / 128][block / 4][row % 32][row / 32 % 4][block % 4].
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "oq_internal.h"
+
+namespace oq {
+
+constexpr int MX_BLOCK = 32;       // elements per scale
+constexpr int MX_COLS = 128;       // elements per scale tile and row padding
+constexpr int MX_ROWS = 128;       // rows per scale tile
+constexpr int MX_TILE_BYTES = 512;
+
+__host__ __device__ inline int mx_col_tiles(int d) { return (d + MX_COLS - 1) / MX_COLS; }
+__host__ __device__ inline int64_t mx_row_tiles(int64_t rows) { return (rows + MX_ROWS - 1) / MX_ROWS; }
+__host__ __device__ inline int64_t mx_row_bytes(int d, int bits) { return (int64_t)mx_col_tiles(d) * (MX_COLS * bits / 8); }
+
+// 32-bit word of a scale tile that holds row r's four block scales
+__device__ __forceinline__ int mx_tile_word(int r) { return (r & 31) * 4 + ((r >> 5) & 3); }
+
+// Eight consecutive row elements in fp32: one 16-byte load of bf16, two of fp32.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ uint32_t mx_pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(mx_pack_bf16(v[0], v[1]), mx_pack_bf16(v[2], v[3]),
+                                            mx_pack_bf16(v[4], v[5]), mx_pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// eight fp32 -> eight e2m1 codes (round to nearest even, saturating at 6), element 0 in the low nibble
+__device__ __forceinline__ uint32_t cvt8_e2m1(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+// four fp32 -> four e4m3 codes (round to nearest even, saturating at 448)
+__device__ __forceinline__ uint32_t cvt4_e4m3(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// Codes of one thread's eight elements and its block's scale code.  Four
+// neighbouring lanes hold a block; every lane of the warp takes part.
+//   scale = 2^(floor(log2 max|v|) - emax), emax 2 (e2m1) or 8 (e4m3): the
+// biased exponent of the largest magnitude less emax, not below code 0.  The
+// products v / scale are exact except below 2^-126, where the elements round
+// to zero either way, so the only rounding is the one to the element type.
+// A block with an infinity or a NaN gets scale code 255 and zero elements, so
+// that all of it reads as NaN.
+template <int BITS>
+__device__ __forceinline__ uint32_t mx_quantize8(float (&v)[8], uint32_t (&out)[BITS / 4]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  const int e = (int)(m >> 23);
+  const int code = e == 255 ? 255 : max(e - (BITS == 4 ? 2 : 8), 0);
+  const float inv = __uint_as_float((uint32_t)(254 - (code == 255 ? 0 : code)) << 23);   // 2^(127 - code)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = code == 255 ? 0.f : v[i] * inv;
+  if constexpr (BITS == 4) {
+    out[0] = cvt8_e2m1(v);
+  } else {
+    out[0] = cvt4_e4m3(v[0], v[1], v[2], v[3]);
+    out[1] = cvt4_e4m3(v[4], v[5], v[6], v[7]);
+  }
+  return (uint32_t)code;
+}
+
+// the four block scales of 16 neighbouring lanes as one word (in every lane)
+__device__ __forceinline__ uint32_t mx_scale_word(uint32_t code) {
+  const int base = threadIdx.x & 16;
+  uint32_t w = 0u;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) w |= __shfl_sync(0xFFFFFFFFu, code, base + 4 * b) << (8 * b);
+  return w;
+}
+
+// launches (oq_mx_quant.cu, oq_mx_gemm.cu, oq_mx_small.cu); arguments checked by the entry points
+oq_status mx_quantize_launch(const void* x, int x_dtype, int64_t rows, int d, int bits, uint8_t* codes,
+                             uint8_t* scales, void* stream);
+oq_status mx_dequantize_launch(const uint8_t* codes, const uint8_t* scales, int64_t rows, int d, int bits, void* x,
+                               int x_dtype, void* stream);
+struct MxNormArgs {
+  const void* x;
+  const void* residual;   // or null: no addition
+  int x_dtype;
+  const void* gain;       // or null: ones
+  int gain_dtype;
+  float eps;
+  int64_t rows;
+  int d, bits;
+  void* residual_out;     // or null: not kept
+  uint8_t* codes;
+  uint8_t* scales;
+};
+oq_status mx_norm_launch(const MxNormArgs& a, void* stream);
+struct MxGemmArgs {
+  const uint8_t* a_codes;   // [T, row bytes] of a_bits
+  const uint8_t* a_scales;
+  const uint8_t* w_codes;   // [N, row bytes] of 4 bits
+  const uint8_t* w_scales;
+  void* y;                  // [T, N]
+  bool y_bf16;
+  int64_t T;
+  int N, K, a_bits;
+  int* err;
+};
+oq_status mx_gemm_launch(const MxGemmArgs& g, void* stream);
+oq_status mx_small_launch(const MxGemmArgs& g, void* stream);
+constexpr int MX_SMALL_MAX_T = 256;   // batches up to this size take the small-batch kernel
+
+}  // namespace oq

@@ -1,0 +1,133 @@
+// Inline PTX of the block-scaled tensor-core path (sm_100a): three-dimensional
+// TMA loads of scale tiles, the copy of scales from shared to tensor memory,
+// and tcgen05.mma with block scales, one CTA or a CTA pair.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+#include <string>
+
+#include "oq_mx.cuh"
+#include "oq_ptx.cuh"
+#include "oq_tmap.cuh"
+
+namespace oq {
+
+__device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* tmap, int32_t x, int32_t y, int32_t z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(smem_u32(dst_smem)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// the form for CTA pairs: bytes counted on a barrier that may lie in the peer CTA (no multicast)
+__device__ __forceinline__ void tma_load_3d_pair(void* dst_smem, const void* tmap, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(smem_u32(dst_smem)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
+      : "memory");
+}
+
+// Descriptor of a 512-byte scale tile for tcgen05.cp.32x128b: 32 rows of 16
+// bytes, unswizzled, groups of eight rows 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
+  d |= (uint64_t)(128 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+// One scale tile into four tensor-memory columns: column c, lane l gets the
+// 32-bit word of row 32 c + l (its four block scales), repeated in the four
+// lane quarters.  With CG = 2 each CTA of the pair copies from its own shared
+// memory, at the same offset, into its own tensor memory.  Copies and MMAs
+// issued by one thread run in issue order.
+template <int CG>
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Block-scaled MMA, K of 32 bytes per row: F4 multiplies 64 e2m1 by 64 e2m1
+// with two scales a row, otherwise 32 elements of 8-bit containers (e4m3, or
+// e2m1 in the low half of each 16-byte group's padding layout) with one.
+template <int CG, bool F4>
+__device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+#define OQ_MX_MMA(CGS, KIND, VEC)                                                                       \
+  asm volatile(                                                                                          \
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                   \
+      "tcgen05.mma.cta_group::" CGS ".kind::" KIND ".block_scale.scale_vec::" VEC                        \
+      " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),                                            \
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                           \
+      : "memory")
+  if constexpr (CG == 2 && F4) OQ_MX_MMA("2", "mxf4", "2X");
+  else if constexpr (CG == 2) OQ_MX_MMA("2", "mxf8f6f4", "1X");
+  else if constexpr (F4) OQ_MX_MMA("1", "mxf4", "2X");
+  else OQ_MX_MMA("1", "mxf8f6f4", "1X");
+#undef OQ_MX_MMA
+}
+
+// Instruction descriptor of the block-scaled kinds: K-major operands, E8M0
+// scales; a_fmt / b_fmt 1 for e2m1 in kind::mxf4, and 0 for e4m3, 5 for e2m1
+// in kind::mxf8f6f4.
+__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, uint32_t a_fmt, uint32_t b_fmt) {
+  return (a_fmt << 7) | (b_fmt << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27);
+}
+// the scale's place in its 32-bit column: byte 0..3 (one scale per MMA), or 0 / 2 (two)
+__host__ __device__ constexpr uint32_t idesc_mx_sf(uint32_t id) { return (id << 4) | (id << 29); }
+
+// arrive on `bar` of this CTA once the thread's earlier tcgen05 work completes: tc_commit (oq_ptx.cuh)
+
+// ------------------------------------------------------------------ tensor maps
+inline oq_status mx_encode(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
+                           const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw, const char* what) {
+  EncodeTiledFn fn = nullptr;
+  const oq_status st = tmap_encode_fn(&fn);
+  if (st != OQ_OK) return st;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, dt, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error(std::string("cuTensorMapEncodeTiled failed for ") + what + " (code " + std::to_string((int)r) + ")");
+    return OQ_ERR_CUDA;
+  }
+  return OQ_OK;
+}
+
+// Code rows in boxes of box_rows x 128 shared-memory bytes (one row of the
+// 128-byte swizzle).  Codes of 8 bits, and 4-bit codes for the 4-bit MMA,
+// travel as bytes; `expand` spreads 4-bit codes to the 8-bit containers of
+// kind::mxf8f6f4 on the way (128 codes a box row).  Rows and columns past the
+// end read as zeros.  The x coordinate is in bytes, or in codes with `expand`;
+// both step by 128.
+inline oq_status mx_encode_codes(CUtensorMap* map, const uint8_t* base, int64_t rows, int K, int bits, bool expand,
+                                 int box_rows, const char* what) {
+  const cuuint64_t row_bytes = (cuuint64_t)mx_row_bytes(K, bits);
+  const cuuint64_t dims[2] = {expand ? 2 * row_bytes : row_bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  return mx_encode(map, expand ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims,
+                   strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+
+// Scale tiles [row tile][column tile][512 bytes] in boxes of row_tiles x
+// col_tiles tiles; tiles past the end read as zeros (scale code 0).
+inline oq_status mx_encode_scales(CUtensorMap* map, const uint8_t* base, int64_t rows, int K, int box_row_tiles,
+                                  int box_col_tiles, const char* what) {
+  const cuuint64_t ct = (cuuint64_t)mx_col_tiles(K);
+  const cuuint64_t dims[3] = {MX_TILE_BYTES / 4, ct, (cuuint64_t)mx_row_tiles(rows)};
+  const cuuint64_t strides[2] = {MX_TILE_BYTES, MX_TILE_BYTES * ct};
+  const cuuint32_t box[3] = {MX_TILE_BYTES / 4, (cuuint32_t)box_col_tiles, (cuuint32_t)box_row_tiles};
+  return mx_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, what);
+}
+
+}  // namespace oq

@@ -1,0 +1,286 @@
+// Product of microscaled operands for small batches (one token to a few
+// hundred): the weights' stream decides the time, so the weight rows are the
+// MMA's M and the batch, padded to BN tokens, its N:
+//   y[t, o] = sum_k w[o, k] a[t, k]
+// A CTA takes 128 weight rows, and the K range is split over the CTAs of a
+// cluster, so that enough CTAs stream weights at once.  Their fp32 partial
+// tiles meet in distributed shared memory and are added in rank order, each
+// CTA for its share of the tokens: no workspace, no atomics, one launch, and
+// the same bits on every call.  4-bit activations use kind::mxf4, 8-bit ones
+// kind::mxf8f6f4 with the weights' codes spread to 8-bit containers by TMA.
+//
+// Warps: 0-3 epilogue, 4 TMA producer, 5 tensor memory and MMAs.
+#include <algorithm>
+#include <cstring>
+
+#include "oq_epilogue.cuh"
+#include "oq_mx_ptx.cuh"
+
+namespace oq {
+namespace {
+
+constexpr int SM_ROWS = 128;                 // weight rows per CTA
+constexpr int W_TILE = SM_ROWS * 128;
+constexpr int TMA_WARP = 4, MMA_WARP = 5, NTHREADS = 6 * 32;
+constexpr int MAX_SPLIT = 8;
+
+template <bool F4, int BN>
+struct Cfg {
+  static constexpr int CT = F4 ? 2 : 1;                       // scale column tiles per stage
+  static constexpr int RT = (BN + MX_ROWS - 1) / MX_ROWS;     // scale row tiles of the batch
+  static constexpr int X_TILE = BN * 128;
+  static constexpr int SX = (RT * CT * MX_TILE_BYTES + 1023) / 1024 * 1024;
+  static constexpr int STAGE = W_TILE + (X_TILE + 1023) / 1024 * 1024 + 1024 + SX;
+  // a load that spreads 4-bit codes counts the packed bytes, half of what it writes
+  static constexpr uint32_t TX = (F4 ? W_TILE : W_TILE / 2) + X_TILE + (1 + RT) * CT * MX_TILE_BYTES;
+  static constexpr int SF_COLS = 2 * CT * 4 * (1 + RT);       // two sets of scale columns
+  static constexpr uint32_t TMEM = BN + SF_COLS <= 32 ? 32 : BN + SF_COLS <= 64 ? 64 : BN + SF_COLS <= 128 ? 128
+                                   : BN + SF_COLS <= 256 ? 256 : 512;
+  // up to 64 tokens two CTAs share an SM
+  static constexpr int BUDGET = BN <= 64 ? 108 * 1024 : 216 * 1024;
+  static constexpr int OS = BUDGET / STAGE < 8 ? BUDGET / STAGE : 8;
+  static constexpr int PART = BN * SM_ROWS * 4;               // fp32 partial tile, over the stages
+  static constexpr size_t SMEM = 1024 + (size_t)(OS * STAGE > PART ? OS * STAGE : PART) + 8 * (2 * OS + 1) + 16;
+};
+
+struct SmallParams {
+  CUtensorMap w_map, x_map, sw_map, sx_map;
+  void* y;
+  bool y_bf16;
+  int64_t T;
+  int N, nkb, split;
+  int* err;
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <bool F4, int BN>
+__global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(const __grid_constant__ SmallParams p) {
+  using C = Cfg<F4, BN>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* op_full = reinterpret_cast<uint64_t*>(smem + (C::OS * C::STAGE > C::PART ? C::OS * C::STAGE : C::PART));
+  uint64_t* op_empty = op_full + C::OS;
+  uint64_t* acc_full = op_empty + C::OS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  float* partial = reinterpret_cast<float*>(smem);   // [BN][128], once every stage has been consumed
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = p.split;
+  const int rank = split > 1 ? (int)cluster_ctarank() : 0;
+  const int n0 = (int)(blockIdx.x / split) * SM_ROWS;
+  const int64_t t0 = (int64_t)blockIdx.y * BN;
+  // this CTA's share of the stages
+  const int kb0 = (int)((int64_t)p.nkb * rank / split), kb1 = (int)((int64_t)p.nkb * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::OS; ++s) {
+      mbar_init(&op_full[s], 1);
+      mbar_init(&op_empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    fence_mbar_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(tmem_slot, C::TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t smem_base = smem_u32(smem);
+
+  if (warp == TMA_WARP) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int s = issued % C::OS;
+        const uint32_t n = (uint32_t)(issued / C::OS);
+        if (n > 0 && !mbar_wait(&op_empty[s], (n - 1) & 1u, p.err)) break;
+        mbar_arrive_expect_tx(&op_full[s], C::TX);
+        unsigned char* st = smem + s * C::STAGE;
+        unsigned char* sw = st + C::STAGE - 1024 - C::SX;
+        tma_load_2d(st, &p.w_map, kb * 128, n0, &op_full[s]);
+        tma_load_2d(st + W_TILE, &p.x_map, kb * 128, (int32_t)t0, &op_full[s]);
+        tma_load_3d(sw, &p.sw_map, 0, kb * C::CT, n0 / MX_ROWS, &op_full[s]);
+        tma_load_3d(sw + 1024, &p.sx_map, 0, kb * C::CT, (int32_t)(t0 / MX_ROWS), &op_full[s]);
+        ++issued;
+      }
+      // no copy may be in flight when the stages are reused or the CTA leaves
+      for (int g = issued > C::OS ? issued - C::OS : 0; g < issued; ++g)
+        mbar_wait(&op_full[g % C::OS], (uint32_t)(g / C::OS) & 1u, p.err);
+    }
+    __syncwarp();
+  } else if (warp == MMA_WARP) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = F4 ? idesc_mx(SM_ROWS, BN, 1, 1) : idesc_mx(SM_ROWS, BN, 5, 0);
+      // the batch's first scale column: its tile begins at a multiple of BN tokens
+      const uint32_t sf_shift = (uint32_t)(t0 % MX_ROWS) / 32;
+      bool ok = true;
+      for (int i = 0; i < kb1 - kb0; ++i) {
+        const int s = i % C::OS;
+        if (!mbar_wait(&op_full[s], (uint32_t)(i / C::OS) & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t st = smem_base + (uint32_t)s * C::STAGE;
+        const uint32_t sc = st + C::STAGE - 1024 - C::SX;
+        const uint32_t sfw = tmem + BN + (uint32_t)(i & 1) * (C::SF_COLS / 2), sfx = sfw + 4 * C::CT;
+#pragma unroll
+        for (int c = 0; c < C::CT; ++c) {
+          tc_copy_scales<1>(sfw + 4 * c, smem_desc_scales(sc + c * MX_TILE_BYTES));
+#pragma unroll
+          for (int r = 0; r < C::RT; ++r)
+            tc_copy_scales<1>(sfx + 4 * (c * C::RT + r),
+                              smem_desc_scales(sc + 1024 + (r * C::CT + c) * MX_TILE_BYTES));
+        }
+        const uint64_t wd = smem_desc_sw128(st), xd = smem_desc_sw128(st + W_TILE);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = F4 ? k / 2 : 0;
+          const uint32_t id = idesc | idesc_mx_sf(F4 ? 2u * (k & 1) : (uint32_t)k);
+          tc_mma_mx<1, F4>(tmem, wd + 2 * k, xd + 2 * k, id, sfw + 4 * c, sfx + 4 * c * C::RT + sf_shift,
+                           i > 0 || k > 0 ? 1u : 0u);
+        }
+        tc_commit(&op_empty[s]);
+      }
+      if (ok) tc_commit(acc_full);
+    }
+    __syncwarp();
+  }
+  __syncthreads();   // the producer's copies have landed: the stages may hold the partial tile
+
+  // the partial tile [token][weight row] in shared memory: a lane writes one
+  // row's value per token, neighbouring lanes neighbouring words
+  if (warp < 4) {
+    const bool ok = kb1 > kb0 && mbar_wait(acc_full, 0u, p.err);
+    tc_fence_after();
+    if constexpr (BN >= 32) {
+#pragma unroll 1
+      for (int cc = 0; cc < BN / 32; ++cc) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(cc * 32), v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          partial[(cc * 32 + j) * SM_ROWS + warp * 32 + lane] = ok ? __uint_as_float(v[j]) : 0.f;
+      }
+    } else {
+      // 16 tokens; the 16 columns read behind them are scales and not used
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(tmem + ((uint32_t)(warp * 32) << 16), v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < BN; ++j) partial[j * SM_ROWS + warp * 32 + lane] = ok ? __uint_as_float(v[j]) : 0.f;
+    }
+  }
+  tc_fence_before();
+  if (split > 1) cluster_sync_all();
+  else __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM);
+  }
+
+  // this CTA's tokens of the tile: sums in rank order
+  const int tokens = (int)(p.T - t0 < BN ? p.T - t0 : BN);
+  const int c0 = tokens * rank / split, c1 = tokens * (rank + 1) / split;
+  uint32_t peer[MAX_SPLIT];
+#pragma unroll
+  for (int r = 0; r < MAX_SPLIT; ++r) peer[r] = split > 1 && r < split ? mapa_shared(smem_base, (uint32_t)r) : smem_base;
+  for (int i = c0 * SM_ROWS + (int)threadIdx.x; i < c1 * SM_ROWS; i += NTHREADS) {
+    float v[MAX_SPLIT];
+#pragma unroll
+    for (int r = 0; r < MAX_SPLIT; ++r) v[r] = r < split ? (split > 1 ? ld_cluster_f32(peer[r] + 4u * i) : partial[i]) : 0.f;
+    float sum = v[0];
+#pragma unroll
+    for (int r = 1; r < MAX_SPLIT; ++r) sum += v[r];
+    const int o = n0 + i % SM_ROWS;
+    if (o < p.N) {
+      const int64_t at = (t0 + i / SM_ROWS) * p.N + o;
+      if (p.y_bf16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(sum);
+      else static_cast<float*>(p.y)[at] = sum;
+    }
+  }
+  if (split > 1) cluster_sync_all();   // no CTA leaves while a peer reads its partial tile
+}
+
+// CTAs that split a weight tile's K range: as many as fill the SMs, each with
+// at least two stages
+int choose_split(int m_tiles, int64_t t_tiles, int nkb, int slots) {
+  int best = 1;
+  for (int s = 2; s <= MAX_SPLIT; s *= 2)
+    if ((int64_t)m_tiles * t_tiles * s <= slots && nkb >= 2 * s) best = s;
+  return best;
+}
+
+template <bool F4, int BN>
+oq_status launch(const MxGemmArgs& g, cudaStream_t stream) {
+  using C = Cfg<F4, BN>;
+  SmallParams kp;
+  std::memset(&kp, 0, sizeof(kp));
+  oq_status st = mx_encode_codes(&kp.w_map, g.w_codes, g.N, g.K, 4, !F4, SM_ROWS, "the weight codes");
+  if (st == OQ_OK) st = mx_encode_codes(&kp.x_map, g.a_codes, g.T, g.K, g.a_bits, false, BN, "the activation codes");
+  if (st == OQ_OK) st = mx_encode_scales(&kp.sw_map, g.w_scales, g.N, g.K, 1, C::CT, "the weight scales");
+  if (st == OQ_OK) st = mx_encode_scales(&kp.sx_map, g.a_scales, g.T, g.K, C::RT, C::CT, "the activation scales");
+  if (st != OQ_OK) return st;
+  kp.y = g.y;
+  kp.y_bf16 = g.y_bf16;
+  kp.T = g.T;
+  kp.N = g.N;
+  kp.nkb = (mx_col_tiles(g.K) + C::CT - 1) / C::CT;
+  kp.err = g.err;
+  const int m_tiles = (g.N + SM_ROWS - 1) / SM_ROWS;
+  const int64_t t_tiles = (g.T + BN - 1) / BN;
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  kp.split = choose_split(m_tiles, t_tiles, kp.nkb, sms * (BN <= 64 ? 2 : 1));
+
+  cudaError_t e = cudaFuncSetAttribute(mx_small_kernel<F4, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(m_tiles * kp.split), (unsigned)t_tiles, 1);
+    cfg.blockDim = dim3(NTHREADS, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)kp.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, mx_small_kernel<F4, BN>, kp);
+  }
+  if (e != cudaSuccess) {
+    set_error(std::string("microscaled small-batch product launch: ") + cudaGetErrorString(e));
+    return OQ_ERR_CUDA;
+  }
+  return OQ_OK;
+}
+
+template <bool F4>
+oq_status launch_bn(const MxGemmArgs& g, cudaStream_t st) {
+  if (g.T <= 16) return launch<F4, 16>(g, st);
+  if (g.T <= 32) return launch<F4, 32>(g, st);
+  if (g.T <= 64) return launch<F4, 64>(g, st);
+  if (g.T <= 128) return launch<F4, 128>(g, st);
+  return launch<F4, 256>(g, st);
+}
+
+}  // namespace
+
+oq_status mx_small_launch(const MxGemmArgs& g, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return g.a_bits == 4 ? launch_bn<true>(g, st) : launch_bn<false>(g, st);
+}
+
+}  // namespace oq

@@ -99,6 +99,7 @@ extern "C" {
 
 oq_status oq_weight_save(const oq_layer* L, const uint32_t* Wcodes, const float* r, const char* path) {
   if (!L || !Wcodes || !r || !path) return fail(OQ_ERR_INVALID_ARG, "oq_weight_save: null argument");
+  if (L->mx) return fail(OQ_ERR_UNSUPPORTED, "oq_weight_save: not available on a microscaled layer");
   const Header h = header_of(L);
   std::vector<float> rh((size_t)L->d_out);
   std::vector<uint32_t> ch((size_t)L->d_out * (size_t)h.words_per_row);
@@ -123,6 +124,7 @@ oq_status oq_weight_save(const oq_layer* L, const uint32_t* Wcodes, const float*
 
 oq_status oq_weight_load(const oq_layer* L, const char* path, uint32_t* Wcodes, float* r) {
   if (!L || !path) return fail(OQ_ERR_INVALID_ARG, "oq_weight_load: null argument");
+  if (L->mx) return fail(OQ_ERR_UNSUPPORTED, "oq_weight_load: not available on a microscaled layer");
   File in;
   in.f = std::fopen(path, "rb");
   if (!in.f) return fail(OQ_ERR_INVALID_ARG, std::string("oq_weight_load: cannot open ") + path);

@@ -1,0 +1,384 @@
+"""GPU tests of the microscaled operators through the Python binding, against
+the plain fp64 reference (mx_reference.py).  Needs a B200.
+
+Bounds.  Quantisation and read-back have one rounding, to the element type,
+and are compared bit for bit.  The norm's fp32 values are off the fp64 ones by
+at most DELTA relative: a thread adds at most 64 squares in turn, then a tree
+of 5 + 4 levels (every rounding 2^-24, all terms positive, so at most 75
+roundings, 73 of them halved by the square root), and the mean, the root, the
+quotient and the two products add at most 7 half-ulps: below 48 * 2^-24, taken
+as 64 * 2^-24.  The product's fp32 sums add one value a 32-element block and
+split; a tensor core may truncate instead of rounding, so each addition is off
+by at most 2^-23 of the magnitudes summed: (K / 32 + 8) 2^-23 sum |a w|, and
+bf16 y adds 2^-8 |y|."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import mx_reference as R
+
+pytestmark = pytest.mark.gpu
+
+DELTA = 64 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from quantized_linear_token_b200 import build
+    build.build()
+    from quantized_linear_token_b200 import binding as B
+    B.load_library()
+    return torch, B
+
+
+def _dtype(torch, name):
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def _rows(rng, rows, d, dtype):
+    """fp32 rows (rounded to bf16 where the input is) with a scale per row, an outlier channel and a zero block."""
+    x = rng.standard_normal((rows, d)) * np.exp(rng.standard_normal((rows, 1)))
+    x[:, rng.integers(d)] *= 30
+    x[rows // 2, :32] = 0
+    x = x.astype(np.float32)
+    return R.bf16(x) if dtype == "bf16" else x
+
+
+def _cuda(torch, x, dtype):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).cuda().to(_dtype(torch, dtype))
+
+
+def _np(t):
+    return t.float().cpu().numpy() if t.dtype.is_floating_point else t.cpu().numpy()
+
+
+# ------------------------------------------------------------------ quantise, read back
+SHAPES = [(1, 32), (3, 160), (64, 256), (127, 128), (128, 96), (129, 288), (300, 2016), (257, 5120)]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,d", SHAPES)
+def test_quantize_and_read_back(env, rows, d, dtype, bits):
+    torch, B = env
+    x = _rows(np.random.default_rng(rows * d + bits), rows, d, dtype)
+    codes, scales = B.oq_mx_quantize(_cuda(torch, x, dtype), bits)
+    want, sc = R.quantize(x.astype(np.float64), bits)
+    c, t = R.pack(want, sc, bits)
+    assert np.array_equal(_np(scales), t)
+    assert np.array_equal(_np(codes), c)
+    v = R.dequantize(want, sc, bits)
+    assert np.array_equal(_np(B.oq_mx_dequantize(codes, scales, d, bits)).astype(np.float64), v)
+    assert np.array_equal(_np(B.oq_mx_dequantize(codes, scales, d, bits, torch.bfloat16)).astype(np.float64), v)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_quantize_ties_extremes_and_non_finite(env, bits):
+    torch, B = env
+    t = R.table(bits)
+    grid = np.concatenate([t, (t[1:] + t[:-1]) / 2])
+    grid = np.concatenate([grid, -grid])
+    rng = np.random.default_rng(5)
+    rows = []
+    for e in (-140, -126, -60, 0, 60, 118):        # blocks on the element grid and on its ties, far scales
+        b = rng.choice(grid, (8, 32)) * 2.0 ** e
+        b[:, 0] = t[-1] * 2.0 ** e
+        rows.append(b.reshape(1, -1))
+    tiny = np.zeros((1, 256))
+    tiny[0, 3], tiny[0, 40], tiny[0, 70] = 2.0 ** -149, -(2.0 ** -126), 3.0e38
+    rows.append(tiny)
+    bad = rng.standard_normal((1, 256))
+    bad[0, 1], bad[0, 45], bad[0, 200] = np.inf, np.nan, -np.inf
+    rows.append(bad)
+    x = np.concatenate(rows).astype(np.float32)
+    codes, scales = B.oq_mx_quantize(_cuda(torch, x, "fp32"), bits)
+    want, sc = R.quantize(x.astype(np.float64), bits)
+    c, tt = R.pack(want, sc, bits)
+    assert np.array_equal(_np(scales), tt)
+    assert np.array_equal(_np(codes), c)
+    v = _np(B.oq_mx_dequantize(codes, scales, 256, bits))
+    np.testing.assert_array_equal(v.astype(np.float64), R.dequantize(want, sc, bits).astype(np.float32))
+    assert np.isnan(v[-1, :64]).all() and np.isnan(v[-1, 192:224]).all() and np.isfinite(v[-1, 64:192]).all()
+
+
+def test_read_back_of_every_code(env):
+    torch, B = env
+    for bits in (4, 8):
+        e = np.tile(np.arange(1 << bits, dtype=np.uint8), 256 >> bits).reshape(1, 256)
+        for s in (0, 1, 100, 127, 200, 246, 255):
+            sc = np.full((1, 8), s, dtype=np.uint8)
+            c, t = R.pack(e, sc, bits)
+            v = _np(B.oq_mx_dequantize(torch.from_numpy(c).cuda(), torch.from_numpy(t).cuda(), 256, bits))
+            np.testing.assert_array_equal(v, R.dequantize(e, sc, bits).astype(np.float32))
+
+
+# ------------------------------------------------------------------ norm
+@pytest.mark.parametrize("rows,d,dtype,bits,residual,gain", [
+    (1, 32, "bf16", 8, True, "fp32"), (5, 96, "fp32", 4, False, None), (130, 160, "bf16", 8, True, "bf16"),
+    (64, 256, "fp32", 8, True, "fp32"), (333, 2016, "bf16", 4, True, "bf16"), (1, 5120, "bf16", 8, True, "fp32"),
+    (100, 5120, "fp32", 8, False, "fp32"), (17, 12288, "bf16", 8, True, None), (9, 13824, "fp32", 8, True, "bf16"),
+    (3, 20032, "bf16", 8, True, "fp32"), (2, 28000, "fp32", 8, True, "fp32"), (2, 40992, "bf16", 8, True, "bf16"),
+    (3, 65504, "fp32", 4, False, "fp32")])
+def test_norm(env, rows, d, dtype, bits, residual, gain):
+    torch, B = env
+    rng = np.random.default_rng(d + rows)
+    x = _rows(rng, rows, d, dtype)
+    r = _rows(rng, rows, d, dtype) if residual else None
+    g = (1 + 0.2 * rng.standard_normal(d)).astype(np.float32) if gain else None
+    if gain == "bf16":
+        g = R.bf16(g)
+    tx = _cuda(torch, x, dtype)
+    tr = _cuda(torch, r, dtype) if residual else None
+    tg = _cuda(torch, g, gain) if gain else None
+    codes, scales, kept = B.oq_rms_norm_mx(tx, tg, tr, eps=1e-6, bits=bits)
+    h, n = R.norm(x.astype(np.float64), None if r is None else r.astype(np.float64),
+                  None if g is None else g.astype(np.float64), 1e-6)
+    e, s = R.unpack(_np(codes), _np(scales), d, bits)
+    off = R.check_quantized(n, e, s, bits, DELTA)
+    assert off <= 10 + 1e-4 * n.size
+    if residual:
+        sums = x + r                       # fp32, as the kernel adds
+        assert np.array_equal(_np(kept), R.bf16(sums) if dtype == "bf16" else sums)
+    else:
+        assert kept is None
+    # what belongs to no row or block holds zeros
+    ref_c, ref_t = R.pack(e, s, bits)
+    assert np.array_equal(_np(codes), ref_c) and np.array_equal(_np(scales), ref_t)
+
+
+def test_norm_degenerate_rows(env):
+    torch, B = env
+    x = np.zeros((4, 160), dtype=np.float32)
+    x[1] = 1e-30
+    x[2, 7] = np.nan
+    x[3, 9] = 5.0
+    codes, scales, _ = B.oq_rms_norm_mx(_cuda(torch, x, "fp32"))
+    v = _np(B.oq_mx_dequantize(codes, scales, 160, 8))
+    assert np.all(v[0] == 0) and np.isfinite(v[1]).all() and np.isnan(v[2]).all()
+    want = 5.0 / np.sqrt(25 / 160 + 1e-6)
+    assert abs(v[3, 9] - want) <= want / 16 and np.all(np.delete(v[3], 9) == 0)
+
+
+@pytest.mark.parametrize("d", [160, 5120, 40992])
+def test_norm_writes_the_residual_in_place(env, d):
+    torch, B = env
+    rng = np.random.default_rng(d)
+    x, r = (_cuda(torch, _rows(rng, 6, d, "bf16"), "bf16") for _ in range(2))
+    want = B.oq_rms_norm_mx(x, residual=r)
+    for which in ("x", "residual"):
+        tx, tr = x.clone(), r.clone()
+        got = B.oq_rms_norm_mx(tx, residual=tr, residual_out=tx if which == "x" else tr)
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ product
+def _operand(rng, rows, d, bits):
+    x = rng.standard_normal((rows, d)) * np.exp(rng.standard_normal((rows, 1)))
+    e, s = R.quantize(R.bf16(x.astype(np.float32)).astype(np.float64), bits)
+    return R.dequantize(e, s, bits), R.pack(e, s, bits)
+
+
+def _product(env, T, d, n, bits, y_dtype, seed=0):
+    torch, B = env
+    rng = np.random.default_rng(seed + T + d + n)
+    a, (ac, at) = _operand(rng, T, d, bits)
+    w, (wc, wt) = _operand(rng, n, d, 4)
+    layer = B.oq_layer_create(d, n, 0, bits, 4, B.OQ_FLAG_MICROSCALED)
+    args = [torch.from_numpy(v).cuda() for v in (ac, at, wc, wt)]
+    y = B.oq_linear_mx(layer, *args, y_dtype=_dtype(torch, y_dtype))
+    torch.cuda.synchronize()
+    B.oq_poll_error(layer)
+    exact = a @ w.T
+    tol = (d / 32 + 8) * 2.0 ** -23 * (np.abs(a) @ np.abs(w).T) + (2.0 ** -8 * np.abs(exact) if y_dtype == "bf16" else 0)
+    err = np.abs(_np(y).astype(np.float64) - exact)
+    assert np.all(err <= tol), f"worst {np.max(err / np.maximum(tol, 1e-300)):.3g} of the bound"
+    # the same call again gives the same bits
+    again = B.oq_linear_mx(layer, *args, y_dtype=_dtype(torch, y_dtype))
+    assert torch.equal(y, again)
+    return layer, args, y
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T,d,n,y", [
+    (1, 32, 16, "fp32"), (1, 256, 128, "fp32"), (1, 2016, 1040, "bf16"), (2, 5120, 272, "fp32"), (16, 128, 144, "bf16"),
+    (17, 288, 256, "fp32"), (33, 1024, 96, "bf16"), (64, 640, 400, "fp32"), (65, 160, 128, "fp32"),
+    (128, 2048, 512, "bf16"), (129, 96, 48, "fp32"), (256, 1056, 640, "bf16")])
+def test_product_small_batches(env, T, d, n, y, bits):
+    _product(env, T, d, n, bits, y)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T,d,n,y", [
+    (257, 32, 16, "fp32"), (257, 256, 192, "fp32"), (300, 160, 208, "bf16"), (384, 2016, 1040, "fp32"),
+    (512, 640, 384, "bf16"), (1001, 1056, 592, "bf16"), (2600, 288, 4624, "fp32")])
+def test_product_large_batches(env, T, d, n, y, bits):
+    _product(env, T, d, n, bits, y)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T", [1, 40, 200, 600])
+def test_product_is_exact_where_fp32_is(env, T, bits):
+    # values in halves, at most 6 (e2m1's grid, which e4m3 holds too), scales 1
+    # and 2: every partial sum is a multiple of 1/4 below 2^22, exact in fp32
+    torch, B = env
+    rng = np.random.default_rng(T)
+    d, n = 1504, 336
+    ops = []
+    for rows, b in ((T, bits), (n, 4)):
+        v = rng.choice(R.E2M1, (rows, d)) * rng.choice([-1.0, 1.0], (rows, d))
+        e = R.round_codes(v, b)
+        s = rng.integers(127, 129, (rows, d // 32)).astype(np.uint8)
+        ops.append((R.dequantize(e, s, b), R.pack(e, s, b)))
+    layer = B.oq_layer_create(d, n, 0, bits, 4, B.OQ_FLAG_MICROSCALED)
+    (a, (ac, at)), (w, (wc, wt)) = ops
+    y = B.oq_linear_mx(layer, *[torch.from_numpy(v).cuda() for v in (ac, at, wc, wt)])
+    assert np.array_equal(_np(y).astype(np.float64), a @ w.T)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T", [40, 300])
+def test_product_of_nan_blocks(env, T, bits):
+    torch, B = env
+    layer, (ac, at, wc, wt), y = _product(env, T, 416, 160, bits, "fp32")
+    at, wt = at.clone(), wt.clone()
+    at[0, 1, 7, 0, 2] = 255          # row 7, block 6
+    wt[0, 0, 3, 1, 0] = 255          # weight row 35, block 0
+    z = _np(B.oq_linear_mx(layer, ac, at, wc, wt))
+    want = _np(y).copy()
+    want[7, :] = np.nan
+    want[:, 35] = np.nan
+    np.testing.assert_array_equal(z, want)
+
+
+def test_product_leaves_what_is_not_its_own(env):
+    torch, B = env
+    for T in (5, 300):
+        layer, args, y = _product(env, T, 288, 144, 8, "bf16")
+        buf = torch.full((T + 4, 144), 7.0, dtype=torch.bfloat16, device="cuda")
+        B.oq_linear_mx(layer, *args, y=buf[2:T + 2])
+        assert torch.equal(buf[2:T + 2], y)
+        assert (buf[:2] == 7).all() and (buf[T + 2:] == 7).all()
+
+
+# ------------------------------------------------------------------ together, streams, graphs, refusals
+@pytest.mark.parametrize("T,d,n", [(1, 2016, 1040), (333, 2016, 1040), (70, 5120, 256)])
+def test_block_input_chain(env, T, d, n):
+    # residual, norm, 8-bit codes, projection: as a block's input runs
+    torch, B = env
+    rng = np.random.default_rng(T)
+    x, r = _rows(rng, T, d, "bf16"), _rows(rng, T, d, "bf16")
+    g = (1 + 0.1 * rng.standard_normal(d)).astype(np.float32)
+    w = (0.02 * rng.standard_normal((n, d))).astype(np.float32)
+    layer = B.oq_layer_create(d, n, 0, 8, 4, B.OQ_FLAG_MICROSCALED)
+    wc, wt = B.oq_mx_quantize(_cuda(torch, w, "fp32"), 4)
+    codes, scales, kept = B.oq_rms_norm_mx(_cuda(torch, x, "bf16"), _cuda(torch, g, "fp32"), _cuda(torch, r, "bf16"))
+    y = _np(B.oq_linear_mx(layer, codes, scales, wc, wt))
+    B.oq_poll_error(layer)
+    a = R.dequantize(*R.unpack(_np(codes), _np(scales), d, 8), 8)
+    wq = R.dequantize(*R.quantize(w.astype(np.float64), 4), 4)
+    R.check_quantized(R.norm(x.astype(np.float64), r.astype(np.float64), g.astype(np.float64), 1e-6)[1],
+                      *R.unpack(_np(codes), _np(scales), d, 8), 8, DELTA)
+    assert np.all(np.abs(y - a @ wq.T) <= (d / 32 + 8) * 2.0 ** -23 * (np.abs(a) @ np.abs(wq).T))
+    assert np.array_equal(_np(kept), R.bf16(x + r))
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_graph_replay_and_other_stream(env, T):
+    torch, B = env
+    d, n = 672, 208
+    layer = B.oq_layer_create(d, n, 0, 8, 4, B.OQ_FLAG_MICROSCALED)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x, r = (torch.randn(T, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    wc, wt = B.oq_mx_quantize(torch.randn(n, d, generator=gen, device="cuda"), 4)
+
+    def step():
+        codes, scales, kept = B.oq_rms_norm_mx(x, residual=r)
+        return B.oq_linear_mx(layer, codes, scales, wc, wt), kept
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    x.mul_(2)
+    graph.replay()
+    want = step()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    torch.cuda.synchronize()
+    B.oq_poll_error(layer)
+
+
+@pytest.mark.parametrize("T", [30, 300])
+def test_two_calls_at_once_on_one_layer(env, T):
+    torch, B = env
+    layer, args, y = _product(env, T, 2016, 400, 4, "fp32")
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = []
+    for k in range(12):
+        with torch.cuda.stream(streams[k % 4]):
+            outs.append(B.oq_linear_mx(layer, *args))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, y) for o in outs)
+
+
+def test_empty_batch(env):
+    torch, B = env
+    x = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
+    codes, scales = B.oq_mx_quantize(x, 4)
+    assert tuple(codes.shape) == (0, 64) and tuple(scales.shape) == (0, 1, 32, 4, 4)
+    assert tuple(B.oq_mx_dequantize(codes, scales, 64, 4).shape) == (0, 64)
+    layer = B.oq_layer_create(64, 32, 0, 4, 4, B.OQ_FLAG_MICROSCALED)
+    wc, wt = B.oq_mx_quantize(torch.zeros(32, 64, device="cuda"), 4)
+    assert tuple(B.oq_linear_mx(layer, codes, scales, wc, wt).shape) == (0, 32)
+    assert B.oq_rms_norm_mx(x, residual=x)[2].shape == x.shape
+
+
+def test_refusals_on_a_microscaled_layer(env):
+    torch, B = env
+    layer = B.oq_layer_create(256, 256, 0, 4, 4, B.OQ_FLAG_MICROSCALED)
+    x = torch.zeros(4, 256, device="cuda")
+    for call in (lambda: B.oq_rotate_quantize(layer, x), lambda: B.oq_weight_prepare(layer, torch.zeros(256, 256, device="cuda")),
+                 lambda: B.oq_rotate_quantize_levels(layer, x.bfloat16()), lambda: layer.perm(),
+                 lambda: B.oq_linear_fused(layer, x, torch.zeros(256, 32, dtype=torch.int32, device="cuda"), x[0])):
+        with pytest.raises(B.OrbitQuantError) as e:
+            call()
+        assert e.value.status == 2
+    assert B.oq_linear_fused_workspace_size(layer, 10) == 0
+    assert B.oq_linear_fused_decoded_workspace_size(layer, 10) == 0
+    assert B.oq_linear_fused_host_workspace_size(layer, 1, 10) == 0
+    # and the microscaled product on another kind of layer
+    plain = B.oq_layer_create(256, 256, 0, 4, 4)
+    codes, scales = B.oq_mx_quantize(x, 4)
+    wc, wt = B.oq_mx_quantize(torch.zeros(256, 256, device="cuda"), 4)
+    with pytest.raises(ValueError):
+        B.oq_linear_mx(plain, codes, scales, wc, wt)
+    L = B.load_library()
+    p = [ctypes.c_void_p(t.data_ptr()) for t in (codes, scales, wc, wt, x)]
+    assert L.oq_linear_mx(plain.handle, p[0], p[1], 4, p[2], p[3], p[4], 0, None) == 2
+    assert L.oq_linear_mx(layer.handle, p[0], p[1], 4, p[2], p[3], None, 0, None) == 1
+    assert L.oq_linear_mx(layer.handle, p[0], None, 4, p[2], p[3], p[4], 0, None) == 1
+    assert L.oq_linear_mx(layer.handle, p[0], p[1], 4, p[2], p[3], p[4], 5, None) == 1
+    # wrong shapes and types
+    for bad in ((codes[:, :64], scales, wc, wt), (codes, scales[:, :1], wc, wt), (codes, scales, wc[:128], wt),
+                (codes.int(), scales, wc, wt)):
+        with pytest.raises(ValueError):
+            B.oq_linear_mx(layer, *bad)
+    with pytest.raises(ValueError):
+        B.oq_mx_quantize(x.t(), 4)
+    with pytest.raises(ValueError):
+        B.oq_rms_norm_mx(x, residual=x.bfloat16())
+    with pytest.raises(ValueError):
+        B.oq_rms_norm_mx(x, torch.ones(128, device="cuda"))
+    with pytest.raises(TypeError):
+        B.oq_mx_quantize(x.half(), 4)
