@@ -55,6 +55,13 @@ __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
+// one lane of a converged warp
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+
 // Block-scaled MMA, K of 32 bytes per row: F4 multiplies 64 e2m1 by 64 e2m1
 // with two scales a row, otherwise 32 elements of 8-bit containers (e4m3, or
 // e2m1 in the low half of each 16-byte group's padding layout) with one.
@@ -84,7 +91,92 @@ __host__ __device__ constexpr uint32_t idesc_mx(int M, int N, uint32_t a_fmt, ui
 // the scale's place in its 32-bit column: byte 0..3 (one scale per MMA), or 0 / 2 (two)
 __host__ __device__ constexpr uint32_t idesc_mx_sf(uint32_t id) { return (id << 4) | (id << 29); }
 
-// arrive on `bar` of this CTA once the thread's earlier tcgen05 work completes: tc_commit (oq_ptx.cuh)
+// Arrival on a barrier of the cluster that hands over tensor memory only: the
+// caller's tcgen05 loads are complete and fenced (before_thread_sync), and no
+// ordinary memory goes with it, so the default scope does; a release at cluster
+// scope would wait some 1000 cycles for the thread's stores.
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Which of the phases `parity` (bit j) of the barriers bar[slot[j]] have
+// completed: three non-blocking checks whose latencies overlap.  Bit j is only
+// asked for where `want` has it.
+__device__ __forceinline__ uint32_t mbar_test3(uint32_t b0, uint32_t b1, uint32_t b2, uint32_t parity,
+                                                       uint32_t want) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p0, p1, p2, q0, q1, q2;\n\t.reg .b32 t0, t1, t2, u;\n\t"
+      "and.b32 u, %5, 1;\n\tsetp.ne.b32 q0, u, 0;\n\tand.b32 u, %5, 2;\n\tsetp.ne.b32 q1, u, 0;\n\t"
+      "and.b32 u, %5, 4;\n\tsetp.ne.b32 q2, u, 0;\n\t"
+      "and.b32 t0, %4, 1;\n\tshr.u32 t1, %4, 1;\n\tand.b32 t1, t1, 1;\n\tshr.u32 t2, %4, 2;\n\tand.b32 t2, t2, 1;\n\t"
+      "setp.ne.b32 p0, 0, 0;\n\tsetp.ne.b32 p1, 0, 0;\n\tsetp.ne.b32 p2, 0, 0;\n\t"
+      "@q0 mbarrier.test_wait.parity.shared::cta.b64 p0, [%1], t0;\n\t"
+      "@q1 mbarrier.test_wait.parity.shared::cta.b64 p1, [%2], t1;\n\t"
+      "@q2 mbarrier.test_wait.parity.shared::cta.b64 p2, [%3], t2;\n\t"
+      "selp.u32 t0, 1, 0, p0;\n\tselp.u32 t1, 2, 0, p1;\n\tselp.u32 t2, 4, 0, p2;\n\t"
+      "or.b32 t0, t0, t1;\n\tor.b32 %0, t0, t2;\n\t}"
+      : "=r"(r)
+      : "r"(b0), "r"(b1), "r"(b2), "r"(parity), "r"(want)
+      : "memory");
+  return r;
+}
+
+// Half a stage of a CTA pair: four MMAs (two K steps of the tile's two column
+// parts) with the scale copies of the NEXT half between them, so that no MMA
+// waits for a copy just issued.  `commit` reports everything issued so far to
+// `commit_bar` in both CTAs.
+//   a, b0, b1     low descriptor words of the operand tiles at the first K step (+2: the second)
+//   i0a .. i1b    instruction descriptors of part 0 / 1 at the two K steps
+//   sf, w0, w1    scale columns of A and of the two parts' weight rows
+//   sf_next       columns of the copies: 4 of A, then 4 of each of RT weight row tiles
+//   ca, cw        low descriptor words of their shared-memory tiles (weights' row tiles STRIDE apart)
+struct MxHalf {
+  uint32_t lead;   // this lane issues
+  uint32_t d0, d1, a, b0, b1, hi, i0a, i0b, i1a, i1b, sf, w0, w1, accumulate;
+  uint32_t sf_next, ca, cw, c_hi, copy;
+  uint64_t* commit_bar;
+  uint32_t commit;
+};
+template <bool F4, int RT, int STRIDE>
+__device__ __forceinline__ void tc_half_stage_pair(const MxHalf& h) {
+#define OQ_DESC(R, LO, OFF, HI) "add.u32 lo, " LO ", " OFF ";\n\tmov.b64 " R ", {lo, " HI "};\n\t"
+#define OQ_MMA(KIND, VEC, D, ID, W, P)                                                                      \
+  "@pl tcgen05.mma.cta_group::2.kind::" KIND ".block_scale.scale_vec::" VEC " [" D "], da, db, " ID ", [%11], [" W "], " P \
+  ";\n\t"
+#define OQ_CP(P, COL, LO, OFF)                                                                              \
+  "add.u32 t, %15, " COL ";\n\t" OQ_DESC("ds", LO, OFF, "%18")                                              \
+  "@" P " tcgen05.cp.cta_group::2.32x128b.warpx4 [t], ds;\n\t"
+#define OQ_HALF(KIND, VEC)                                                                                  \
+  "{\n\t.reg .pred pl, pa, pt, pc, c0, c1, c2, c3, c4;\n\t.reg .b64 da, db, ds;\n\t.reg .b32 lo, t;\n\t"    \
+  "setp.ne.b32 pl, %0, 0;\n\tsetp.ne.b32 pa, %14, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"                                  \
+  "setp.ne.and.b32 pc, %21, 0, pl;\n\tsetp.ne.and.b32 c0, %19, 0, pl;\n\tsetp.gt.and.s32 c1, %23, 0, c0;\n\t"                \
+  "setp.gt.and.s32 c2, %23, 1, c0;\n\tsetp.gt.and.s32 c3, %23, 2, c0;\n\tsetp.gt.and.s32 c4, %23, 3, c0;\n\t" \
+  OQ_DESC("da", "%3", "0", "%6") OQ_DESC("db", "%4", "0", "%6") OQ_MMA(KIND, VEC, "%1", "%7", "%12", "pa")  \
+  OQ_CP("c0", "0", "%16", "0")                                                                              \
+  OQ_DESC("da", "%3", "2", "%6") OQ_DESC("db", "%4", "2", "%6") OQ_MMA(KIND, VEC, "%1", "%8", "%12", "pt")  \
+  OQ_CP("c1", "4", "%17", "0") OQ_CP("c2", "8", "%17", "%24")                                               \
+  OQ_DESC("da", "%3", "0", "%6") OQ_DESC("db", "%5", "0", "%6") OQ_MMA(KIND, VEC, "%2", "%9", "%13", "pa")  \
+  OQ_CP("c3", "12", "%17", "%25") OQ_CP("c4", "16", "%17", "%26")                                           \
+  OQ_DESC("da", "%3", "2", "%6") OQ_DESC("db", "%5", "2", "%6") OQ_MMA(KIND, VEC, "%2", "%10", "%13", "pt") \
+  "@pc tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%20], %22;\n\t" \
+  "}"
+#define OQ_ARGS                                                                                             \
+  :                                                                                                         \
+  : "r"(h.lead), "r"(h.d0), "r"(h.d1), "r"(h.a), "r"(h.b0), "r"(h.b1), "r"(h.hi), "r"(h.i0a), "r"(h.i0b), "r"(h.i1a),     \
+    "r"(h.i1b), "r"(h.sf), "r"(h.w0), "r"(h.w1), "r"(h.accumulate), "r"(h.sf_next), "r"(h.ca), "r"(h.cw),    \
+    "r"(h.c_hi), "r"(h.copy), "r"(smem_u32(h.commit_bar)), "r"(h.commit),                                    \
+    "h"((uint16_t)0x3), "n"(RT), "n"(STRIDE), "n"(2 * STRIDE),            \
+    "n"(3 * STRIDE)                                                                                         \
+  : "memory"
+  if constexpr (F4) asm volatile(OQ_HALF("mxf4", "2X") OQ_ARGS);
+  else asm volatile(OQ_HALF("mxf8f6f4", "1X") OQ_ARGS);
+#undef OQ_ARGS
+#undef OQ_HALF
+#undef OQ_CP
+#undef OQ_MMA
+#undef OQ_DESC
+}
 
 // ------------------------------------------------------------------ tensor maps
 inline oq_status mx_encode(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
