@@ -8,7 +8,6 @@ if the library is missing or no GPU is present the calls raise.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -188,9 +187,15 @@ def oq_layer_create(d_in: int, d_out: int, seed: int, a_bits: int, w_bits: int, 
 
 
 # ------------------------------------------------------------------ device calls
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(t):
@@ -432,47 +437,99 @@ def oq_mx_scales_size(rows: int, d: int) -> int:
     return int(load_library().oq_mx_scales_size(rows, d))
 
 
-def _on_device(device):
-    """A context in which `device` is the current one (the C calls work on the current device)."""
+_raw = None   # (current device, raw current stream of a device, uint8, dtype codes), on first use
+
+
+def _raw_calls():
+    global _raw
     torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    _raw = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, torch.uint8,
+            {torch.float32: OQ_DTYPE_F32, torch.bfloat16: OQ_DTYPE_BF16})
+    return _raw
 
 
-def _mx_arrays(codes, scales, rows: int, d: int, bits: int, device, name: str):
-    """Codes [rows, row bytes] and scale tiles [row tiles, column tiles, 32, 4, 4]
-    of a [rows, d] operand: new ones, or the given ones checked."""
-    torch = _torch()
-    ct = (d + 127) // 128
-    for t, shape, what in ((codes, (rows, ct * 16 * bits), "codes"), (scales, ((rows + 127) // 128, ct, 32, 4, 4), "scales")):
-        if t is not None and (t.dtype != torch.uint8 or tuple(t.shape) != shape or t.device != device):
-            raise ValueError(f"{name}{what} must be uint8 {list(shape)} on {device}")
-    if codes is None:
-        codes = torch.empty((rows, ct * 16 * bits), dtype=torch.uint8, device=device)
-    if scales is None:
-        scales = torch.empty(((rows + 127) // 128, ct, 32, 4, 4), dtype=torch.uint8, device=device)
-    return codes, scales
+def _launch(name: str, device, *args):
+    """Call an entry point with `device` current and its current stream as the
+    last argument.  Small calls are bound by the host, so this and the checks
+    below spend as little as they can."""
+    get_device, get_stream, _, _ = _raw or _raw_calls()
+    fn = getattr(_lib or load_library(), name)
+    i = device.index
+    if get_device() == i:
+        status = fn(*args, get_stream(i))
+    else:
+        with _torch().cuda.device(device):
+            status = fn(*args, get_stream(i))
+    if status:
+        _check(status, name)
 
 
-def _mx_shape(t, name: str, bits: int):
-    if t.dim() != 2:
+def _mx_ptr(t, shape, device, name: str) -> int:
+    """The address of a contiguous uint8 tensor of this shape on `device`."""
+    if t.dtype is not (_raw or _raw_calls())[2] or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous uint8 {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _mx_dtype(t) -> int:
+    code = (_raw or _raw_calls())[3].get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}: use bfloat16 or float32")
+    return code
+
+
+def _mx_input(x, name: str, bits: int) -> int:
+    """The address of a [rows, d] operand to quantize."""
+    if x.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
-    if bits not in (4, 8) or t.shape[1] == 0 or t.shape[1] % 32:
+    d = x.shape[1]
+    if (bits != 4 and bits != 8) or d == 0 or d % 32:
         raise ValueError(f"bits must be 4 or 8 and {name}'s width a positive multiple of 32")
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return x.data_ptr()
+
+
+def _mx_shapes(rows: int, d: int, bits: int):
+    """Shapes of the codes and the scale tiles of a [rows, d] operand."""
+    ct = (d + 127) // 128
+    return (rows, ct * 16 * bits), ((rows + 127) // 128, ct, 32, 4, 4)
+
+
+def _mx_outputs(codes, scales, rows: int, d: int, bits: int, device):
+    """Codes and scales to write: new ones, or the given ones checked; and their addresses."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError("the operands must be CUDA tensors")
+    cs, ss = _mx_shapes(rows, d, bits)
+    if codes is None:
+        codes = torch.empty(cs, dtype=torch.uint8, device=device)
+        pc = codes.data_ptr()
+    else:
+        pc = _mx_ptr(codes, cs, device, "codes")
+    if scales is None:
+        scales = torch.empty(ss, dtype=torch.uint8, device=device)
+        ps = scales.data_ptr()
+    else:
+        ps = _mx_ptr(scales, ss, device, "scales")
+    return codes, scales, pc, ps
+
+
+def _mx_rows(t, shape, dtype, device, name: str) -> int:
+    """The address of a contiguous tensor of this shape, type and device."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}")
+    return t.data_ptr()
 
 
 def oq_mx_quantize(x, bits: int, codes=None, scales=None):
     """x [rows, d] (bf16/fp32, CUDA) -> (codes [rows, row bytes] uint8, scales
     [row tiles, column tiles, 32, 4, 4] uint8): microscaled e2m1 (bits = 4) or
     e4m3 (bits = 8) elements, one E8M0 scale per 32 (include/orbitquant.h)."""
-    _mx_shape(x, "x", bits)
+    px, dt, device = _mx_input(x, "x", bits), _mx_dtype(x), x.device
     rows, d = x.shape
-    px, dt = _dev(x, "x"), _dtype_code(x)
-    codes, scales = _mx_arrays(codes, scales, rows, d, bits, x.device, "")
-    with _on_device(x.device):
-        _check(load_library().oq_mx_quantize(px, dt, rows, d, bits, _dev(codes, "codes"), _dev(scales, "scales"),
-                                             _stream(x)), "oq_mx_quantize")
+    codes, scales, pc, ps = _mx_outputs(codes, scales, rows, d, bits, device)
+    _launch("oq_mx_quantize", device, px, dt, rows, d, bits, pc, ps)
     return codes, scales
 
 
@@ -482,15 +539,14 @@ def oq_mx_dequantize(codes, scales, d: int, bits: int, dtype=None, x=None):
     torch = _torch()
     if codes.dim() != 2 or bits not in (4, 8) or d <= 0 or d % 32:
         raise ValueError("codes must be a matrix, bits 4 or 8 and d a positive multiple of 32")
-    rows = codes.shape[0]
-    codes, scales = _mx_arrays(codes, scales, rows, d, bits, codes.device, "")
+    rows, device = codes.shape[0], codes.device
+    _, _, pc, ps = _mx_outputs(codes, scales, rows, d, bits, device)
     if x is None:
-        x = torch.empty((rows, d), dtype=torch.float32 if dtype is None else dtype, device=codes.device)
-    elif tuple(x.shape) != (rows, d) or x.device != codes.device or (dtype is not None and x.dtype != dtype):
-        raise ValueError(f"x must be [{rows}, {d}] on {codes.device}")
-    with _on_device(codes.device):
-        _check(load_library().oq_mx_dequantize(_dev(codes, "codes"), _dev(scales, "scales"), rows, d, bits,
-                                               _dev(x, "x"), _dtype_code(x), _stream(codes)), "oq_mx_dequantize")
+        x = torch.empty((rows, d), dtype=torch.float32 if dtype is None else dtype, device=device)
+        px = x.data_ptr()
+    else:
+        px = _mx_rows(x, (rows, d), x.dtype if dtype is None else dtype, device, "x")
+    _launch("oq_mx_dequantize", device, pc, ps, rows, d, bits, px, _mx_dtype(x))
     return x
 
 
@@ -501,25 +557,24 @@ def oq_rms_norm_mx(x, gain=None, residual=None, eps: float = 1e-6, bits: int = 8
     to x's type, or None without a residual).  residual_out may be x or
     residual itself."""
     torch = _torch()
-    _mx_shape(x, "x", bits)
-    rows, d = x.shape
-    px, dt = _dev(x, "x"), _dtype_code(x)
-    if gain is not None and (tuple(gain.shape) != (d,) or gain.device != x.device):
-        raise ValueError(f"gain must be [{d}] on {x.device}")
-    if residual is None and residual_out is not None:
+    px, dt = _mx_input(x, "x", bits), _mx_dtype(x)
+    rows, d = shape = x.shape
+    dtype, device = x.dtype, x.device
+    pr = po = pg = None
+    gdt = OQ_DTYPE_F32
+    if residual is not None:
+        pr = _mx_rows(residual, shape, dtype, device, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+            po = residual_out.data_ptr()
+        else:
+            po = _mx_rows(residual_out, shape, dtype, device, "residual_out")
+    elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
-    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != x.device):
-            raise ValueError(f"{name} must have x's shape, type and device")
-    codes, scales = _mx_arrays(codes, scales, rows, d, bits, x.device, "")
-    with _on_device(x.device):
-        _check(load_library().oq_rms_norm_mx(
-            px, None if residual is None else _dev(residual, "residual"), dt,
-            None if gain is None else _dev(gain, "gain"), OQ_DTYPE_F32 if gain is None else _dtype_code(gain), eps,
-            rows, d, bits, None if residual_out is None else _dev(residual_out, "residual_out"),
-            _dev(codes, "codes"), _dev(scales, "scales"), _stream(x)), "oq_rms_norm_mx")
+    if gain is not None:
+        gdt, pg = _mx_dtype(gain), _mx_rows(gain, (d,), gain.dtype, device, "gain")
+    codes, scales, pc, ps = _mx_outputs(codes, scales, rows, d, bits, device)
+    _launch("oq_rms_norm_mx", device, px, pr, dt, pg, gdt, eps, rows, d, bits, po, pc, ps)
     return codes, scales, residual_out
 
 
@@ -529,18 +584,20 @@ def oq_linear_mx(layer: Layer, codes, scales, Wcodes, Wscales, y=None, y_dtype=N
     OQ_FLAG_MICROSCALED."""
     if not layer.flags & OQ_FLAG_MICROSCALED:
         raise ValueError("the layer was not created with OQ_FLAG_MICROSCALED")
-    if codes.dim() != 2:
-        raise ValueError("codes must be a matrix")
-    T, device = codes.shape[0], codes.device
-    _mx_arrays(codes, scales, T, layer.d_in, layer.a_bits, device, "")
-    _mx_arrays(Wcodes, Wscales, layer.d_out, layer.d_in, 4, device, "W")
-    y, ycode = _y_out(y, T, layer.d_out, y_dtype, device)
-    if tuple(y.shape) != (T, layer.d_out) or y.device != device:
-        raise ValueError(f"y must be [{T}, {layer.d_out}] on {device}")
-    with _on_device(device):
-        _check(load_library().oq_linear_mx(layer.handle, _dev(codes, "codes"), _dev(scales, "scales"), T,
-                                           _dev(Wcodes, "Wcodes"), _dev(Wscales, "Wscales"), _dev(y, "y"), ycode,
-                                           _stream(codes)), "oq_linear_mx")
+    if codes.dim() != 2 or not codes.is_cuda:
+        raise ValueError("codes must be a CUDA matrix")
+    T, device, n = codes.shape[0], codes.device, layer.d_out
+    cs, ss = _mx_shapes(T, layer.d_in, layer.a_bits)
+    ws, wt = _mx_shapes(n, layer.d_in, 4)
+    pointers = (_mx_ptr(codes, cs, device, "codes"), _mx_ptr(scales, ss, device, "scales"), T,
+                _mx_ptr(Wcodes, ws, device, "Wcodes"), _mx_ptr(Wscales, wt, device, "Wscales"))
+    if y is None:
+        y = _torch().empty((T, n), dtype=_torch().float32 if y_dtype is None else y_dtype, device=device)
+        py = y.data_ptr()
+    else:
+        py = _mx_rows(y, (T, n), y.dtype, device, "y")
+    ycode = _mx_dtype(y)
+    _launch("oq_linear_mx", device, layer.handle, *pointers, py, ycode)
     return y
 
 

@@ -9,6 +9,7 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "oq_internal.h"
@@ -133,6 +134,12 @@ __device__ __forceinline__ uint32_t mx_scale_word(uint32_t code) {
   for (int b = 0; b < 4; ++b) w |= __shfl_sync(0xFFFFFFFFu, code, base + 4 * b) << (8 * b);
   return w;
 }
+
+// Multiprocessors of the current device, asked for once per device, and the
+// opt-in to a kernel's shared memory, once per kernel and device (`done`: a bit
+// per device): both cost a small call as much as its other host work.
+int mx_sm_count(int* device);
+oq_status mx_allow_smem(const void* kernel, size_t bytes, int device, std::atomic<uint64_t>* done);
 
 // launches (oq_mx_quant.cu, oq_mx_gemm.cu, oq_mx_small.cu); arguments checked by the entry points
 oq_status mx_quantize_launch(const void* x, int x_dtype, int64_t rows, int d, int bits, uint8_t* codes,

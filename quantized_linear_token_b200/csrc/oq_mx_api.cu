@@ -46,6 +46,27 @@ oq_status unsupported(oq_status st, const char* who) {
 
 }  // namespace
 
+int mx_sm_count(int* device) {
+  static std::atomic<int> known[64];
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  *device = dev;
+  if (dev >= 0 && dev < 64 && (sms = known[dev].load(std::memory_order_relaxed))) return sms;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
+oq_status mx_allow_smem(const void* kernel, size_t bytes, int device, std::atomic<uint64_t>* done) {
+  const uint64_t bit = device >= 0 && device < 64 ? (uint64_t)1 << device : 0;
+  if (done->load(std::memory_order_relaxed) & bit) return OQ_OK;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess)
+    return fail(OQ_ERR_CUDA, std::string("cudaFuncSetAttribute(microscaled product): ") + cudaGetErrorString(e));
+  done->fetch_or(bit, std::memory_order_relaxed);
+  return OQ_OK;
+}
+
 oq_status create_mx_layer(int32_t d_in, int32_t d_out, uint64_t seed, int32_t a_bits, int32_t w_bits, int32_t flags,
                           oq_layer** out) {
   if (flags != OQ_FLAG_MICROSCALED) return fail(OQ_ERR_INVALID_ARG, "OQ_FLAG_MICROSCALED takes no other flag");

@@ -372,15 +372,8 @@ oq_status encode_y(CUtensorMap* map, void* y, int64_t M, int N, bool bf16) {
                    box, CU_TENSOR_MAP_SWIZZLE_64B, "y");
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 template <bool F4, int N0, int N1>
-oq_status launch(const MxGemmArgs& g, int sms, cudaStream_t stream) {
+oq_status launch(const MxGemmArgs& g, int sms, int device, cudaStream_t stream) {
   using C = Cfg<F4, N0, N1>;
   MxParams kp;
   std::memset(&kp, 0, sizeof(kp));
@@ -398,17 +391,14 @@ oq_status launch(const MxGemmArgs& g, int sms, cudaStream_t stream) {
   if (st == OQ_OK) st = encode_y(&kp.y_map, g.y, g.T, g.N, g.y_bf16);
   if (st != OQ_OK) return st;
 
-  cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<F4, N0, N1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::SMEM);
-  if (e != cudaSuccess) {
-    set_error(std::string("cudaFuncSetAttribute(microscaled product): ") + cudaGetErrorString(e));
-    return OQ_ERR_CUDA;
-  }
+  static std::atomic<uint64_t> smem_set{0};
+  if ((st = mx_allow_smem(reinterpret_cast<const void*>(mx_gemm_kernel<F4, N0, N1>), C::SMEM, device, &smem_set)) != OQ_OK)
+    return st;
   const int64_t grid = std::min<int64_t>(2 * kp.tiles, (int64_t)(sms & ~1));
   // stage counters are 32-bit
   if (((kp.tiles + grid / 2 - 1) / (grid / 2)) * (int64_t)kp.nkb >= (int64_t)1 << 31) return OQ_ERR_UNSUPPORTED;
   mx_gemm_kernel<F4, N0, N1><<<(unsigned)grid, NTHREADS, C::SMEM, stream>>>(kp);
-  e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error(std::string("microscaled product launch: ") + cudaGetErrorString(e));
     return OQ_ERR_CUDA;
@@ -421,7 +411,8 @@ oq_status launch(const MxGemmArgs& g, int sms, cudaStream_t stream) {
 // MMAs of every width take less or as much).
 template <bool F4>
 oq_status launch_width(const MxGemmArgs& g, cudaStream_t st) {
-  const int sms = sm_count();
+  int device = 0;
+  const int sms = mx_sm_count(&device);
   const int64_t m_tiles = (g.T + 2 * RM - 1) / (2 * RM), pairs = sms / 2;
   int best = 0;
   int64_t cost = 0;
@@ -434,11 +425,11 @@ oq_status launch_width(const MxGemmArgs& g, cudaStream_t st) {
     }
   }
   switch (best) {
-    case 448: return launch<F4, 256, 192>(g, sms, st);
-    case 320: return launch<F4, 192, 128>(g, sms, st);
-    case 256: return launch<F4, 128, 128>(g, sms, st);
-    case 192: return launch<F4, 128, 64>(g, sms, st);
-    default: return launch<F4, 64, 64>(g, sms, st);
+    case 448: return launch<F4, 256, 192>(g, sms, device, st);
+    case 320: return launch<F4, 192, 128>(g, sms, device, st);
+    case 256: return launch<F4, 128, 128>(g, sms, device, st);
+    case 192: return launch<F4, 128, 64>(g, sms, device, st);
+    default: return launch<F4, 64, 64>(g, sms, device, st);
   }
 }
 

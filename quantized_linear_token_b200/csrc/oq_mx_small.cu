@@ -39,6 +39,7 @@ struct Cfg {
   // up to 64 tokens two CTAs share an SM
   static constexpr int BUDGET = BN <= 64 ? 108 * 1024 : 216 * 1024;
   static constexpr int OS = BUDGET / STAGE < 8 ? BUDGET / STAGE : 8;
+  static_assert(OS >= 3, "the checks cover three stages");
   static constexpr int PART = BN * SM_ROWS * 4;               // fp32 partial tile, over the stages
   static constexpr size_t SMEM = 1024 + (size_t)(OS * STAGE > PART ? OS * STAGE : PART) + 8 * (2 * OS + 1) + 16;
 };
@@ -52,9 +53,12 @@ struct SmallParams {
   int* err;
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -70,7 +74,7 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
   float* partial = reinterpret_cast<float*>(smem);   // [BN][128], once every stage has been consumed
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int split = p.split;
   const int rank = split > 1 ? (int)cluster_ctarank() : 0;
   const int n0 = (int)(blockIdx.x / split) * SM_ROWS;
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp == TMA_WARP) {
@@ -118,41 +122,65 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
     }
     __syncwarp();
   } else if (warp == MMA_WARP) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = F4 ? idesc_mx(SM_ROWS, BN, 1, 1) : idesc_mx(SM_ROWS, BN, 5, 0);
-      // the batch's first scale column: its tile begins at a multiple of BN tokens
-      const uint32_t sf_shift = (uint32_t)(t0 % MX_ROWS) / 32;
-      bool ok = true;
-      for (int i = 0; i < kb1 - kb0; ++i) {
-        const int s = i % C::OS;
-        if (!mbar_wait(&op_full[s], (uint32_t)(i / C::OS) & 1u, p.err)) {
-          ok = false;
-          break;
+    // The whole warp runs the loop, one elected lane issues: uniform values
+    // keep the descriptors in uniform registers (see oq_mx_gemm.cu).
+    constexpr uint32_t idesc = F4 ? idesc_mx(SM_ROWS, BN, 1, 1) : idesc_mx(SM_ROWS, BN, 5, 0);
+    const uint32_t lead = elect_one();
+    const uint64_t desc0 = smem_desc_sw128(smem_base);
+    const uint64_t sdesc0 = smem_desc_scales(smem_base + C::STAGE - 1024 - C::SX);
+    const int count = kb1 - kb0;
+    int s = 0, ahead = 0;
+    uint32_t parity = 0, acc = 0, set = 0;
+    bool ok = true;
+    for (int i = 0; i < count; ++i) {
+      if (ahead == 0) {   // this stage and the next two, in one check
+        const int s1 = s + 1 == C::OS ? 0 : s + 1, s2 = s1 + 1 == C::OS ? 0 : s1 + 1;
+        const uint32_t f = smem_u32(op_full), left = (uint32_t)(count - i);
+        const uint32_t flip = (s1 == 0 ? 6u : 0u) | (s2 == 0 ? 4u : 0u);
+        const uint32_t full = mbar_test3(f + 8u * s, f + 8u * s1, f + 8u * s2, (parity ? 7u : 0u) ^ flip,
+                                         left > 2 ? 7u : left > 1 ? 3u : 1u);
+        ahead = !__all_sync(0xFFFFFFFFu, full & 1u)   ? 0
+                : !__all_sync(0xFFFFFFFFu, full & 2u) ? 1
+                : !__all_sync(0xFFFFFFFFu, full & 4u) ? 2
+                                                      : 3;
+        if (ahead == 0) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&op_full[s], parity, p.err))) {
+            ok = false;
+            break;
+          }
+          ahead = 1;
         }
         tc_fence_after();
-        const uint32_t st = smem_base + (uint32_t)s * C::STAGE;
-        const uint32_t sc = st + C::STAGE - 1024 - C::SX;
-        const uint32_t sfw = tmem + BN + (uint32_t)(i & 1) * (C::SF_COLS / 2), sfx = sfw + 4 * C::CT;
+      }
+      --ahead;
+      const uint32_t off = (uint32_t)s * (uint32_t)(C::STAGE >> 4);
+      const uint64_t wd = desc0 + off, xd = wd + (W_TILE >> 4), sd = sdesc0 + off;
+      const uint32_t sfw = tmem + BN + set * (C::SF_COLS / 2), sfx = sfw + 4 * C::CT;
+      set ^= 1u;
+      if (lead) {
 #pragma unroll
         for (int c = 0; c < C::CT; ++c) {
-          tc_copy_scales<1>(sfw + 4 * c, smem_desc_scales(sc + c * MX_TILE_BYTES));
+          tc_copy_scales<1>(sfw + 4 * c, sd + (c * MX_TILE_BYTES >> 4));
 #pragma unroll
           for (int r = 0; r < C::RT; ++r)
-            tc_copy_scales<1>(sfx + 4 * (c * C::RT + r),
-                              smem_desc_scales(sc + 1024 + (r * C::CT + c) * MX_TILE_BYTES));
+            tc_copy_scales<1>(sfx + 4 * (c * C::RT + r), sd + ((1024 + (r * C::CT + c) * MX_TILE_BYTES) >> 4));
         }
-        const uint64_t wd = smem_desc_sw128(st), xd = smem_desc_sw128(st + W_TILE);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = F4 ? k / 2 : 0;
-          const uint32_t id = idesc | idesc_mx_sf(F4 ? 2u * (k & 1) : (uint32_t)k);
-          tc_mma_mx<1, F4>(tmem, wd + 2 * k, xd + 2 * k, id, sfw + 4 * c, sfx + 4 * c * C::RT + sf_shift,
-                           i > 0 || k > 0 ? 1u : 0u);
+          tc_mma_mx<1, F4>(tmem, wd + 2 * k, xd + 2 * k, idesc | idesc_mx_sf(F4 ? 2u * (k & 1) : (uint32_t)k), sfw + 4 * c,
+                           sfx + 4 * c * C::RT, k > 0 ? 1u : acc);
         }
         tc_commit(&op_empty[s]);
       }
-      if (ok) tc_commit(acc_full);
+      __syncwarp();
+      acc = 1u;
+      if (++s == C::OS) {
+        s = 0;
+        parity ^= 1u;
+      }
     }
+    if (ok && lead) tc_commit(acc_full);
     __syncwarp();
   }
   __syncthreads();   // the producer's copies have landed: the stages may hold the partial tile
@@ -189,25 +217,32 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
     tmem_dealloc(tmem, C::TMEM);
   }
 
-  // this CTA's tokens of the tile: sums in rank order
-  const int tokens = (int)(p.T - t0 < BN ? p.T - t0 : BN);
-  const int c0 = tokens * rank / split, c1 = tokens * (rank + 1) / split;
-  uint32_t peer[MAX_SPLIT];
+  // this CTA's share of the tile, four outputs of a token at a time: sums in rank order
+  const int quads = (int)(p.T - t0 < BN ? p.T - t0 : BN) * (SM_ROWS / 4);
+  const int i0 = quads * rank / split, i1 = quads * (rank + 1) / split;
+  for (int i = i0 + (int)threadIdx.x; i < i1; i += NTHREADS) {
+    const int o = n0 + 4 * (i % (SM_ROWS / 4));
+    if (o >= p.N) continue;
+    float4 v[MAX_SPLIT];
 #pragma unroll
-  for (int r = 0; r < MAX_SPLIT; ++r) peer[r] = split > 1 && r < split ? mapa_shared(smem_base, (uint32_t)r) : smem_base;
-  for (int i = c0 * SM_ROWS + (int)threadIdx.x; i < c1 * SM_ROWS; i += NTHREADS) {
-    float v[MAX_SPLIT];
+    for (int r = 0; r < MAX_SPLIT; ++r)
+      if (r < split) v[r] = split > 1 ? ld_cluster_f32x4(mapa_shared(smem_base + 16u * i, (uint32_t)r)) : reinterpret_cast<const float4*>(partial)[i];
+    float4 sum = v[0];
 #pragma unroll
-    for (int r = 0; r < MAX_SPLIT; ++r) v[r] = r < split ? (split > 1 ? ld_cluster_f32(peer[r] + 4u * i) : partial[i]) : 0.f;
-    float sum = v[0];
-#pragma unroll
-    for (int r = 1; r < MAX_SPLIT; ++r) sum += v[r];
-    const int o = n0 + i % SM_ROWS;
-    if (o < p.N) {
-      const int64_t at = (t0 + i / SM_ROWS) * p.N + o;
-      if (p.y_bf16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(sum);
-      else static_cast<float*>(p.y)[at] = sum;
+    for (int r = 1; r < MAX_SPLIT; ++r) {
+      if (r < split) {
+        sum.x += v[r].x;
+        sum.y += v[r].y;
+        sum.z += v[r].z;
+        sum.w += v[r].w;
+      }
     }
+    const int64_t at = (t0 + i / (SM_ROWS / 4)) * p.N + o;
+    if (p.y_bf16)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) =
+          make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = sum;
   }
   if (split > 1) cluster_sync_all();   // no CTA leaves while a peer reads its partial tile
 }
@@ -216,7 +251,7 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
 // at least two stages
 int choose_split(int m_tiles, int64_t t_tiles, int nkb, int slots) {
   int best = 1;
-  for (int s = 2; s <= MAX_SPLIT; s *= 2)
+  for (int s = 2; s <= MAX_SPLIT; ++s)
     if ((int64_t)m_tiles * t_tiles * s <= slots && nkb >= 2 * s) best = s;
   return best;
 }
@@ -239,13 +274,15 @@ oq_status launch(const MxGemmArgs& g, cudaStream_t stream) {
   kp.err = g.err;
   const int m_tiles = (g.N + SM_ROWS - 1) / SM_ROWS;
   const int64_t t_tiles = (g.T + BN - 1) / BN;
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int device = 0;
+  const int sms = mx_sm_count(&device);
   kp.split = choose_split(m_tiles, t_tiles, kp.nkb, sms * (BN <= 64 ? 2 : 1));
 
-  cudaError_t e = cudaFuncSetAttribute(mx_small_kernel<F4, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-  if (e == cudaSuccess) {
+  static std::atomic<uint64_t> smem_set{0};
+  if ((st = mx_allow_smem(reinterpret_cast<const void*>(mx_small_kernel<F4, BN>), C::SMEM, device, &smem_set)) != OQ_OK)
+    return st;
+  cudaError_t e;
+  {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(m_tiles * kp.split), (unsigned)t_tiles, 1);
     cfg.blockDim = dim3(NTHREADS, 1, 1);
