@@ -97,42 +97,57 @@ __device__ __forceinline__ uint32_t cvt4_e4m3(float a, float b, float c, float d
   return r;
 }
 
-// Codes of one thread's eight elements and its block's scale code.  Four
-// neighbouring lanes hold a block; every lane of the warp takes part.
-//   scale = 2^(floor(log2 max|v|) - emax), emax 2 (e2m1) or 8 (e4m3): the
-// biased exponent of the largest magnitude less emax, not below code 0.  The
-// products v / scale are exact except below 2^-126, where the elements round
-// to zero either way, so the only rounding is the one to the element type.
-// A block with an infinity or a NaN gets scale code 255 and zero elements, so
-// that all of it reads as NaN.
-template <int BITS>
-__device__ __forceinline__ uint32_t mx_quantize8(float (&v)[8], uint32_t (&out)[BITS / 4]) {
-  uint32_t m = 0u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  const int e = (int)(m >> 23);
-  const int code = e == 255 ? 255 : max(e - (BITS == 4 ? 2 : 8), 0);
-  const float inv = __uint_as_float((uint32_t)(254 - (code == 255 ? 0 : code)) << 23);   // 2^(127 - code)
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = code == 255 ? 0.f : v[i] * inv;
-  if constexpr (BITS == 4) {
-    out[0] = cvt8_e2m1(v);
-  } else {
-    out[0] = cvt4_e4m3(v[0], v[1], v[2], v[3]);
-    out[1] = cvt4_e4m3(v[4], v[5], v[6], v[7]);
-  }
-  return (uint32_t)code;
+// |a|, |b|, |c|: the largest, NaN if one of them is
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
-// the four block scales of 16 neighbouring lanes as one word (in every lane)
-__device__ __forceinline__ uint32_t mx_scale_word(uint32_t code) {
-  const int base = threadIdx.x & 16;
-  uint32_t w = 0u;
+// Largest magnitude of a block of 32 elements, eight in each of four
+// neighbouring lanes, as fp32 bits (a NaN or an infinity on top); every lane of
+// the warp takes part.
+__device__ __forceinline__ uint32_t mx_block_max(const float (&v)[8]) {
+  const float m8 = max3_abs_nan(max3_abs_nan(v[0], v[1], v[2]), max3_abs_nan(v[3], v[4], v[5]), max3_abs_nan(v[6], v[7], 0.f));
+  uint32_t m = __float_as_uint(m8);   // not negative: ordered as integers
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+}
+
+// Its scale code: scale = 2^(floor(log2 max) - emax), emax 2 (e2m1) or 8
+// (e4m3), is the biased exponent of the largest magnitude less emax, not below
+// 0; 255 for a block with an infinity or a NaN.
+template <int BITS>
+__device__ __forceinline__ uint32_t mx_scale_code(uint32_t block_max) {
+  const int e = (int)(block_max >> 23);
+  return e == 255 ? 255u : (uint32_t)max(e - (BITS == 4 ? 2 : 8), 0);
+}
+
+// 1 / scale = 2^(127 - code), a normal number for every code below 255
+__device__ __forceinline__ float mx_inverse_scale(uint32_t code) { return __uint_as_float((254u - min(code, 254u)) << 23); }
+
+// Element codes of w = v / scale.  The products are exact except below 2^-126,
+// where the elements round to zero either way, so the only rounding is the one
+// to the element type.  A NaN block gets zero elements (its scale says NaN).
+template <int BITS>
+__device__ __forceinline__ void mx_element_codes(const float (&w)[8], uint32_t code, uint32_t (&out)[BITS / 4]) {
+  if constexpr (BITS == 4) {
+    out[0] = cvt8_e2m1(w);
+  } else {
+    out[0] = cvt4_e4m3(w[0], w[1], w[2], w[3]);
+    out[1] = cvt4_e4m3(w[4], w[5], w[6], w[7]);
+  }
+  if (code == 255u) {
 #pragma unroll
-  for (int b = 0; b < 4; ++b) w |= __shfl_sync(0xFFFFFFFFu, code, base + 4 * b) << (8 * b);
-  return w;
+    for (int i = 0; i < BITS / 4; ++i) out[i] = 0u;
+  }
+}
+
+// the four block codes of 16 neighbouring lanes as one word (in every lane)
+__device__ __forceinline__ uint32_t mx_scale_word(uint32_t code) {
+  uint32_t w = code << ((threadIdx.x & 12) << 1);
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
+  return w | __shfl_xor_sync(0xFFFFFFFFu, w, 8);
 }
 
 // Multiprocessors of the current device, asked for once per device, and the

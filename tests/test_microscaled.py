@@ -3,11 +3,10 @@ the plain fp64 reference (mx_reference.py).  Needs a B200.
 
 Bounds.  Quantisation and read-back have one rounding, to the element type,
 and are compared bit for bit.  The norm's fp32 values are off the fp64 ones by
-at most DELTA relative: a thread adds at most 64 squares in turn, then a tree
-of 5 + 4 levels (every rounding 2^-24, all terms positive, so at most 75
-roundings, 73 of them halved by the square root), and the mean, the root, the
-quotient and the two products add at most 7 half-ulps: below 48 * 2^-24, taken
-as 64 * 2^-24.  The product's fp32 sums add one value a 32-element block and
+at most DELTA relative: the sum of squares rounds in fp32 at most 75 times
+(2^-24 each, all terms positive, halved by the square root), and the mean, the
+root, the quotient and the two products add at most 7 half-ulps: below
+48 * 2^-24, taken as 64 * 2^-24.  The product's fp32 sums add one value a 32-element block and
 split; a tensor core may truncate instead of rounding, so each addition is off
 by at most 2^-23 of the magnitudes summed: (K / 32 + 8) 2^-23 sum |a w|, and
 bf16 y adds 2^-8 |y|."""
@@ -113,8 +112,10 @@ def test_read_back_of_every_code(env):
         for s in (0, 1, 100, 127, 200, 246, 255):
             sc = np.full((1, 8), s, dtype=np.uint8)
             c, t = R.pack(e, sc, bits)
-            v = _np(B.oq_mx_dequantize(torch.from_numpy(c).cuda(), torch.from_numpy(t).cuda(), 256, bits))
-            np.testing.assert_array_equal(v, R.dequantize(e, sc, bits).astype(np.float32))
+            tc, tt = torch.from_numpy(c).cuda(), torch.from_numpy(t).cuda()
+            want = R.dequantize(e, sc, bits).astype(np.float32)
+            np.testing.assert_array_equal(_np(B.oq_mx_dequantize(tc, tt, 256, bits)), want)
+            np.testing.assert_array_equal(_np(B.oq_mx_dequantize(tc, tt, 256, bits, torch.bfloat16)), R.bf16(want))
 
 
 # ------------------------------------------------------------------ norm
@@ -175,6 +176,28 @@ def test_norm_writes_the_residual_in_place(env, d):
         got = B.oq_rms_norm_mx(tx, residual=tr, residual_out=tx if which == "x" else tr)
         for a, b in zip(want, got):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_norm_codes_are_those_of_the_exact_values(env, dtype, bits):
+    # Elements next to a border between two codes are formed in fp64, so what
+    # is left is the sum of squares: eight are added four fp32 roundings deep,
+    # the rest in fp64, and the root halves that: 2 * 2^-24, taken as 2.5.  A
+    # code may differ from the fp64 value's only that close to a border.
+    # (e4m3's subnormals, below 2^-14 of a block's largest, are formed in fp32.)
+    torch, B = env
+    rng = np.random.default_rng(3)
+    rows, d, delta = 1000, 2048, 2.5 * 2.0 ** -24
+    x, r = _rows(rng, rows, d, dtype), _rows(rng, rows, d, dtype)
+    g = (1 + 0.2 * rng.standard_normal(d)).astype(np.float32)
+    codes, scales, _ = B.oq_rms_norm_mx(_cuda(torch, x, dtype), _cuda(torch, g, "fp32"), _cuda(torch, r, dtype), bits=bits)
+    n = R.norm(x.astype(np.float64), r.astype(np.float64), g.astype(np.float64), 1e-6)[1]
+    e, s = R.unpack(_np(codes), _np(scales), d, bits)
+    want, sc = R.quantize(n, bits)
+    normal = (want & 0x7F) >= 8 if bits == 8 else np.ones_like(want, dtype=bool)
+    R.check_quantized(n, np.where(normal, e, want), s, bits, delta)
+    R.check_quantized(n, e, s, bits, DELTA)
 
 
 # ------------------------------------------------------------------ product
