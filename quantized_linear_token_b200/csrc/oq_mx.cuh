@@ -28,6 +28,37 @@ __host__ __device__ inline int64_t mx_row_bytes(int d, int bits) { return (int64
 // 32-bit word of a scale tile that holds row r's four block scales
 __device__ __forceinline__ int mx_tile_word(int r) { return (r & 31) * 4 + ((r >> 5) & 3); }
 
+// Pairs of fp32 in one 64-bit register: one instruction does both
+// (round to nearest, as the scalar forms).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void unpack8(const f32x2 (&a)[4], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack2(a[i], v[2 * i], v[2 * i + 1]);
+}
+
 // Eight consecutive row elements in fp32: one 16-byte load of bf16, two of fp32.
 template <typename T>
 struct Vec8;
@@ -44,6 +75,12 @@ struct Vec8<__nv_bfloat16> {
       v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
   }
+  __device__ __forceinline__ void get(f32x2 (&v)[4]) const {
+    float f[8];
+    get(f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+  }
 };
 template <>
 struct Vec8<float> {
@@ -56,6 +93,10 @@ struct Vec8<float> {
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void get(f32x2 (&v)[4]) const {
+    v[0] = pack2(a.x, a.y), v[1] = pack2(a.z, a.w);
+    v[2] = pack2(b.x, b.y), v[3] = pack2(b.z, b.w);
   }
 };
 

@@ -202,17 +202,27 @@ __global__ void __launch_bounds__(QT) mx_dequantize_kernel(const uint8_t* __rest
 //
 // tpr threads own a row, each NCH vectors of eight neighbouring elements that
 // stay in registers between the sum and the quantisation (one pass over x and
-// r).  NCH = 0 reads x and r a second time instead (rows too long for the
-// registers): each thread re-reads only elements that it alone writes, so the
-// kept residual may overwrite either input in both forms.
+// r).  Two kernels:
+//   - rows by the hundred: CTAs stay and walk over rows, and every thread copies
+//     its vectors of the next row into its own places in shared memory
+//     (cp.async) while it works on this one.  Loads are then in flight all the
+//     time without holding registers, and no barrier is about the data
+//     (32760 x 5120 bf16, residual kept: 236 us, 5.0 TB/s; 337 us with a CTA a row).
+//   - few rows, or rows too long for two stages of shared memory: a CTA a row,
+//     straight from global memory.  NCH = 0 reads x and r a second time instead
+//     of keeping them (rows too long for the registers).
+// A thread re-reads only elements that it alone writes, so the kept residual may
+// overwrite either input everywhere.
 //
-// Precision: a thread adds its own squares in fp32, the row's sum is fp64, and
-// so is 1 / sqrt (an fp32 estimate, two Newton steps).  n is formed in fp32; it
-// may be four ulps off, which matters only where an element lies that close to
-// the border between two codes (or the block's largest to a power of two).  A
-// warp that meets such an element (0.2 % of its steps) forms its elements
-// again in fp64, rounded to fp32 towards the odd neighbour, from which the
-// rounding to the element type is that of the fp64 value.
+// Precision: eight squares are added in fp32 (four roundings deep), their sums
+// and 1 / sqrt in fp64, so the factor is within 2^-23 of exact.  n is formed in
+// fp32; it may be four ulps off, which matters only where an element lies that
+// close to the border between two codes (or the block's largest to a power of
+// two).  A warp that meets such an element (0.2 % of its steps) forms its
+// elements again in fp64, rounded to fp32 towards the odd neighbour, from which
+// the rounding to the element type is that of the fp64 value.
+constexpr size_t NORM_SMEM = 224 * 1024;   // stages of the streaming kernel
+
 struct NormParams {
   const void* x;
   const void* r;
@@ -228,24 +238,24 @@ struct NormParams {
 };
 
 template <typename T>
-__device__ __forceinline__ void load_h(const T* x, const T* r, float (&h)[8]) {
+__device__ __forceinline__ void load_h(const T* x, const T* r, f32x2 (&h)[4]) {
   Vec8<T> a;
   a.load(x);
   a.get(h);
   if (r) {
-    float b[8];
+    f32x2 b[4];
     Vec8<T> c;
     c.load(r);
     c.get(b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] += b[i];
+    for (int i = 0; i < 4; ++i) h[i] = add2(h[i], b[i]);
   }
 }
 
-__device__ __forceinline__ void load_gain(const NormParams& p, int col, float (&g)[8]) {
+__device__ __forceinline__ void load_gain(const NormParams& p, int col, f32x2 (&g)[4]) {
   if (!p.g) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = 1.f;
+    for (int i = 0; i < 4; ++i) g[i] = pack2(1.f, 1.f);
   } else if (p.g_bf16) {
     Vec8<__nv_bfloat16> q;
     q.load(static_cast<const __nv_bfloat16*>(p.g) + col);
@@ -270,20 +280,121 @@ __device__ __forceinline__ double rsqrt64(double v) {
   return y * (1.5 - 0.5 * v * y * y);
 }
 
+// squares of one vector, added four roundings deep
+__device__ __forceinline__ float sum_squares(const f32x2 (&v)[4]) {
+  const f32x2 q = add2(fma2(v[1], v[1], mul2(v[0], v[0])), fma2(v[3], v[3], mul2(v[2], v[2])));
+  float lo, hi;
+  unpack2(q, lo, hi);
+  return lo + hi;
+}
+
+// the row's sum over its tpr threads (warps w0 .. of the CTA), in every one of them
+__device__ __forceinline__ double row_sum(double v, double* part, int tpr, int w0) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if (tpr > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+    for (int w = 0; w < (tpr >> 5); ++w) v += part[w0 + w];
+  }
+  return v;
+}
+
+// One vector of a row: its codes, its scale and the kept residual.  Every lane
+// of the warp takes part; `in`: the vector holds elements; `own`: it lies in the
+// row's padded length.  x, r: where its elements can be read again.
+template <typename T, int BITS>
+__device__ __forceinline__ void norm_vector(const NormParams& p, const f32x2 (&v)[4], const T* x, const T* r, int col,
+                                            bool in, bool own, f32x2 rs2, double rs64, T* r_out, uint8_t* codes,
+                                            uint8_t* scales) {
+  f32x2 g[4];
+  if (in) {
+    load_gain(p, col, g);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = 0ull;
+  }
+  float w[8];
+  f32x2 n[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) n[i] = mul2(mul2(v[i], rs2), g[i]);
+  unpack8(n, w);
+  const uint32_t top = mx_block_max(w);
+  uint32_t code = mx_scale_code<BITS>(top);
+  const f32x2 inv2 = pack2(mx_inverse_scale(code), mx_inverse_scale(code));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) n[i] = mul2(n[i], inv2);
+  unpack8(n, w);
+  // Borders between codes, in the bits of w = n / scale: for e4m3 the middle of
+  // the low 20 mantissa bits; for e2m1 the zero of the low 21 (the borders of
+  // its least steps among them).  e4m3's subnormals, 2^-15 of the block's
+  // largest and less, are left out.
+  constexpr int SHIFT = BITS == 4 ? 11 : 12;
+  constexpr uint32_t OFFSET = (BITS == 4 ? 4u : 4u - 0x80000u) << SHIFT;
+  uint32_t near = 0xFFFFFFFFu;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t at = (__float_as_uint(w[i]) << SHIFT) + OFFSET;
+    near = min(near, BITS == 4 && fabsf(w[i]) < 0.2f ? near : at);
+  }
+  const bool border = in && top != 0u && (near <= (8u << SHIFT) || ((top + 4u) & 0x7FFFFFu) <= 8u);
+  if (__any_sync(0xFFFFFFFFu, border)) {
+    if (in) {
+      float a[8], c[8], gf[8];
+      unpack8(g, gf);
+      if (r) {   // the sum in fp64
+        Vec8<T> q;
+        q.load(x);
+        q.get(a);
+        q.load(r);
+        q.get(c);
+      } else {
+        unpack8(v, a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = to_odd(((double)a[i] + (double)c[i]) * rs64 * (double)gf[i]);
+    }
+    code = mx_scale_code<BITS>(mx_block_max(w));
+    const float inv = mx_inverse_scale(code);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] *= inv;
+  }
+  uint32_t out[BITS / 4];
+  mx_element_codes<BITS>(w, code, out);
+  const uint32_t word = mx_scale_word(code);
+  if (in && r_out) {
+    float f[8];
+    unpack8(v, f);
+    store8(r_out + col, f);
+  }
+  if (own) {
+    uint8_t* q = codes + col * BITS / 8;
+    if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(q) = out[0];
+    else *reinterpret_cast<uint2*>(q) = make_uint2(out[0], out[1]);
+    if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(scales + (col / MX_COLS) * MX_TILE_BYTES) = word;
+  }
+}
+
+// scales of the rows behind the last one, to the end of its tile: code 0 (one
+// CTA of at least 128 threads)
+__device__ __forceinline__ void norm_clear_padding(const NormParams& p) {
+  const int r = threadIdx.x & (MX_ROWS - 1), step = blockDim.x / MX_ROWS;
+  if (r < (int)(p.rows & (MX_ROWS - 1))) return;
+  uint32_t* w = reinterpret_cast<uint32_t*>(p.scales + (p.rows / MX_ROWS) * p.col_tiles * MX_TILE_BYTES) + mx_tile_word(r);
+  for (int c = threadIdx.x / MX_ROWS; c < p.col_tiles && (int)threadIdx.x < step * MX_ROWS; c += step)
+    w[c * (MX_TILE_BYTES / 4)] = 0u;
+}
+
 template <typename T, int BITS, int NCH>
 __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 1024 : 512) mx_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ double part[32];
   if ((int)blockIdx.x >= p.row_ctas) {
-    // scales of the rows behind the last one, to the end of its tile: code 0
-    const int r = threadIdx.x & (MX_ROWS - 1);
-    if (r < (int)(p.rows & (MX_ROWS - 1))) return;
-    uint32_t* w = reinterpret_cast<uint32_t*>(p.scales + (p.rows / MX_ROWS) * p.col_tiles * MX_TILE_BYTES) + mx_tile_word(r);
-    const int step = blockDim.x / MX_ROWS;   // a CTA has at least 128 threads
-    for (int c = threadIdx.x / MX_ROWS; c < p.col_tiles && (int)threadIdx.x < step * MX_ROWS; c += step)
-      w[c * (MX_TILE_BYTES / 4)] = 0u;
+    norm_clear_padding(p);
     return;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rpb = blockDim.x / p.tpr;                       // rows per CTA
   const int sub = threadIdx.x / p.tpr, t = threadIdx.x - sub * p.tpr;
   const int64_t row = (int64_t)blockIdx.x * rpb + sub;
@@ -292,33 +403,23 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 1024 : 512) mx_norm_ker
   const T* x = static_cast<const T*>(p.x) + base;
   const T* r = p.r ? static_cast<const T*>(p.r) + base : nullptr;
   const int steps = NCH ? NCH : (p.col_tiles * 16 + p.tpr - 1) / p.tpr;
-  float h[NCH ? NCH : 1][8];
+  f32x2 h[NCH ? NCH : 1][4];
   double total = 0.0;
-#pragma unroll
-  for (int k = 0; k < (NCH ? NCH : steps); ++k) {
-    const int col = (k * p.tpr + t) * 8;
-    float(&v)[8] = h[NCH ? k : 0];
+  auto load = [&](int col, f32x2(&v)[4]) {
     if (live && col < p.d) {
       load_h(x + col, r ? r + col : r, v);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int i = 0; i < 4; ++i) v[i] = 0ull;
     }
-    const float a = fmaf(v[1], v[1], v[0] * v[0]), b = fmaf(v[3], v[3], v[2] * v[2]);
-    const float c = fmaf(v[5], v[5], v[4] * v[4]), e = fmaf(v[7], v[7], v[6] * v[6]);
-    total += (double)((a + b) + (c + e));
-  }
+  };
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-  if (p.tpr > 32) {
-    if (lane == 0) part[warp] = total;
-    __syncthreads();
-    const int w0 = sub * (p.tpr >> 5);
-    total = 0.0;
-    for (int w = 0; w < (p.tpr >> 5); ++w) total += part[w0 + w];
+  for (int k = 0; k < (NCH ? NCH : steps); ++k) {
+    load((k * p.tpr + t) * 8, h[NCH ? k : 0]);
+    total += (double)sum_squares(h[NCH ? k : 0]);
   }
-  const double rs64 = rsqrt64(total * p.inv_d + (double)p.eps);
-  const float rs = (float)rs64;
+  const double rs64 = rsqrt64(row_sum(total, part, p.tpr, sub * (p.tpr >> 5)) * p.inv_d + (double)p.eps);
+  const f32x2 rs2 = pack2((float)rs64, (float)rs64);
 
   T* r_out = p.r_out ? static_cast<T*>(p.r_out) + base : nullptr;
   uint8_t* codes = p.codes + (live ? row : 0) * p.col_tiles * (MX_COLS * BITS / 8);
@@ -326,80 +427,97 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 1024 : 512) mx_norm_ker
 #pragma unroll
   for (int k = 0; k < (NCH ? NCH : steps); ++k) {
     const int col = (k * p.tpr + t) * 8;
-    float(&v)[8] = h[NCH ? k : 0];
-    const bool in = live && col < p.d;
-    float g[8], n[8], w[8];
-    if constexpr (NCH == 0) {
-      if (in) {
-        load_h(x + col, r ? r + col : r, v);
+    if constexpr (NCH == 0) load(col, h[0]);
+    norm_vector<T, BITS>(p, h[NCH ? k : 0], x + col, r ? r + col : r, col, live && col < p.d,
+                         live && col < p.col_tiles * MX_COLS, rs2, rs64, r_out, codes, scales);
+  }
+}
+
+__device__ __forceinline__ void copy_async16(void* dst_smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst_smem)), "l"(src)
+               : "memory");
+}
+
+template <typename T, int BITS, int NCH>
+__global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_constant__ NormParams p) {
+  __shared__ double part[2][16];
+  extern __shared__ __align__(16) unsigned char stage_mem[];
+  if ((int)blockIdx.x >= p.row_ctas) {
+    norm_clear_padding(p);
+    return;
+  }
+  constexpr int VB = 8 * (int)sizeof(T);   // bytes of a vector
+  const int t = threadIdx.x, tpr = blockDim.x;
+  const T* xs = static_cast<const T*>(p.x);
+  const T* rs_in = static_cast<const T*>(p.r);
+  // a stage: the row's vectors of x, then of r; a thread uses its own places only
+  const int plane = p.d * (int)sizeof(T), stage = rs_in ? 2 * plane : plane;
+  unsigned char* mine = stage_mem + t * VB;
+  auto fetch = [&](int64_t row, int s) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) {
+        const int col = (k * tpr + t) * 8;
+        if (col < p.d) {
+          unsigned char* q = mine + s * stage + k * tpr * VB;
+          const int64_t off = row * p.d + col;
+#pragma unroll
+          for (int b = 0; b < VB; b += 16) copy_async16(q + b, reinterpret_cast<const unsigned char*>(xs + off) + b);
+          if (rs_in) {
+#pragma unroll
+            for (int b = 0; b < VB; b += 16) copy_async16(q + plane + b, reinterpret_cast<const unsigned char*>(rs_in + off) + b);
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int s = 0;
+  fetch(blockIdx.x, 0);
+  for (int64_t row = blockIdx.x; row < p.rows; row += p.row_ctas, s ^= 1) {
+    fetch(row + p.row_ctas, s ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const unsigned char* q = mine + s * stage;
+    f32x2 h[NCH][4];
+    double total = 0.0;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const T* a = reinterpret_cast<const T*>(q + k * tpr * VB);
+      if ((k * tpr + t) * 8 < p.d) {
+        load_h(a, rs_in ? reinterpret_cast<const T*>(q + k * tpr * VB + plane) : nullptr, h[k]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        for (int i = 0; i < 4; ++i) h[k][i] = 0ull;
       }
+      total += (double)sum_squares(h[k]);
     }
-    if (in) {
-      load_gain(p, col, g);
-    } else {
+    const double rs64 = rsqrt64(row_sum(total, part[s], tpr, 0) * p.inv_d + (double)p.eps);
+    const f32x2 rs2 = pack2((float)rs64, (float)rs64);
+    T* r_out = p.r_out ? static_cast<T*>(p.r_out) + row * p.d : nullptr;
+    uint8_t* codes = p.codes + row * p.col_tiles * (MX_COLS * BITS / 8);
+    uint8_t* scales = p.scales + row / MX_ROWS * p.col_tiles * MX_TILE_BYTES + 4 * mx_tile_word((int)(row % MX_ROWS));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) n[i] = v[i] * rs * g[i];
-    uint32_t top = mx_block_max(n);
-    uint32_t code = mx_scale_code<BITS>(top);
-    float inv = mx_inverse_scale(code);
-    // Borders between codes, in the bits of w = n / scale: for e4m3 the middle
-    // of the low 20 mantissa bits; for e2m1 the zero of the low 21 (the borders
-    // of its least steps among them).  e4m3's subnormals, 2^-15 of the block's
-    // largest and less, are left out.
-    constexpr int SHIFT = BITS == 4 ? 11 : 12;
-    constexpr uint32_t OFFSET = (BITS == 4 ? 4u : 4u - 0x80000u) << SHIFT;
-    uint32_t near = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = n[i] * inv;
-      const uint32_t at = (__float_as_uint(w[i]) << SHIFT) + OFFSET;
-      near = min(near, BITS == 4 && fabsf(w[i]) < 0.2f ? near : at);
-    }
-    const bool border = near <= (8u << SHIFT) || ((top + 4u) & 0x7FFFFFu) <= 8u;
-    if (__any_sync(0xFFFFFFFFu, in && border && top != 0u)) {
-      if (in) {
-        double b[8];
-        if (r) {   // the sum in fp64: this step's elements are not written yet
-          float a[8];
-          Vec8<T> q;
-          q.load(x + col);
-          q.get(a);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] = (double)a[i];
-          q.load(r + col);
-          q.get(a);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] += (double)a[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] = (double)v[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = to_odd(b[i] * rs64 * (double)g[i]);
-      }
-      top = mx_block_max(n);
-      code = mx_scale_code<BITS>(top);
-      inv = mx_inverse_scale(code);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = n[i] * inv;
-    }
-    uint32_t out[BITS / 4];
-    mx_element_codes<BITS>(w, code, out);
-    const uint32_t word = mx_scale_word(code);
-    if (in && r_out) store8(r_out + col, v);
-    if (live && col < p.col_tiles * MX_COLS) {
-      uint8_t* q = codes + col * BITS / 8;
-      if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(q) = out[0];
-      else *reinterpret_cast<uint2*>(q) = make_uint2(out[0], out[1]);
-      if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(scales + (col / MX_COLS) * MX_TILE_BYTES) = word;
+    for (int k = 0; k < NCH; ++k) {
+      const int col = (k * tpr + t) * 8;
+      const T* a = reinterpret_cast<const T*>(q + k * tpr * VB);
+      norm_vector<T, BITS>(p, h[k], a, rs_in ? reinterpret_cast<const T*>(q + k * tpr * VB + plane) : nullptr, col,
+                           col < p.d, col < p.col_tiles * MX_COLS, rs2, rs64, r_out, codes, scales);
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <typename T, int BITS, int NCH>
+oq_status norm_stream_launch(NormParams& p, int threads, int sms, int device, size_t smem, cudaStream_t st) {
+  static std::atomic<uint64_t> smem_set{0};
+  const oq_status ok = mx_allow_smem(reinterpret_cast<const void*>(mx_norm_stream_kernel<T, BITS, NCH>), NORM_SMEM, device,
+                                     &smem_set);
+  if (ok != OQ_OK) return ok;
+  // CTAs an SM holds: 64 registers a thread, 228 KB of shared memory with 1 KB a CTA of the system's and 256 bytes of sums
+  const int resident = std::max(1, std::min(1024 / threads, (int)(228 * 1024 / (smem + 1024 + 256))));
+  p.row_ctas = (int)std::min<int64_t>(p.rows, (int64_t)sms * resident);
+  mx_norm_stream_kernel<T, BITS, NCH><<<(unsigned)p.row_ctas + (p.rows % MX_ROWS ? 1u : 0u), threads, smem, st>>>(p);
+  return launch_status("oq_rms_norm_mx");
 }
 
 template <typename T, int BITS>
@@ -409,39 +527,33 @@ oq_status norm_launch(const NormParams& p0, cudaStream_t st) {
   const int sms = mx_sm_count(&device);
   const int chunks = p.col_tiles * 16;   // vectors of eight, padding included
   auto threads_for = [&](int n) { return ((chunks + n - 1) / n + 31) / 32 * 32; };
-  // Vectors a thread holds.  Few rows: as many threads as a CTA takes, for the
-  // least latency.  Otherwise the count of 2 to 8 that leaves the fewest idle
-  // places, four at a tie (loads in flight against registers).
-  int nch = 0;
-  if (p.rows <= sms) {
-    for (const int n : {1, 2, 3, 4, 5, 6, 7, 8})
-      if (!nch && threads_for(n) <= (n <= 2 ? 1024 : 512)) nch = n;
-  } else {
-    for (const int n : {4, 3, 5, 2, 6, 7, 8})
-      if (threads_for(n) <= 512 && (!nch || threads_for(n) * n < threads_for(nch) * nch)) nch = n;
+  // the streaming kernel, where there are rows enough to walk over
+  if (p.rows > 2 * sms) {
+    // vectors a thread holds: two where a CTA's threads allow it (64 registers
+    // without spills), four where they leave fewer idle places or must
+    const int nch = threads_for(2) <= 512 && (threads_for(2) <= 2 * threads_for(4) || threads_for(4) < 128) ? 2 : 4;
+    const int threads = threads_for(nch);
+    const size_t smem = (size_t)2 * p.d * sizeof(T) * (p.r ? 2 : 1);
+    if (threads >= 128 && threads <= 512 && smem <= NORM_SMEM)
+      return nch == 2 ? norm_stream_launch<T, BITS, 2>(p, threads, sms, device, smem, st)
+                      : norm_stream_launch<T, BITS, 4>(p, threads, sms, device, smem, st);
   }
+  // A CTA a row: as many threads as fit, for the least latency
+  int nch = 0;
+  for (const int n : {1, 2, 4, 8})
+    if (!nch && threads_for(n) <= (n <= 2 ? 1024 : 512)) nch = n;
   p.tpr = nch ? threads_for(nch) : 512;
   const int rpb = (127 + p.tpr) / p.tpr, threads = p.tpr * rpb;
   const int64_t grid = (p.rows + rpb - 1) / rpb;
   p.row_ctas = (int)grid;
   const unsigned ctas = (unsigned)grid + (p.rows % MX_ROWS ? 1u : 0u);
-#define OQ_NORM(N)                                                        \
-  case N:                                                                 \
-    mx_norm_kernel<T, BITS, N><<<ctas, threads, 0, st>>>(p);              \
-    break
   switch (nch) {
-    OQ_NORM(1);
-    OQ_NORM(2);
-    OQ_NORM(3);
-    OQ_NORM(4);
-    OQ_NORM(5);
-    OQ_NORM(6);
-    OQ_NORM(7);
-    OQ_NORM(8);
-    default:
-      mx_norm_kernel<T, BITS, 0><<<ctas, threads, 0, st>>>(p);
+    case 1: mx_norm_kernel<T, BITS, 1><<<ctas, threads, 0, st>>>(p); break;
+    case 2: mx_norm_kernel<T, BITS, 2><<<ctas, threads, 0, st>>>(p); break;
+    case 4: mx_norm_kernel<T, BITS, 4><<<ctas, threads, 0, st>>>(p); break;
+    case 8: mx_norm_kernel<T, BITS, 8><<<ctas, threads, 0, st>>>(p); break;
+    default: mx_norm_kernel<T, BITS, 0><<<ctas, threads, 0, st>>>(p);
   }
-#undef OQ_NORM
   return launch_status("oq_rms_norm_mx");
 }
 
