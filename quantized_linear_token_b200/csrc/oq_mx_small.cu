@@ -3,10 +3,11 @@
 // MMA's M and the batch, padded to BN tokens, its N:
 //   y[t, o] = sum_k w[o, k] a[t, k]
 // A CTA takes 128 weight rows, and the K range is split over the CTAs of a
-// cluster, so that enough CTAs stream weights at once.  Their fp32 partial
-// tiles meet in distributed shared memory and are added in rank order, each
-// CTA for its share of the tokens: no workspace, no atomics, one launch, and
-// the same bits on every call.  4-bit activations use kind::mxf4, 8-bit ones
+// cluster, so that enough CTAs stream weights at once.  Each CTA owns a share of
+// the tokens; all send it their fp32 partial sums by bulk copies from shared
+// memory to shared memory, and it adds them in rank order: no workspace, no
+// atomics, one launch, and the same bits on every call.  (At 256 tokens, 13824
+// deep, loading the peers' sums instead took a third of the kernel.)  4-bit activations use kind::mxf4, 8-bit ones
 // kind::mxf8f6f4 with the weights' codes spread to 8-bit containers by TMA.
 //
 // Warps: 0-3 epilogue, 4 TMA producer, 5 tensor memory and MMAs.
@@ -22,7 +23,6 @@ namespace {
 constexpr int SM_ROWS = 128;                 // weight rows per CTA
 constexpr int W_TILE = SM_ROWS * 128;
 constexpr int TMA_WARP = 4, MMA_WARP = 5, NTHREADS = 6 * 32;
-constexpr int MAX_SPLIT = 8;
 
 template <bool F4, int BN>
 struct Cfg {
@@ -40,8 +40,14 @@ struct Cfg {
   static constexpr int BUDGET = BN <= 64 ? 108 * 1024 : 216 * 1024;
   static constexpr int OS = BUDGET / STAGE < 8 ? BUDGET / STAGE : 8;
   static_assert(OS >= 3, "the checks cover three stages");
-  static constexpr int PART = BN * SM_ROWS * 4;               // fp32 partial tile, over the stages
-  static constexpr size_t SMEM = 1024 + (size_t)(OS * STAGE > PART ? OS * STAGE : PART) + 8 * (2 * OS + 1) + 16;
+  // CTAs that may split the K range: what is received must fit behind the CTA's
+  // own partial sums, both in the stages' place once all products are done
+  static constexpr int SPLIT = BN <= 128 ? 8 : 3;
+  static constexpr int PART = BN * SM_ROWS * 4;               // [token][128 rows]
+  static constexpr int RECV = (BN <= 128 ? BN + SPLIT : 2 * ((BN + 2) / 3)) * SM_ROWS * 4;
+  static constexpr int RING = OS * STAGE > PART + RECV ? OS * STAGE : PART + RECV;
+  static constexpr size_t SMEM = 1024 + (size_t)RING + 8 * (2 * OS + 2) + 16;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 struct SmallParams {
@@ -53,14 +59,18 @@ struct SmallParams {
   int* err;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+// bulk copy of this CTA's shared memory into a peer's, counted on the peer's barrier (cluster addresses)
+__device__ __forceinline__ void bulk_s2peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
                : "memory");
-  return v;
 }
+// The two halves of a cluster barrier.  The arrival is relaxed: what it tells is
+// that this CTA's asynchronous reads and writes of its shared memory are done,
+// each of them seen complete on an mbarrier; no ordinary store goes with it (a
+// release would wait for those, some 1200 cycles).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 template <bool F4, int BN>
 __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(const __grid_constant__ SmallParams p) {
@@ -68,11 +78,12 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* op_full = reinterpret_cast<uint64_t*>(smem + (C::OS * C::STAGE > C::PART ? C::OS * C::STAGE : C::PART));
+  uint64_t* op_full = reinterpret_cast<uint64_t*>(smem + C::RING);
   uint64_t* op_empty = op_full + C::OS;
   uint64_t* acc_full = op_empty + C::OS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
-  float* partial = reinterpret_cast<float*>(smem);   // [BN][128], once every stage has been consumed
+  uint64_t* received = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(received + 1);
+  float* partial = reinterpret_cast<float*>(smem);   // [token][128 rows], then the peers' [source][owned token][128 rows]
 
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int split = p.split;
@@ -81,14 +92,29 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
   const int64_t t0 = (int64_t)blockIdx.y * BN;
   // this CTA's share of the stages
   const int kb0 = (int)((int64_t)p.nkb * rank / split), kb1 = (int)((int64_t)p.nkb * (rank + 1) / split);
+  const int count = kb1 - kb0;
 
-  if (threadIdx.x == 0) {
+  // stage i of this CTA's share
+  auto fetch = [&](int i) {
+    const int s = i % C::OS, kb = kb0 + i;
+    mbar_arrive_expect_tx(&op_full[s], C::TX);
+    unsigned char* st = smem + s * C::STAGE;
+    unsigned char* sw = st + C::STAGE - 1024 - C::SX;
+    tma_load_2d(st, &p.w_map, kb * 128, n0, &op_full[s]);
+    tma_load_2d(st + W_TILE, &p.x_map, kb * 128, (int32_t)t0, &op_full[s]);
+    tma_load_3d(sw, &p.sw_map, 0, kb * C::CT, n0 / MX_ROWS, &op_full[s]);
+    tma_load_3d(sw + 1024, &p.sx_map, 0, kb * C::CT, (int32_t)(t0 / MX_ROWS), &op_full[s]);
+  };
+  // the first two stages' loads leave before tensor memory is there
+  if (warp == TMA_WARP && lane == 0) {
     for (int s = 0; s < C::OS; ++s) {
       mbar_init(&op_full[s], 1);
       mbar_init(&op_empty[s], 1);
     }
     mbar_init(acc_full, 1);
+    mbar_init(received, 1);
     fence_mbar_init();
+    for (int i = 0; i < count && i < 2; ++i) fetch(i);
   }
   if (warp == MMA_WARP) {
     tmem_alloc(tmem_slot, C::TMEM);
@@ -102,19 +128,10 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
 
   if (warp == TMA_WARP) {
     if (lane == 0) {
-      int issued = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const int s = issued % C::OS;
-        const uint32_t n = (uint32_t)(issued / C::OS);
-        if (n > 0 && !mbar_wait(&op_empty[s], (n - 1) & 1u, p.err)) break;
-        mbar_arrive_expect_tx(&op_full[s], C::TX);
-        unsigned char* st = smem + s * C::STAGE;
-        unsigned char* sw = st + C::STAGE - 1024 - C::SX;
-        tma_load_2d(st, &p.w_map, kb * 128, n0, &op_full[s]);
-        tma_load_2d(st + W_TILE, &p.x_map, kb * 128, (int32_t)t0, &op_full[s]);
-        tma_load_3d(sw, &p.sw_map, 0, kb * C::CT, n0 / MX_ROWS, &op_full[s]);
-        tma_load_3d(sw + 1024, &p.sx_map, 0, kb * C::CT, (int32_t)(t0 / MX_ROWS), &op_full[s]);
-        ++issued;
+      int issued = count < 2 ? count : 2;
+      for (; issued < count; ++issued) {
+        if (issued >= C::OS && !mbar_wait(&op_empty[issued % C::OS], (uint32_t)(issued / C::OS - 1) & 1u, p.err)) break;
+        fetch(issued);
       }
       // no copy may be in flight when the stages are reused or the CTA leaves
       for (int g = issued > C::OS ? issued - C::OS : 0; g < issued; ++g)
@@ -128,7 +145,6 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
     const uint32_t lead = elect_one();
     const uint64_t desc0 = smem_desc_sw128(smem_base);
     const uint64_t sdesc0 = smem_desc_scales(smem_base + C::STAGE - 1024 - C::SX);
-    const int count = kb1 - kb0;
     int s = 0, ahead = 0;
     uint32_t parity = 0, acc = 0, set = 0;
     bool ok = true;
@@ -183,16 +199,20 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
     if (ok && lead) tc_commit(acc_full);
     __syncwarp();
   }
-  __syncthreads();   // the producer's copies have landed: the stages may hold the partial tile
-
-  // the partial tile [token][weight row] in shared memory: a lane writes one
-  // row's value per token, neighbouring lanes neighbouring words
+  const bool ok = mbar_wait(acc_full, 0u, p.err);
+  tc_fence_after();
+  __syncthreads();   // the producer's copies have landed too: the stages are free
+  const int tokens = (int)(p.T - t0 < BN ? p.T - t0 : BN);
+  const int c0 = tokens * rank / split, owned = tokens * (rank + 1) / split - c0;
+  if (split > 1) {
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(received, (uint32_t)((split - 1) * owned * SM_ROWS * 4));
+    cluster_arrive();
+  }
+  // the partial tile: a lane holds one weight row, neighbouring lanes write neighbouring words
   if (warp < 4) {
-    const bool ok = kb1 > kb0 && mbar_wait(acc_full, 0u, p.err);
-    tc_fence_after();
     if constexpr (BN >= 32) {
 #pragma unroll 1
-      for (int cc = 0; cc < BN / 32; ++cc) {
+      for (int cc = 0; cc * 32 < tokens; ++cc) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(cc * 32), v);
         tmem_wait_ld();
@@ -201,57 +221,77 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
           partial[(cc * 32 + j) * SM_ROWS + warp * 32 + lane] = ok ? __uint_as_float(v[j]) : 0.f;
       }
     } else {
-      // 16 tokens; the 16 columns read behind them are scales and not used
+      // 16 tokens; the 16 columns behind them are scales and not used
       uint32_t v[32];
       tmem_ld_32x32b_x32(tmem + ((uint32_t)(warp * 32) << 16), v);
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < BN; ++j) partial[j * SM_ROWS + warp * 32 + lane] = ok ? __uint_as_float(v[j]) : 0.f;
     }
+    fence_proxy_async_smem();
   }
   tc_fence_before();
-  if (split > 1) cluster_sync_all();
-  else __syncthreads();
+  __syncthreads();
   if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM);
   }
-
-  // this CTA's share of the tile, four outputs of a token at a time: sums in rank order
-  const int quads = (int)(p.T - t0 < BN ? p.T - t0 : BN) * (SM_ROWS / 4);
-  const int i0 = quads * rank / split, i1 = quads * (rank + 1) / split;
-  for (int i = i0 + (int)threadIdx.x; i < i1; i += NTHREADS) {
-    const int o = n0 + 4 * (i % (SM_ROWS / 4));
-    if (o >= p.N) continue;
-    float4 v[MAX_SPLIT];
-#pragma unroll
-    for (int r = 0; r < MAX_SPLIT; ++r)
-      if (r < split) v[r] = split > 1 ? ld_cluster_f32x4(mapa_shared(smem_base + 16u * i, (uint32_t)r)) : reinterpret_cast<const float4*>(partial)[i];
-    float4 sum = v[0];
-#pragma unroll
-    for (int r = 1; r < MAX_SPLIT; ++r) {
-      if (r < split) {
-        sum.x += v[r].x;
-        sum.y += v[r].y;
-        sum.z += v[r].z;
-        sum.w += v[r].w;
-      }
+  if (split > 1) {
+    cluster_wait();   // every CTA's stages are free and its barrier armed
+    const int r = (int)threadIdx.x;
+    if (r < split && r != rank) {
+      const int first = tokens * r / split, theirs = tokens * (r + 1) / split - first;
+      // in the peer: the sources before and after it, without a place of its own
+      const int slot = rank < r ? rank : rank - 1;
+      if (theirs > 0)
+        bulk_s2peer(mapa_shared(smem_base + (uint32_t)((BN + slot * theirs) * SM_ROWS * 4), (uint32_t)r),
+                    smem_base + (uint32_t)(first * SM_ROWS * 4), (uint32_t)(theirs * SM_ROWS * 4),
+                    mapa_shared(smem_u32(received), (uint32_t)r));
     }
-    const int64_t at = (t0 + i / (SM_ROWS / 4)) * p.N + o;
-    if (p.y_bf16)
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) =
-          make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = sum;
+    __syncwarp();
+    mbar_wait(received, 0u, p.err);
+    cluster_arrive();   // what was sent here has arrived
   }
-  if (split > 1) cluster_sync_all();   // no CTA leaves while a peer reads its partial tile
+
+  // The owned tokens, four outputs a thread: sums in rank order.  The sources
+  // are loaded before the first is used.
+  const int quad = threadIdx.x & 31, o = n0 + 4 * quad;
+  if (o < p.N) {
+    constexpr int QUADS = SM_ROWS / 4;
+    const float4* mine = reinterpret_cast<const float4*>(partial + c0 * SM_ROWS) + quad;
+    const float4* recv = reinterpret_cast<const float4*>(partial + BN * SM_ROWS) + quad;
+#pragma unroll 2
+    for (int c = threadIdx.x >> 5; c < owned; c += NTHREADS / 32) {
+      float4 v[C::SPLIT];
+#pragma unroll
+      for (int r = 0; r < C::SPLIT; ++r)
+        if (r < split) v[r] = r == rank ? mine[c * QUADS] : recv[((r < rank ? r : r - 1) * owned + c) * QUADS];
+      float4 sum = v[0];
+#pragma unroll
+      for (int r = 1; r < C::SPLIT; ++r) {
+        if (r < split) {
+          sum.x += v[r].x;
+          sum.y += v[r].y;
+          sum.z += v[r].z;
+          sum.w += v[r].w;
+        }
+      }
+      const int64_t at = (t0 + c0 + c) * p.N + o;
+      if (p.y_bf16)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) =
+            make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = sum;
+    }
+  }
+  if (split > 1) cluster_wait();   // no CTA leaves before its sums have been copied out
 }
 
 // CTAs that split a weight tile's K range: as many as fill the SMs, each with
 // at least two stages
-int choose_split(int m_tiles, int64_t t_tiles, int nkb, int slots) {
+int choose_split(int m_tiles, int64_t t_tiles, int nkb, int slots, int most) {
   int best = 1;
-  for (int s = 2; s <= MAX_SPLIT; ++s)
+  for (int s = 2; s <= most; ++s)
     if ((int64_t)m_tiles * t_tiles * s <= slots && nkb >= 2 * s) best = s;
   return best;
 }
@@ -276,7 +316,7 @@ oq_status launch(const MxGemmArgs& g, cudaStream_t stream) {
   const int64_t t_tiles = (g.T + BN - 1) / BN;
   int device = 0;
   const int sms = mx_sm_count(&device);
-  kp.split = choose_split(m_tiles, t_tiles, kp.nkb, sms * (BN <= 64 ? 2 : 1));
+  kp.split = choose_split(m_tiles, t_tiles, kp.nkb, sms * (BN <= 64 ? 2 : 1), C::SPLIT);
 
   static std::atomic<uint64_t> smem_set{0};
   if ((st = mx_allow_smem(reinterpret_cast<const void*>(mx_small_kernel<F4, BN>), C::SMEM, device, &smem_set)) != OQ_OK)
