@@ -229,6 +229,14 @@ struct MxGemmArgs {
 };
 oq_status mx_gemm_launch(const MxGemmArgs& g, void* stream);
 oq_status mx_small_launch(const MxGemmArgs& g, void* stream);
-constexpr int MX_SMALL_MAX_T = 256;   // batches up to this size take the small-batch kernel
+// Batches that take the small-batch kernel: up to 128 tokens, and up to 256
+// where K runs over more than 24 stages (of 256 4-bit or 128 8-bit elements), so
+// that splitting K pays for the exchange of 256 tokens' sums.  Measured at 256
+// tokens (us, small / pairs): 13824 -> 5120 17.1 / 24.7 (4 bits, 54 stages), 22.9
+// / 44.1 (8 bits, 108); 5120 -> 5120 13.0 / 12.0 (20), 15.3 / 20.0 (40); 2048 ->
+// 1040 10.2 / 7.4 (8), 10.9 / 10.2 (16).  At 300 tokens the pairs are even or ahead.
+inline bool mx_small_batch(int64_t T, int K, int a_bits) {
+  return T <= 128 || (T <= 256 && mx_col_tiles(K) * a_bits / 8 > 24);
+}
 
 }  // namespace oq

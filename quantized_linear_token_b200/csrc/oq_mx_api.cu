@@ -190,7 +190,7 @@ oq_status oq_linear_mx(const oq_layer* L, const uint8_t* codes, const uint8_t* s
   g.K = L->d_in;
   g.a_bits = L->a_bits;
   g.err = L->d_error;
-  return unsupported(T <= MX_SMALL_MAX_T ? mx_small_launch(g, stream) : mx_gemm_launch(g, stream), who);
+  return unsupported(mx_small_batch(T, g.K, g.a_bits) ? mx_small_launch(g, stream) : mx_gemm_launch(g, stream), who);
 }
 
 }  // extern "C"

@@ -33,7 +33,8 @@ struct Cfg {
   static constexpr int STAGE = W_TILE + (X_TILE + 1023) / 1024 * 1024 + 1024 + SX;
   // a load that spreads 4-bit codes counts the packed bytes, half of what it writes
   static constexpr uint32_t TX = (F4 ? W_TILE : W_TILE / 2) + X_TILE + (1 + RT) * CT * MX_TILE_BYTES;
-  static constexpr int SF_COLS = 2 * CT * 4 * (1 + RT);       // two sets of scale columns
+  static constexpr int SF_SET = CT * 4 * (1 + RT), SF_SETS = 4;   // scale columns of a stage; sets used in turn
+  static constexpr int SF_COLS = SF_SET * SF_SETS;
   static constexpr uint32_t TMEM = BN + SF_COLS <= 32 ? 32 : BN + SF_COLS <= 64 ? 64 : BN + SF_COLS <= 128 ? 128
                                    : BN + SF_COLS <= 256 ? 256 : 512;
   // up to 64 tokens two CTAs share an SM
@@ -171,8 +172,8 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
       --ahead;
       const uint32_t off = (uint32_t)s * (uint32_t)(C::STAGE >> 4);
       const uint64_t wd = desc0 + off, xd = wd + (W_TILE >> 4), sd = sdesc0 + off;
-      const uint32_t sfw = tmem + BN + set * (C::SF_COLS / 2), sfx = sfw + 4 * C::CT;
-      set ^= 1u;
+      const uint32_t sfw = tmem + BN + set * C::SF_SET, sfx = sfw + 4 * C::CT;
+      set = (set + 1) % C::SF_SETS;
       if (lead) {
 #pragma unroll
         for (int c = 0; c < C::CT; ++c) {

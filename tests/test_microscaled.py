@@ -231,7 +231,8 @@ def _product(env, T, d, n, bits, y_dtype, seed=0):
 @pytest.mark.parametrize("T,d,n,y", [
     (1, 32, 16, "fp32"), (1, 256, 128, "fp32"), (1, 2016, 1040, "bf16"), (2, 5120, 272, "fp32"), (16, 128, 144, "bf16"),
     (17, 288, 256, "fp32"), (33, 1024, 96, "bf16"), (64, 640, 400, "fp32"), (65, 160, 128, "fp32"),
-    (128, 2048, 512, "bf16"), (129, 96, 48, "fp32"), (256, 1056, 640, "bf16")])
+    (128, 2048, 512, "bf16"), (129, 96, 48, "fp32"), (256, 1056, 640, "bf16"), (200, 6720, 272, "fp32"),
+    (256, 13824, 144, "bf16")])
 def test_product_small_batches(env, T, d, n, y, bits):
     _product(env, T, d, n, bits, y)
 
@@ -277,6 +278,66 @@ def test_product_of_nan_blocks(env, T, bits):
     want[7, :] = np.nan
     want[:, 35] = np.nan
     np.testing.assert_array_equal(z, want)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T", [9, 280])
+def test_product_over_the_range_of_scales(env, T, bits):
+    # a scale code per row from 2^-110 to 2^110, against weight rows from 2^-60
+    # to 2^60 (products stay normal in fp32 where both ends do not meet)
+    torch, B = env
+    rng = np.random.default_rng(bits)
+    d, n = 288, 80
+    ops = []
+    for rows, b, far in ((T, bits, 110), (n, 4, 60)):
+        v = rng.choice(R.E2M1[1:], (rows, d)) * rng.choice([-1.0, 1.0], (rows, d))
+        s = np.repeat(127 + rng.integers(-far, far + 1, (rows, 1)), d // 32, axis=1).astype(np.uint8)
+        e = R.round_codes(v, b)
+        ops.append((R.dequantize(e, s, b), R.pack(e, s, b)))
+    layer = B.oq_layer_create(d, n, 0, bits, 4, B.OQ_FLAG_MICROSCALED)
+    (a, (ac, at)), (w, (wc, wt)) = ops
+    y = _np(B.oq_linear_mx(layer, *[torch.from_numpy(v).cuda() for v in (ac, at, wc, wt)])).astype(np.float64)
+    # Every partial sum is a multiple of a quarter of the two rows' scales, and
+    # at most 288 * 36 of them, so fp32 holds it exactly: as long as it is normal
+    # (first condition), and as no partial sum can overflow, which the sum of
+    # magnitudes bounds (the result alone does not: terms of both signs).
+    exact = a @ w.T
+    fine = (np.abs(a).max(1)[:, None] * np.abs(w).max(1)[None, :] > 2.0 ** -100) & (np.abs(a) @ np.abs(w).T < 2.0 ** 127)
+    assert fine.mean() > 0.5 and np.array_equal(y[fine], exact[fine])
+
+
+def test_offsets_past_32_bits(env):
+    # 4.6e9 elements of x, 2.3 GB of codes; and y of 4.4e9 elements: the last
+    # rows are those of a call on them alone
+    torch, B = env
+    rows, d = 70016, 65504                # the last 128-row tile begins at a multiple of 128
+    x = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda")
+    x[:-300].zero_()
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x[-300:] = torch.randn(300, d, generator=gen, device="cuda").bfloat16()
+    start = (rows - 300) // 128 * 128
+    codes, scales = B.oq_mx_quantize(x, 4)
+    c, s = B.oq_mx_quantize(x[start:], 4)
+    assert torch.equal(codes[start:], c) and torch.equal(scales[start // 128:], s)
+    v = B.oq_mx_dequantize(codes, scales, d, 4, torch.bfloat16)
+    assert torch.equal(v[start:], B.oq_mx_dequantize(c, s, d, 4, torch.bfloat16))
+    del v, codes, scales, c, s
+    codes, scales, kept = B.oq_rms_norm_mx(x, residual=x, residual_out=x)
+    assert kept is x
+    codes1, scales1, _ = B.oq_rms_norm_mx(x[start:])      # h = 2x doubled x in place; the norm of 2x is the same
+    assert torch.equal(codes[start:], codes1) and torch.equal(scales[start // 128:], scales1)
+    del x, kept, codes, scales, codes1, scales1
+    T, k, n = 1 << 19, 64, 8448
+    layer = B.oq_layer_create(k, n, 0, 4, 4, B.OQ_FLAG_MICROSCALED)
+    ac, at = B.oq_mx_quantize(torch.randn(T, k, generator=gen, device="cuda"), 4)
+    wc, wt = B.oq_mx_quantize(torch.randn(n, k, generator=gen, device="cuda"), 4)
+    y = B.oq_linear_mx(layer, ac, at, wc, wt, y_dtype=torch.bfloat16)
+    last = B.oq_linear_mx(layer, ac[-384:], at[-3:], wc, wt, y_dtype=torch.bfloat16)
+    assert torch.equal(y[-384:], last)
+    torch.cuda.synchronize()
+    B.oq_poll_error(layer)
+    del y
+    torch.cuda.empty_cache()
 
 
 def test_product_leaves_what_is_not_its_own(env):
