@@ -503,12 +503,13 @@ def _mx_outputs(codes, scales, rows: int, d: int, bits: int, device):
         raise ValueError("the operands must be CUDA tensors")
     cs, ss = _mx_shapes(rows, d, bits)
     if codes is None:
-        codes = torch.empty(cs, dtype=torch.uint8, device=device)
+        # (empty_strided takes two thirds of the time of empty)
+        codes = torch.empty_strided(cs, (cs[1], 1), dtype=torch.uint8, device=device)
         pc = codes.data_ptr()
     else:
         pc = _mx_ptr(codes, cs, device, "codes")
     if scales is None:
-        scales = torch.empty(ss, dtype=torch.uint8, device=device)
+        scales = torch.empty_strided(ss, (512 * ss[1], 512, 16, 4, 1), dtype=torch.uint8, device=device)
         ps = scales.data_ptr()
     else:
         ps = _mx_ptr(scales, ss, device, "scales")
@@ -542,7 +543,7 @@ def oq_mx_dequantize(codes, scales, d: int, bits: int, dtype=None, x=None):
     rows, device = codes.shape[0], codes.device
     _, _, pc, ps = _mx_outputs(codes, scales, rows, d, bits, device)
     if x is None:
-        x = torch.empty((rows, d), dtype=torch.float32 if dtype is None else dtype, device=device)
+        x = torch.empty_strided((rows, d), (d, 1), dtype=torch.float32 if dtype is None else dtype, device=device)
         px = x.data_ptr()
     else:
         px = _mx_rows(x, (rows, d), x.dtype if dtype is None else dtype, device, "x")
@@ -592,7 +593,8 @@ def oq_linear_mx(layer: Layer, codes, scales, Wcodes, Wscales, y=None, y_dtype=N
     pointers = (_mx_ptr(codes, cs, device, "codes"), _mx_ptr(scales, ss, device, "scales"), T,
                 _mx_ptr(Wcodes, ws, device, "Wcodes"), _mx_ptr(Wscales, wt, device, "Wscales"))
     if y is None:
-        y = _torch().empty((T, n), dtype=_torch().float32 if y_dtype is None else y_dtype, device=device)
+        torch = _torch()
+        y = torch.empty_strided((T, n), (n, 1), dtype=torch.float32 if y_dtype is None else y_dtype, device=device)
         py = y.data_ptr()
     else:
         py = _mx_rows(y, (T, n), y.dtype, device, "y")
