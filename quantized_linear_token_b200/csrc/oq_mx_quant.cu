@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(QT) mx_dequantize_kernel(const uint8_t* __rest
 //     its vectors of the next row into its own places in shared memory
 //     (cp.async) while it works on this one.  Loads are then in flight all the
 //     time without holding registers, and no barrier is about the data
-//     (32760 x 5120 bf16, residual kept: 236 us, 5.0 TB/s; 337 us with a CTA a row).
+//     (32760 x 5120 bf16, residual kept: 225 us, 5.2 TB/s; 337 us with a CTA a row).
 //   - few rows, or rows too long for two stages of shared memory: a CTA a row,
 //     straight from global memory.  NCH = 0 reads x and r a second time instead
 //     of keeping them (rows too long for the registers).
@@ -274,10 +274,13 @@ __device__ __forceinline__ float to_odd(double v) {
 }
 
 // 1 / sqrt(v) to 1e-13: an fp32 estimate and one Newton step
+__device__ __noinline__ double rsqrt64_far(double v) { return 1.0 / sqrt(v); }
 __device__ __forceinline__ double rsqrt64(double v) {
-  if (!(v > 1e-36 && v < 1e36)) return 1.0 / sqrt(v);
-  const double y = (double)rsqrtf((float)v);
-  return y * (1.5 - 0.5 * v * y * y);
+  if (!(v > 1e-36 && v < 1e36)) return rsqrt64_far(v);
+  float e;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(e) : "f"((float)v));   // 2 ulps: squared by the step
+  const double y = (double)e, h = 0.5 * v;
+  return y * fma(-h * y, y, 1.5);
 }
 
 // squares of one vector, added four roundings deep
@@ -288,40 +291,90 @@ __device__ __forceinline__ float sum_squares(const f32x2 (&v)[4]) {
   return lo + hi;
 }
 
-// the row's sum over its tpr threads (warps w0 .. of the CTA), in every one of them
-__device__ __forceinline__ double row_sum(double v, double* part, int tpr, int w0) {
+// the row's sum over its `warps` warps (at most 32, w0 the first), in every thread of them
+__device__ __forceinline__ double row_sum(double v, double* part, int warps, int w0) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if (tpr > 32) {
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  if (warps > 1) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
-    for (int w = 0; w < (tpr >> 5); ++w) v += part[w0 + w];
+    v = lane < warps ? part[w0 + lane] : 0.0;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+      if (o < warps) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (warps > 1) v = __shfl_sync(0xFFFFFFFFu, v, 0);
   }
   return v;
 }
 
+// codes and scale of one vector from w = n / scale
+template <int BITS>
+__device__ __forceinline__ void norm_store(const float (&w)[8], uint32_t code, int col, bool own, uint8_t* codes,
+                                           uint8_t* scales) {
+  uint32_t out[BITS / 4];
+  mx_element_codes<BITS>(w, code, out);
+  const uint32_t word = mx_scale_word(code);
+  if (own) {
+    uint8_t* q = codes + col * BITS / 8;
+    if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(q) = out[0];
+    else *reinterpret_cast<uint2*>(q) = make_uint2(out[0], out[1]);
+    if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(scales + (col >> 7) * MX_TILE_BYTES) = word;
+  }
+}
+
+// The vector's codes formed in fp64 from x and r; every lane of the warp takes part.
+template <typename T, int BITS>
+__device__ __forceinline__ void norm_vector_exact(const NormParams& p, const T* x, const T* r, int col, bool in, bool own,
+                                                  double rs64, uint8_t* codes, uint8_t* scales) {
+  float w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = 0.f;
+  if (in) {
+    float a[8], c[8], g[8];
+    f32x2 g2[4];
+    Vec8<T> q;
+    q.load(x);
+    q.get(a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = 0.f;
+    if (r) {
+      q.load(r);
+      q.get(c);
+    }
+    load_gain(p, col, g2);
+    unpack8(g2, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = to_odd(((double)a[i] + (double)c[i]) * rs64 * (double)g[i]);
+  }
+  const uint32_t code = mx_scale_code<BITS>(mx_block_max(w));
+  const float inv = mx_inverse_scale(code);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] *= inv;
+  norm_store<BITS>(w, code, col, own, codes, scales);
+}
+
 // One vector of a row: its codes, its scale and the kept residual.  Every lane
 // of the warp takes part; `in`: the vector holds elements; `own`: it lies in the
-// row's padded length.  x, r: where its elements can be read again.
-template <typename T, int BITS>
-__device__ __forceinline__ void norm_vector(const NormParams& p, const f32x2 (&v)[4], const T* x, const T* r, int col,
+// row's padded length.  True (in all lanes) where the warp met a border between
+// codes and norm_vector_exact has to follow; with REDO it has, from x and r,
+// before the kept residual is written, which may lie over them.
+template <typename T, int BITS, bool REDO>
+__device__ __forceinline__ bool norm_vector(const NormParams& p, const f32x2 (&v)[4], const T* x, const T* r, int col,
                                             bool in, bool own, f32x2 rs2, double rs64, T* r_out, uint8_t* codes,
                                             uint8_t* scales) {
-  f32x2 g[4];
+  f32x2 n[4];
   if (in) {
-    load_gain(p, col, g);
+    load_gain(p, col, n);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) g[i] = 0ull;
+    for (int i = 0; i < 4; ++i) n[i] = 0ull;
   }
   float w[8];
-  f32x2 n[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) n[i] = mul2(mul2(v[i], rs2), g[i]);
+  for (int i = 0; i < 4; ++i) n[i] = mul2(mul2(v[i], rs2), n[i]);
   unpack8(n, w);
-  const uint32_t top = mx_block_max(w);
-  uint32_t code = mx_scale_code<BITS>(top);
+  const uint32_t top = mx_block_max(w), code = mx_scale_code<BITS>(top);
   const f32x2 inv2 = pack2(mx_inverse_scale(code), mx_inverse_scale(code));
 #pragma unroll
   for (int i = 0; i < 4; ++i) n[i] = mul2(n[i], inv2);
@@ -334,48 +387,25 @@ __device__ __forceinline__ void norm_vector(const NormParams& p, const f32x2 (&v
   constexpr uint32_t OFFSET = (BITS == 4 ? 4u : 4u - 0x80000u) << SHIFT;
   uint32_t near = 0xFFFFFFFFu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t at = (__float_as_uint(w[i]) << SHIFT) + OFFSET;
-    near = min(near, BITS == 4 && fabsf(w[i]) < 0.2f ? near : at);
+  for (int i = 0; i < 8; i += 2) {
+    uint32_t at[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      at[j] = (__float_as_uint(w[i + j]) << SHIFT) + OFFSET;
+      if (BITS == 4 && fabsf(w[i + j]) < 0.2f) at[j] = 0xFFFFFFFFu;
+    }
+    near = __vimin3_u32(near, at[0], at[1]);
   }
   const bool border = in && top != 0u && (near <= (8u << SHIFT) || ((top + 4u) & 0x7FFFFFu) <= 8u);
-  if (__any_sync(0xFFFFFFFFu, border)) {
-    if (in) {
-      float a[8], c[8], gf[8];
-      unpack8(g, gf);
-      if (r) {   // the sum in fp64
-        Vec8<T> q;
-        q.load(x);
-        q.get(a);
-        q.load(r);
-        q.get(c);
-      } else {
-        unpack8(v, a);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = to_odd(((double)a[i] + (double)c[i]) * rs64 * (double)gf[i]);
-    }
-    code = mx_scale_code<BITS>(mx_block_max(w));
-    const float inv = mx_inverse_scale(code);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] *= inv;
-  }
-  uint32_t out[BITS / 4];
-  mx_element_codes<BITS>(w, code, out);
-  const uint32_t word = mx_scale_word(code);
+  const bool any = __any_sync(0xFFFFFFFFu, border);
+  if (REDO && any) norm_vector_exact<T, BITS>(p, x, r, col, in, own, rs64, codes, scales);
+  else norm_store<BITS>(w, code, col, own, codes, scales);
   if (in && r_out) {
     float f[8];
     unpack8(v, f);
     store8(r_out + col, f);
   }
-  if (own) {
-    uint8_t* q = codes + col * BITS / 8;
-    if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(q) = out[0];
-    else *reinterpret_cast<uint2*>(q) = make_uint2(out[0], out[1]);
-    if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(scales + (col / MX_COLS) * MX_TILE_BYTES) = word;
-  }
+  return any;
 }
 
 // scales of the rows behind the last one, to the end of its tile: code 0 (one
@@ -418,7 +448,7 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 1024 : 512) mx_norm_ker
     load((k * p.tpr + t) * 8, h[NCH ? k : 0]);
     total += (double)sum_squares(h[NCH ? k : 0]);
   }
-  const double rs64 = rsqrt64(row_sum(total, part, p.tpr, sub * (p.tpr >> 5)) * p.inv_d + (double)p.eps);
+  const double rs64 = rsqrt64(row_sum(total, part, p.tpr >> 5, sub * (p.tpr >> 5)) * p.inv_d + (double)p.eps);
   const f32x2 rs2 = pack2((float)rs64, (float)rs64);
 
   T* r_out = p.r_out ? static_cast<T*>(p.r_out) + base : nullptr;
@@ -428,7 +458,7 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 1024 : 512) mx_norm_ker
   for (int k = 0; k < (NCH ? NCH : steps); ++k) {
     const int col = (k * p.tpr + t) * 8;
     if constexpr (NCH == 0) load(col, h[0]);
-    norm_vector<T, BITS>(p, h[NCH ? k : 0], x + col, r ? r + col : r, col, live && col < p.d,
+    norm_vector<T, BITS, true>(p, h[NCH ? k : 0], x + col, r ? r + col : r, col, live && col < p.d,
                          live && col < p.col_tiles * MX_COLS, rs2, rs64, r_out, codes, scales);
   }
 }
@@ -453,29 +483,35 @@ __global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_con
   // a stage: the row's vectors of x, then of r; a thread uses its own places only
   const int plane = p.d * (int)sizeof(T), stage = rs_in ? 2 * plane : plane;
   unsigned char* mine = stage_mem + t * VB;
-  auto fetch = [&](int64_t row, int s) {
-    if (row < p.rows) {
+  const int cols = p.col_tiles * MX_COLS;
+  const int64_t step = (int64_t)p.row_ctas * p.d;
+  const T* x_next = xs + (int64_t)blockIdx.x * p.d;   // the next row to fetch
+  const T* r_next = rs_in ? rs_in + (int64_t)blockIdx.x * p.d : nullptr;
+  auto fetch = [&](bool there, unsigned char* to) {
+    if (there) {
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
         const int col = (k * tpr + t) * 8;
         if (col < p.d) {
-          unsigned char* q = mine + s * stage + k * tpr * VB;
-          const int64_t off = row * p.d + col;
+          unsigned char* q = to + k * tpr * VB;
 #pragma unroll
-          for (int b = 0; b < VB; b += 16) copy_async16(q + b, reinterpret_cast<const unsigned char*>(xs + off) + b);
+          for (int b = 0; b < VB; b += 16) copy_async16(q + b, reinterpret_cast<const unsigned char*>(x_next + col) + b);
           if (rs_in) {
 #pragma unroll
-            for (int b = 0; b < VB; b += 16) copy_async16(q + plane + b, reinterpret_cast<const unsigned char*>(rs_in + off) + b);
+            for (int b = 0; b < VB; b += 16) copy_async16(q + plane + b, reinterpret_cast<const unsigned char*>(r_next + col) + b);
           }
         }
       }
+      x_next += step;
+      if (rs_in) r_next += step;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int s = 0;
-  fetch(blockIdx.x, 0);
+  fetch(true, mine);
+  T* r_out = p.r_out ? static_cast<T*>(p.r_out) + (int64_t)blockIdx.x * p.d : nullptr;
   for (int64_t row = blockIdx.x; row < p.rows; row += p.row_ctas, s ^= 1) {
-    fetch(row + p.row_ctas, s ^ 1);
+    fetch(row + p.row_ctas < p.rows, mine + (s ^ 1) * stage);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     const unsigned char* q = mine + s * stage;
     f32x2 h[NCH][4];
@@ -491,18 +527,30 @@ __global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_con
       }
       total += (double)sum_squares(h[k]);
     }
-    const double rs64 = rsqrt64(row_sum(total, part[s], tpr, 0) * p.inv_d + (double)p.eps);
+    const double rs64 = rsqrt64(row_sum(total, part[s], tpr >> 5, 0) * p.inv_d + (double)p.eps);
     const f32x2 rs2 = pack2((float)rs64, (float)rs64);
-    T* r_out = p.r_out ? static_cast<T*>(p.r_out) + row * p.d : nullptr;
-    uint8_t* codes = p.codes + row * p.col_tiles * (MX_COLS * BITS / 8);
-    uint8_t* scales = p.scales + row / MX_ROWS * p.col_tiles * MX_TILE_BYTES + 4 * mx_tile_word((int)(row % MX_ROWS));
+    uint8_t* codes = p.codes + row * (cols * BITS / 8);
+    uint8_t* scales = p.scales + (row >> 7) * (p.col_tiles * MX_TILE_BYTES) + 4 * mx_tile_word((int)row & (MX_ROWS - 1));
+    uint32_t redo = 0u;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int col = (k * tpr + t) * 8;
-      const T* a = reinterpret_cast<const T*>(q + k * tpr * VB);
-      norm_vector<T, BITS>(p, h[k], a, rs_in ? reinterpret_cast<const T*>(q + k * tpr * VB + plane) : nullptr, col,
-                           col < p.d, col < p.col_tiles * MX_COLS, rs2, rs64, r_out, codes, scales);
+      if (norm_vector<T, BITS, false>(p, h[k], nullptr, nullptr, col, col < p.d, col < cols, rs2, rs64, r_out, codes, scales))
+        redo |= 1u << k;
     }
+    // the warp's vectors next to a border, again from the stage, which nothing
+    // has overwritten (apart from the loop above: its registers are the speed)
+    if (redo) {
+#pragma unroll 1
+      for (int k = 0; k < NCH; ++k) {
+        const int col = (k * tpr + t) * 8;
+        const T* a = reinterpret_cast<const T*>(q + k * tpr * VB);
+        if (redo >> k & 1u)
+          norm_vector_exact<T, BITS>(p, a, rs_in ? reinterpret_cast<const T*>(q + k * tpr * VB + plane) : nullptr, col,
+                                     col < p.d, col < cols, rs64, codes, scales);
+      }
+    }
+    if (r_out) r_out += step;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
