@@ -6,16 +6,25 @@
 // kind::mxf4 (K 64 an MMA), 8-bit activations kind::mxf8f6f4 (K 32), for which
 // TMA spreads the weights' 4-bit codes to 8-bit containers on the way.
 //
-// A pair's tile is 256 tokens (128 a CTA) by PN = N0 + N1 outputs in two parts
-// (MMAs of N0 and N1 columns), and a stage 128 bytes of every row: 256
-// elements of 4 bits or 128 of 8.  What bounds it is the feed: from L2 an SM
-// takes about 99 bytes a nanosecond, while a stage of the narrow 256 x 192 tile
-// wants 31 KB per 384 cycles of MMAs (145 bytes a nanosecond).  Wider tiles
-// reuse the activations' bytes: 256 x 448 wants 49 KB per 896 cycles, as much
-// as the feed gives.  448 columns and the scales' 64 fill tensor memory, so
-// there is one
-// accumulator; it is drained to registers and handed back before
-// the first store.  Narrower tiles are there for batches that would not fill the pairs.
+// A pair's tile is 256 tokens (128 a CTA) by PN outputs, in one part of up to
+// 256 columns or two, and a stage is 128 bytes of every row: 256 elements of 4
+// bits or 128 of 8.  What bounds a narrow tile is the feed: from L2 an SM takes
+// about 99 bytes a nanosecond (measured, copies alone), while a stage of 256 x
+// 192 wants 31 KB per 384 cycles of MMAs (145 bytes a nanosecond).  Wider tiles
+// reuse the activations' bytes: 256 x 448 wants 49 KB per 896 cycles, as much as
+// the feed gives.  448 columns and the scales' 64 fill tensor memory, so there is
+// one accumulator; it is drained to registers and handed back to the MMAs before
+// the first store.  Narrower tiles are for batches that would leave pairs idle.
+//
+// The other bound is the thread that issues: per stage and 10 scale copies it
+// has 896 cycles.  So the loop runs warp-uniform (1555 cycles a stage otherwise),
+// scale copies stand between MMAs that do not need them, and barriers are asked
+// for three stages at a time (about 230 cycles a check).  Measured: 881 cycles a
+// stage, and 4500 from one tile's last MMA to the next one's first.
+//
+// 32760 x 5120 -> 5120 with 4-bit activations: 310 us alone (5.5 PFLOP/s), 366 us
+// in a stream of such calls, where the 1000 W limit holds the clock at 1.46 GHz;
+// 4096 x 13824 -> 5120 with 8-bit activations: 200 and 238 us (2.9, 2.4).
 //
 // Scales: a 512-byte tile (128 rows x 4 blocks) is one tcgen05.cp into four
 // tensor-memory columns.  The pair's weight rows start at a multiple of 64, so
@@ -56,7 +65,7 @@ struct Cfg {
   static constexpr int SF_SET = 4 + 4 * RT;                       // scale columns of one column tile
   static constexpr int SF_SETS = 64 / SF_SET < 4 ? 64 / SF_SET : 4;   // sets used in turn
   static_assert(OS >= 4, "the checks look three stages ahead");
-  static_assert(N0 % 64 == 0 && N1 % 64 == 0 && N0 <= 256 && N1 > 0 && N1 <= N0 && PN <= (int)SF_COL && SF_SETS >= 3, "tile");
+  static_assert(N0 % 64 == 0 && N1 % 64 == 0 && N0 <= 256 && N1 <= N0 && PN <= (int)SF_COL && SF_SETS >= 3, "tile");
 };
 
 struct MxParams {
@@ -200,7 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const uint32_t bar = full0 + 8u * (uint32_t)s;
         tma_load_2d_pair(st, &p.a_map, kb * 128, m0, bar);
         tma_load_2d_pair(st + C::B0, &p.w0_map, kb * 128, n0 + (int32_t)rank * (N0 / 2), bar);
-        tma_load_2d_pair(st + C::B1, &p.w1_map, kb * 128, n0 + N0 + (int32_t)rank * (N1 / 2), bar);
+        if constexpr (N1 > 0) tma_load_2d_pair(st + C::B1, &p.w1_map, kb * 128, n0 + N0 + (int32_t)rank * (N1 / 2), bar);
         tma_load_3d_pair(st + C::SA_OFF, &p.sa_map, 0, kb * CT, m0 / MX_ROWS, bar);
         tma_load_3d_pair(st + C::SW_OFF, &p.sw_map, 0, kb * CT, n0 / MX_ROWS, bar);
         ++issued;
@@ -239,12 +248,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   } else if (warp == MMA_WARP && rank == 0) {
     // The whole warp runs this loop and one elected lane issues: with every
     // value uniform over the warp the descriptors stay in uniform registers,
-    // where the tensor instructions take them.  (From one lane's own registers
-    // each is moved there first: 1555 against 881 cycles a stage of 896 MMA
-    // cycles, 4-bit activations.)
+    // where the tensor instructions take them (from one lane's own registers
+    // each is moved there first).
     {
       constexpr uint32_t AF = F4 ? 1 : 0, BF = F4 ? 1 : 5;
-      constexpr uint32_t id0 = idesc_mx(2 * RM, N0, AF, BF), id1 = idesc_mx(2 * RM, N1, AF, BF);
+      constexpr uint32_t id0 = idesc_mx(2 * RM, N0, AF, BF), id1 = idesc_mx(2 * RM, N1 ? N1 : N0, AF, BF);
       constexpr int STRIDE = CT * MX_TILE_BYTES >> 4;
       // the stages' descriptors share their high words
       const uint64_t desc0 = smem_desc_sw128(smem_base), sdesc0 = smem_desc_scales(smem_base + C::SA_OFF);
@@ -296,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           h.cw = h.ca + SW;
           h.commit = 0u;
           h.commit_bar = &op_empty[s];
-          tc_half_stage_pair<F4, C::RT, STRIDE>(h);
+          tc_half_stage_pair<F4, (N1 > 0), C::RT, STRIDE>(h);
           // The next stage's operands.  A check costs this thread some 230
           // cycles (it queues behind the issued tensor work), and issuing a
           // stage takes about 45 a copy and 53 an MMA of the 896 that its MMAs
@@ -343,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           h.ca = s_lo + off1;
           h.cw = h.ca + SW;
           h.commit = 1u;
-          tc_half_stage_pair<F4, C::RT, STRIDE>(h);
+          tc_half_stage_pair<F4, (N1 > 0), C::RT, STRIDE>(h);
           s = s1;
           if (s1 == 0) n ^= 1u;
         }
@@ -385,7 +393,7 @@ oq_status launch(const MxGemmArgs& g, int sms, int device, cudaStream_t stream) 
   kp.nkb = (mx_col_tiles(g.K) + C::CT - 1) / C::CT;
   oq_status st = mx_encode_codes(&kp.a_map, g.a_codes, g.T, g.K, g.a_bits, false, RM, "the activation codes");
   if (st == OQ_OK) st = mx_encode_codes(&kp.w0_map, g.w_codes, g.N, g.K, 4, !F4, N0 / 2, "the weight codes");
-  if (st == OQ_OK) st = mx_encode_codes(&kp.w1_map, g.w_codes, g.N, g.K, 4, !F4, N1 / 2, "the weight codes");
+  if (st == OQ_OK && N1 > 0) st = mx_encode_codes(&kp.w1_map, g.w_codes, g.N, g.K, 4, !F4, N1 / 2, "the weight codes");
   if (st == OQ_OK) st = mx_encode_scales(&kp.sa_map, g.a_scales, g.T, g.K, 1, C::CT, "the activation scales");
   if (st == OQ_OK) st = mx_encode_scales(&kp.sw_map, g.w_scales, g.N, g.K, C::RT, C::CT, "the weight scales");
   if (st == OQ_OK) st = encode_y(&kp.y_map, g.y, g.T, g.N, g.y_bf16);
@@ -427,9 +435,9 @@ oq_status launch_width(const MxGemmArgs& g, cudaStream_t st) {
   switch (best) {
     case 448: return launch<F4, 256, 192>(g, sms, device, st);
     case 320: return launch<F4, 192, 128>(g, sms, device, st);
-    case 256: return launch<F4, 128, 128>(g, sms, device, st);
-    case 192: return launch<F4, 128, 64>(g, sms, device, st);
-    default: return launch<F4, 64, 64>(g, sms, device, st);
+    case 256: return launch<F4, 256, 0>(g, sms, device, st);
+    case 192: return launch<F4, 192, 0>(g, sms, device, st);
+    default: return launch<F4, 128, 0>(g, sms, device, st);
   }
 }
 

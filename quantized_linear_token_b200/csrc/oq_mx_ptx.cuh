@@ -122,8 +122,8 @@ __device__ __forceinline__ uint32_t mbar_test3(uint32_t b0, uint32_t b1, uint32_
   return r;
 }
 
-// Half a stage of a CTA pair: four MMAs (two K steps of the tile's two column
-// parts) with the scale copies of the NEXT half between them, so that no MMA
+// Half a stage of a CTA pair: two K steps of the tile's column parts (one, or
+// two with TWO: two or four MMAs) with the scale copies of the NEXT half between them, so that no MMA
 // waits for a copy just issued.  `commit` reports everything issued so far to
 // `commit_bar` in both CTAs.
 //   a, b0, b1     low descriptor words of the operand tiles at the first K step (+2: the second)
@@ -138,7 +138,7 @@ struct MxHalf {
   uint64_t* commit_bar;
   uint32_t commit;
 };
-template <bool F4, int RT, int STRIDE>
+template <bool F4, bool TWO, int RT, int STRIDE>
 __device__ __forceinline__ void tc_half_stage_pair(const MxHalf& h) {
 #define OQ_DESC(R, LO, OFF, HI) "add.u32 lo, " LO ", " OFF ";\n\tmov.b64 " R ", {lo, " HI "};\n\t"
 #define OQ_MMA(KIND, VEC, D, ID, W, P)                                                                      \
@@ -147,7 +147,7 @@ __device__ __forceinline__ void tc_half_stage_pair(const MxHalf& h) {
 #define OQ_CP(P, COL, LO, OFF)                                                                              \
   "add.u32 t, %15, " COL ";\n\t" OQ_DESC("ds", LO, OFF, "%18")                                              \
   "@" P " tcgen05.cp.cta_group::2.32x128b.warpx4 [t], ds;\n\t"
-#define OQ_HALF(KIND, VEC)                                                                                  \
+#define OQ_HALF(KIND, VEC, PART1)                                                                              \
   "{\n\t.reg .pred pl, pa, pt, pc, c0, c1, c2, c3, c4;\n\t.reg .b64 da, db, ds;\n\t.reg .b32 lo, t;\n\t"    \
   "setp.ne.b32 pl, %0, 0;\n\tsetp.ne.b32 pa, %14, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"                                  \
   "setp.ne.and.b32 pc, %21, 0, pl;\n\tsetp.ne.and.b32 c0, %19, 0, pl;\n\tsetp.gt.and.s32 c1, %23, 0, c0;\n\t"                \
@@ -155,12 +155,13 @@ __device__ __forceinline__ void tc_half_stage_pair(const MxHalf& h) {
   OQ_DESC("da", "%3", "0", "%6") OQ_DESC("db", "%4", "0", "%6") OQ_MMA(KIND, VEC, "%1", "%7", "%12", "pa")  \
   OQ_CP("c0", "0", "%16", "0")                                                                              \
   OQ_DESC("da", "%3", "2", "%6") OQ_DESC("db", "%4", "2", "%6") OQ_MMA(KIND, VEC, "%1", "%8", "%12", "pt")  \
-  OQ_CP("c1", "4", "%17", "0") OQ_CP("c2", "8", "%17", "%24")                                               \
-  OQ_DESC("da", "%3", "0", "%6") OQ_DESC("db", "%5", "0", "%6") OQ_MMA(KIND, VEC, "%2", "%9", "%13", "pa")  \
-  OQ_CP("c3", "12", "%17", "%25") OQ_CP("c4", "16", "%17", "%26")                                           \
-  OQ_DESC("da", "%3", "2", "%6") OQ_DESC("db", "%5", "2", "%6") OQ_MMA(KIND, VEC, "%2", "%10", "%13", "pt") \
+  OQ_CP("c1", "4", "%17", "0") OQ_CP("c2", "8", "%17", "%24") PART1                                         \
   "@pc tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%20], %22;\n\t" \
   "}"
+#define OQ_PART1(KIND, VEC)                                                                                 \
+  OQ_DESC("da", "%3", "0", "%6") OQ_DESC("db", "%5", "0", "%6") OQ_MMA(KIND, VEC, "%2", "%9", "%13", "pa")  \
+  OQ_CP("c3", "12", "%17", "%25") OQ_CP("c4", "16", "%17", "%26")                                           \
+  OQ_DESC("da", "%3", "2", "%6") OQ_DESC("db", "%5", "2", "%6") OQ_MMA(KIND, VEC, "%2", "%10", "%13", "pt")
 #define OQ_ARGS                                                                                             \
   :                                                                                                         \
   : "r"(h.lead), "r"(h.d0), "r"(h.d1), "r"(h.a), "r"(h.b0), "r"(h.b1), "r"(h.hi), "r"(h.i0a), "r"(h.i0b), "r"(h.i1a),     \
@@ -169,9 +170,13 @@ __device__ __forceinline__ void tc_half_stage_pair(const MxHalf& h) {
     "h"((uint16_t)0x3), "n"(RT), "n"(STRIDE), "n"(2 * STRIDE),            \
     "n"(3 * STRIDE)                                                                                         \
   : "memory"
-  if constexpr (F4) asm volatile(OQ_HALF("mxf4", "2X") OQ_ARGS);
-  else asm volatile(OQ_HALF("mxf8f6f4", "1X") OQ_ARGS);
+  static_assert(TWO || RT <= 2, "one part's copies follow its two MMAs");
+  if constexpr (F4 && TWO) asm volatile(OQ_HALF("mxf4", "2X", OQ_PART1("mxf4", "2X")) OQ_ARGS);
+  else if constexpr (F4) asm volatile(OQ_HALF("mxf4", "2X", "") OQ_ARGS);
+  else if constexpr (TWO) asm volatile(OQ_HALF("mxf8f6f4", "1X", OQ_PART1("mxf8f6f4", "1X")) OQ_ARGS);
+  else asm volatile(OQ_HALF("mxf8f6f4", "1X", "") OQ_ARGS);
 #undef OQ_ARGS
+#undef OQ_PART1
 #undef OQ_HALF
 #undef OQ_CP
 #undef OQ_MMA
