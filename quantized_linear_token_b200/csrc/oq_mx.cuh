@@ -8,6 +8,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 
 #include <atomic>
 #include <cstdint>
@@ -196,6 +197,35 @@ __device__ __forceinline__ uint32_t mx_scale_word(uint32_t code) {
 // per device): both cost a small call as much as its other host work.
 int mx_sm_count(int* device);
 oq_status mx_allow_smem(const void* kernel, size_t bytes, int device, std::atomic<uint64_t>* done);
+
+// The microscaled kernels follow one another in a stream (norm, product, norm),
+// so each is launched as a programmatic dependent: it may be set up on the SMs
+// while the kernel before it ends.  It reads and writes global memory only after
+// dependency_wait, which returns when that kernel is complete, and lets the next
+// one begin its set-up from there.  (After a kernel that announces nothing the
+// launch is an ordinary one.)
+__device__ __forceinline__ void dependency_wait() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+// launch with that attribute; cluster: CTAs of a cluster along x, or 0 for the kernel's own
+template <typename P>
+cudaError_t mx_launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, const P& p) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 // launches (oq_mx_quant.cu, oq_mx_gemm.cu, oq_mx_small.cu); arguments checked by the entry points
 oq_status mx_quantize_launch(const void* x, int x_dtype, int64_t rows, int d, int bits, uint8_t* codes,

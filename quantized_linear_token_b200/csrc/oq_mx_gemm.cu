@@ -186,6 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   cluster_sync_all();   // barriers of both CTAs initialised before any remote arrival or load
   tc_fence_after();
+  dependency_wait();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const uint32_t smem_base = smem_u32(smem);
   const int total = my_tiles * nkb;
@@ -405,8 +406,7 @@ oq_status launch(const MxGemmArgs& g, int sms, int device, cudaStream_t stream) 
   const int64_t grid = std::min<int64_t>(2 * kp.tiles, (int64_t)(sms & ~1));
   // stage counters are 32-bit
   if (((kp.tiles + grid / 2 - 1) / (grid / 2)) * (int64_t)kp.nkb >= (int64_t)1 << 31) return OQ_ERR_UNSUPPORTED;
-  mx_gemm_kernel<F4, N0, N1><<<(unsigned)grid, NTHREADS, C::SMEM, stream>>>(kp);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = mx_launch(mx_gemm_kernel<F4, N0, N1>, dim3((unsigned)grid), NTHREADS, C::SMEM, 0, stream, kp);
   if (e != cudaSuccess) {
     set_error(std::string("microscaled product launch: ") + cudaGetErrorString(e));
     return OQ_ERR_CUDA;

@@ -12,8 +12,7 @@
 namespace oq {
 namespace {
 
-oq_status launch_status(const char* what) {
-  const cudaError_t e = cudaGetLastError();
+oq_status launch_status(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return OQ_OK;
   set_error(std::string(what) + " launch: " + cudaGetErrorString(e));
   return OQ_ERR_CUDA;
@@ -46,13 +45,25 @@ __device__ __forceinline__ TileSpan tile_span(int64_t rows, int col_tiles) {
   return t;
 }
 
+// quantise: x -> codes, scales; read back: codes, scales -> x
+struct QuantParams {
+  void* x;
+  int64_t rows;
+  int d, col_tiles;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+
 template <typename T, int BITS>
-__global__ void __launch_bounds__(QT) mx_quantize_kernel(const T* __restrict__ x, int64_t rows, int d, int col_tiles,
-                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+__global__ void __launch_bounds__(QT) mx_quantize_kernel(const __grid_constant__ QuantParams p) {
   __shared__ uint32_t tile[MX_TILE_BYTES / 4];
-  const TileSpan t = tile_span(rows, col_tiles);
+  const int d = p.d, col_tiles = p.col_tiles;
+  uint8_t* __restrict__ const codes = p.codes;
+  uint8_t* __restrict__ const scales = p.scales;
+  const TileSpan t = tile_span(p.rows, col_tiles);
   const bool in_cols = t.col < d;
-  const T* src = x + t.row0 * d + t.col;
+  const T* __restrict__ const src = static_cast<const T*>(p.x) + t.row0 * d + t.col;
+  dependency_wait();
   Vec8<T> in[QROWS];
 #pragma unroll
   for (int i = 0; i < QROWS; ++i) {
@@ -166,10 +177,12 @@ __device__ __forceinline__ void mx_values(const uint32_t (&in)[BITS / 4], uint32
 }
 
 template <typename T, int BITS>
-__global__ void __launch_bounds__(QT) mx_dequantize_kernel(const uint8_t* __restrict__ codes,
-                                                           const uint8_t* __restrict__ scales, int64_t rows, int d,
-                                                           int col_tiles, T* __restrict__ x) {
-  const TileSpan t = tile_span(rows, col_tiles);
+__global__ void __launch_bounds__(QT) mx_dequantize_kernel(const __grid_constant__ QuantParams p) {
+  const int d = p.d, col_tiles = p.col_tiles;
+  const uint8_t* __restrict__ const codes = p.codes;
+  const uint8_t* __restrict__ const scales = p.scales;
+  const TileSpan t = tile_span(p.rows, col_tiles);
+  dependency_wait();
   if (t.col >= d) return;
   const int pitch = col_tiles * (MX_COLS * BITS / 8);
   const uint8_t* src = codes + t.row0 * pitch + t.col * BITS / 8;
@@ -188,7 +201,7 @@ __global__ void __launch_bounds__(QT) mx_dequantize_kernel(const uint8_t* __rest
     }
     sc[i] = tile[4 * mx_tile_word(t.sub + i * QSTEP)];
   }
-  T* dst = x + t.row0 * d + t.col;
+  T* __restrict__ const dst = static_cast<T*>(p.x) + t.row0 * d + t.col;
 #pragma unroll
   for (int i = 0; i < QROWS; ++i) {
     if (i * QSTEP >= t.live) break;
@@ -421,6 +434,7 @@ __device__ __forceinline__ void norm_clear_padding(const NormParams& p) {
 template <typename T, int BITS, int NCH>
 __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 1024 : 512) mx_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ double part[32];
+  dependency_wait();
   if ((int)blockIdx.x >= p.row_ctas) {
     norm_clear_padding(p);
     return;
@@ -472,6 +486,7 @@ template <typename T, int BITS, int NCH>
 __global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_constant__ NormParams p) {
   __shared__ double part[2][16];
   extern __shared__ __align__(16) unsigned char stage_mem[];
+  dependency_wait();
   if ((int)blockIdx.x >= p.row_ctas) {
     norm_clear_padding(p);
     return;
@@ -564,8 +579,8 @@ oq_status norm_stream_launch(NormParams& p, int threads, int sms, int device, si
   // CTAs an SM holds: 64 registers a thread, 228 KB of shared memory with 1 KB a CTA of the system's and 256 bytes of sums
   const int resident = std::max(1, std::min(1024 / threads, (int)(228 * 1024 / (smem + 1024 + 256))));
   p.row_ctas = (int)std::min<int64_t>(p.rows, (int64_t)sms * resident);
-  mx_norm_stream_kernel<T, BITS, NCH><<<(unsigned)p.row_ctas + (p.rows % MX_ROWS ? 1u : 0u), threads, smem, st>>>(p);
-  return launch_status("oq_rms_norm_mx");
+  const unsigned grid = (unsigned)p.row_ctas + (p.rows % MX_ROWS ? 1u : 0u);
+  return launch_status(mx_launch(mx_norm_stream_kernel<T, BITS, NCH>, dim3(grid), threads, smem, 0, st, p), "oq_rms_norm_mx");
 }
 
 template <typename T, int BITS>
@@ -595,52 +610,38 @@ oq_status norm_launch(const NormParams& p0, cudaStream_t st) {
   const int64_t grid = (p.rows + rpb - 1) / rpb;
   p.row_ctas = (int)grid;
   const unsigned ctas = (unsigned)grid + (p.rows % MX_ROWS ? 1u : 0u);
-  switch (nch) {
-    case 1: mx_norm_kernel<T, BITS, 1><<<ctas, threads, 0, st>>>(p); break;
-    case 2: mx_norm_kernel<T, BITS, 2><<<ctas, threads, 0, st>>>(p); break;
-    case 4: mx_norm_kernel<T, BITS, 4><<<ctas, threads, 0, st>>>(p); break;
-    case 8: mx_norm_kernel<T, BITS, 8><<<ctas, threads, 0, st>>>(p); break;
-    default: mx_norm_kernel<T, BITS, 0><<<ctas, threads, 0, st>>>(p);
-  }
-  return launch_status("oq_rms_norm_mx");
+  auto kernel = nch == 1   ? mx_norm_kernel<T, BITS, 1>
+                : nch == 2 ? mx_norm_kernel<T, BITS, 2>
+                : nch == 4 ? mx_norm_kernel<T, BITS, 4>
+                : nch == 8 ? mx_norm_kernel<T, BITS, 8>
+                           : mx_norm_kernel<T, BITS, 0>;
+  return launch_status(mx_launch(kernel, dim3(ctas), threads, 0, 0, st, p), "oq_rms_norm_mx");
 }
 
 }  // namespace
 
 oq_status mx_quantize_launch(const void* x, int x_dtype, int64_t rows, int d, int bits, uint8_t* codes,
                              uint8_t* scales, void* stream) {
-  const int ct = mx_col_tiles(d);
-  const int64_t grid = mx_row_tiles(rows) * ct;
+  const QuantParams p{const_cast<void*>(x), rows, d, mx_col_tiles(d), codes, scales};
+  const int64_t grid = mx_row_tiles(rows) * p.col_tiles;
   if (grid > 0x7FFFFFFF) return OQ_ERR_UNSUPPORTED;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (x_dtype == OQ_DTYPE_BF16) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x);
-    if (bits == 4) mx_quantize_kernel<__nv_bfloat16, 4><<<(unsigned)grid, QT, 0, st>>>(p, rows, d, ct, codes, scales);
-    else mx_quantize_kernel<__nv_bfloat16, 8><<<(unsigned)grid, QT, 0, st>>>(p, rows, d, ct, codes, scales);
-  } else {
-    const float* p = static_cast<const float*>(x);
-    if (bits == 4) mx_quantize_kernel<float, 4><<<(unsigned)grid, QT, 0, st>>>(p, rows, d, ct, codes, scales);
-    else mx_quantize_kernel<float, 8><<<(unsigned)grid, QT, 0, st>>>(p, rows, d, ct, codes, scales);
-  }
-  return launch_status("oq_mx_quantize");
+  const bool bf16 = x_dtype == OQ_DTYPE_BF16;
+  auto kernel = bf16 ? (bits == 4 ? mx_quantize_kernel<__nv_bfloat16, 4> : mx_quantize_kernel<__nv_bfloat16, 8>)
+                     : (bits == 4 ? mx_quantize_kernel<float, 4> : mx_quantize_kernel<float, 8>);
+  return launch_status(mx_launch(kernel, dim3((unsigned)grid), QT, 0, 0, static_cast<cudaStream_t>(stream), p),
+                       "oq_mx_quantize");
 }
 
 oq_status mx_dequantize_launch(const uint8_t* codes, const uint8_t* scales, int64_t rows, int d, int bits, void* x,
                                int x_dtype, void* stream) {
-  const int ct = mx_col_tiles(d);
-  const int64_t grid = mx_row_tiles(rows) * ct;
+  const QuantParams p{x, rows, d, mx_col_tiles(d), const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales)};
+  const int64_t grid = mx_row_tiles(rows) * p.col_tiles;
   if (grid > 0x7FFFFFFF) return OQ_ERR_UNSUPPORTED;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (x_dtype == OQ_DTYPE_BF16) {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(x);
-    if (bits == 4) mx_dequantize_kernel<__nv_bfloat16, 4><<<(unsigned)grid, QT, 0, st>>>(codes, scales, rows, d, ct, p);
-    else mx_dequantize_kernel<__nv_bfloat16, 8><<<(unsigned)grid, QT, 0, st>>>(codes, scales, rows, d, ct, p);
-  } else {
-    float* p = static_cast<float*>(x);
-    if (bits == 4) mx_dequantize_kernel<float, 4><<<(unsigned)grid, QT, 0, st>>>(codes, scales, rows, d, ct, p);
-    else mx_dequantize_kernel<float, 8><<<(unsigned)grid, QT, 0, st>>>(codes, scales, rows, d, ct, p);
-  }
-  return launch_status("oq_mx_dequantize");
+  const bool bf16 = x_dtype == OQ_DTYPE_BF16;
+  auto kernel = bf16 ? (bits == 4 ? mx_dequantize_kernel<__nv_bfloat16, 4> : mx_dequantize_kernel<__nv_bfloat16, 8>)
+                     : (bits == 4 ? mx_dequantize_kernel<float, 4> : mx_dequantize_kernel<float, 8>);
+  return launch_status(mx_launch(kernel, dim3((unsigned)grid), QT, 0, 0, static_cast<cudaStream_t>(stream), p),
+                       "oq_mx_dequantize");
 }
 
 oq_status mx_norm_launch(const MxNormArgs& a, void* stream) {

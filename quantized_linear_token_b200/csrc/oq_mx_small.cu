@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
     mbar_init(acc_full, 1);
     mbar_init(received, 1);
     fence_mbar_init();
+    dependency_wait();
     for (int i = 0; i < count && i < 2; ++i) fetch(i);
   }
   if (warp == MMA_WARP) {
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  dependency_wait();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const uint32_t smem_base = smem_u32(smem);
 
@@ -322,22 +324,8 @@ oq_status launch(const MxGemmArgs& g, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
   if ((st = mx_allow_smem(reinterpret_cast<const void*>(mx_small_kernel<F4, BN>), C::SMEM, device, &smem_set)) != OQ_OK)
     return st;
-  cudaError_t e;
-  {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(m_tiles * kp.split), (unsigned)t_tiles, 1);
-    cfg.blockDim = dim3(NTHREADS, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)kp.split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mx_small_kernel<F4, BN>, kp);
-  }
+  const cudaError_t e = mx_launch(mx_small_kernel<F4, BN>, dim3((unsigned)(m_tiles * kp.split), (unsigned)t_tiles), NTHREADS,
+                                  C::SMEM, kp.split, stream, kp);
   if (e != cudaSuccess) {
     set_error(std::string("microscaled small-batch product launch: ") + cudaGetErrorString(e));
     return OQ_ERR_CUDA;
