@@ -20,11 +20,11 @@
 // has 896 cycles.  So the loop runs warp-uniform (1555 cycles a stage otherwise),
 // scale copies stand between MMAs that do not need them, and barriers are asked
 // for three stages at a time (about 230 cycles a check).  Measured: 881 cycles a
-// stage, and 4500 from one tile's last MMA to the next one's first.
+// stage, and 2100 from one tile's last MMA issued to the next one's first.
 //
-// 32760 x 5120 -> 5120 with 4-bit activations: 310 us alone (5.5 PFLOP/s), 366 us
+// 32760 x 5120 -> 5120 with 4-bit activations: 288 us alone (6.0 PFLOP/s), 333 us
 // in a stream of such calls, where the 1000 W limit holds the clock at 1.46 GHz;
-// 4096 x 13824 -> 5120 with 8-bit activations: 200 and 238 us (2.9, 2.4).
+// 4096 x 13824 -> 5120 with 8-bit activations: 195 and 229 us (3.0, 2.5).
 //
 // Scales: a 512-byte tile (128 rows x 4 blocks) is one tcgen05.cp into four
 // tensor-memory columns.  The pair's weight rows start at a multiple of 64, so
@@ -100,17 +100,15 @@ __device__ __forceinline__ void store_box(const MxParams& p, const uint32_t* w, 
 template <int PN>
 __device__ __forceinline__ void drain_bf16(const MxParams& p, uint32_t tmem_q, int e, int lane, int n0, int32_t row0,
                                            unsigned char* box, uint32_t empty_bar) {
-  constexpr int NC = (PN / 32 + 1) / 2;
+  constexpr int NC = PN / 64;
   uint32_t v[NC][16];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    if ((2 * c + e) * 32 < PN) {
-      uint32_t w[32];
-      tmem_ld_32x32b_x32(tmem_q + (uint32_t)((2 * c + e) * 32), w);
-      tmem_wait_ld();
+    uint32_t w[32];
+    tmem_ld_32x32b_x32(tmem_q + (uint32_t)((2 * c + e) * 32), w);
+    tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[c][j] = pack_bf16x2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
-    }
+    for (int j = 0; j < 16; ++j) v[c][j] = pack_bf16x2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
   }
   tc_fence_before();
   __syncwarp();
@@ -118,20 +116,19 @@ __device__ __forceinline__ void drain_bf16(const MxParams& p, uint32_t tmem_q, i
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int col = n0 + (2 * c + e) * 32;
-    if ((2 * c + e) * 32 < PN && col < p.N) store_box(p, v[c], lane, col, row0, box);
+    if (col < p.N) store_box(p, v[c], lane, col, row0, box);
   }
 }
 
 template <int PN>
 __device__ __forceinline__ void drain_f32(const MxParams& p, uint32_t tmem_q, int e, int lane, int n0, int32_t row0,
                                           unsigned char* box, uint32_t empty_bar) {
-  constexpr int NC = (PN / 32 + 1) / 2, STEP = 3;
+  constexpr int NC = PN / 64, STEP = 3;
 #pragma unroll
   for (int c0 = 0; c0 < NC; c0 += STEP) {
     uint32_t v[STEP][32];
 #pragma unroll
-    for (int c = 0; c < STEP; ++c)
-      if (c0 + c < NC && (2 * (c0 + c) + e) * 32 < PN) tmem_ld_32x32b_x32(tmem_q + (uint32_t)((2 * (c0 + c) + e) * 32), v[c]);
+    for (int c = 0; c < STEP && c0 + c < NC; ++c) tmem_ld_32x32b_x32(tmem_q + (uint32_t)((2 * (c0 + c) + e) * 32), v[c]);
     tmem_wait_ld();
     if (c0 + STEP >= NC) {
       tc_fence_before();
@@ -139,12 +136,10 @@ __device__ __forceinline__ void drain_f32(const MxParams& p, uint32_t tmem_q, in
       if (lane == 0) mbar_arrive_tmem(empty_bar);
     }
 #pragma unroll
-    for (int c = 0; c < STEP; ++c) {
+    for (int c = 0; c < STEP && c0 + c < NC; ++c) {
       const int col = n0 + (2 * (c0 + c) + e) * 32;
-      if (c0 + c < NC && (2 * (c0 + c) + e) * 32 < PN && col < p.N) {
-        store_box(p, v[c], lane, col, row0, box);
-        if (col + 16 < p.N) store_box(p, v[c] + 16, lane, col + 16, row0, box);
-      }
+      if (col < p.N) store_box(p, v[c], lane, col, row0, box);
+      if (col + 16 < p.N) store_box(p, v[c] + 16, lane, col + 16, row0, box);
     }
   }
 }
