@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "oq_internal.h"
 #include "oq_mx.cuh"
@@ -21,13 +22,15 @@ oq_status launch_status(cudaError_t e, const char* what) {
 // ------------------------------------------------------------------ quantise
 // A CTA owns one scale tile: 128 rows x 128 elements.  Sixteen lanes take a
 // row of the tile, eight elements each, so a warp's loads cover two rows'
-// 256-byte (bf16) segments; a thread loads its eight rows' vectors before it
-// uses the first.  The tile's 512 scale bytes are gathered in shared memory
+// 256-byte (bf16) segments; a thread loads its rows' vectors before it uses the
+// first.  The tile's 512 scale bytes are gathered in shared memory
 // and leave as whole sectors.  Rows past the end read as zeros and get scale
 // code 0; columns past d get zero codes and scale code 0.
-constexpr int QT = 256;
-constexpr int QSTEP = QT / 16;                // rows between a thread's rows
-constexpr int QROWS = MX_ROWS / QSTEP;        // rows per thread
+//
+// 256 threads, or 512 with half as many rows each: where there are only a few
+// tiles for an SM (1001 x 2016 in 8 bits 2.8 -> 2.4 us), and for bf16 rows in 8
+// bits (32760 x 5120 87 -> 81 us; in 4 bits 78 -> 81, fp32 32 -> 34 at 8192 x 5120).
+constexpr int QT_WIDE = 512, QT_DEEP = 256;
 
 // the tile of this CTA: row tile, column tile, and how many of this thread's rows exist
 struct TileSpan {
@@ -54,8 +57,9 @@ struct QuantParams {
   uint8_t* scales;
 };
 
-template <typename T, int BITS>
+template <typename T, int BITS, int QT>
 __global__ void __launch_bounds__(QT) mx_quantize_kernel(const __grid_constant__ QuantParams p) {
+  constexpr int QSTEP = QT / 16, QROWS = MX_ROWS / QSTEP;   // rows between a thread's rows, and their number
   __shared__ uint32_t tile[MX_TILE_BYTES / 4];
   const int d = p.d, col_tiles = p.col_tiles;
   uint8_t* __restrict__ const codes = p.codes;
@@ -176,8 +180,9 @@ __device__ __forceinline__ void mx_values(const uint32_t (&in)[BITS / 4], uint32
   }
 }
 
-template <typename T, int BITS>
+template <typename T, int BITS, int QT>
 __global__ void __launch_bounds__(QT) mx_dequantize_kernel(const __grid_constant__ QuantParams p) {
+  constexpr int QSTEP = QT / 16, QROWS = MX_ROWS / QSTEP;
   const int d = p.d, col_tiles = p.col_tiles;
   const uint8_t* __restrict__ const codes = p.codes;
   const uint8_t* __restrict__ const scales = p.scales;
@@ -618,6 +623,11 @@ oq_status norm_launch(const NormParams& p0, cudaStream_t st) {
   return launch_status(mx_launch(kernel, dim3(ctas), threads, 0, 0, st, p), "oq_rms_norm_mx");
 }
 
+bool few_tiles(int64_t tiles) {
+  int device = 0;
+  return tiles <= 4 * mx_sm_count(&device);
+}
+
 }  // namespace
 
 oq_status mx_quantize_launch(const void* x, int x_dtype, int64_t rows, int d, int bits, uint8_t* codes,
@@ -625,10 +635,14 @@ oq_status mx_quantize_launch(const void* x, int x_dtype, int64_t rows, int d, in
   const QuantParams p{const_cast<void*>(x), rows, d, mx_col_tiles(d), codes, scales};
   const int64_t grid = mx_row_tiles(rows) * p.col_tiles;
   if (grid > 0x7FFFFFFF) return OQ_ERR_UNSUPPORTED;
-  const bool bf16 = x_dtype == OQ_DTYPE_BF16;
-  auto kernel = bf16 ? (bits == 4 ? mx_quantize_kernel<__nv_bfloat16, 4> : mx_quantize_kernel<__nv_bfloat16, 8>)
-                     : (bits == 4 ? mx_quantize_kernel<float, 4> : mx_quantize_kernel<float, 8>);
-  return launch_status(mx_launch(kernel, dim3((unsigned)grid), QT, 0, 0, static_cast<cudaStream_t>(stream), p),
+  const bool bf16 = x_dtype == OQ_DTYPE_BF16, wide = few_tiles(grid) || (bf16 && bits == 8);
+  auto pick = [&](auto threads) {
+    constexpr int QT = decltype(threads)::value;
+    return bf16 ? (bits == 4 ? mx_quantize_kernel<__nv_bfloat16, 4, QT> : mx_quantize_kernel<__nv_bfloat16, 8, QT>)
+                : (bits == 4 ? mx_quantize_kernel<float, 4, QT> : mx_quantize_kernel<float, 8, QT>);
+  };
+  auto kernel = wide ? pick(std::integral_constant<int, QT_WIDE>()) : pick(std::integral_constant<int, QT_DEEP>());
+  return launch_status(mx_launch(kernel, dim3((unsigned)grid), wide ? QT_WIDE : QT_DEEP, 0, 0, static_cast<cudaStream_t>(stream), p),
                        "oq_mx_quantize");
 }
 
@@ -637,10 +651,14 @@ oq_status mx_dequantize_launch(const uint8_t* codes, const uint8_t* scales, int6
   const QuantParams p{x, rows, d, mx_col_tiles(d), const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales)};
   const int64_t grid = mx_row_tiles(rows) * p.col_tiles;
   if (grid > 0x7FFFFFFF) return OQ_ERR_UNSUPPORTED;
-  const bool bf16 = x_dtype == OQ_DTYPE_BF16;
-  auto kernel = bf16 ? (bits == 4 ? mx_dequantize_kernel<__nv_bfloat16, 4> : mx_dequantize_kernel<__nv_bfloat16, 8>)
-                     : (bits == 4 ? mx_dequantize_kernel<float, 4> : mx_dequantize_kernel<float, 8>);
-  return launch_status(mx_launch(kernel, dim3((unsigned)grid), QT, 0, 0, static_cast<cudaStream_t>(stream), p),
+  const bool bf16 = x_dtype == OQ_DTYPE_BF16, wide = few_tiles(grid);
+  auto pick = [&](auto threads) {
+    constexpr int QT = decltype(threads)::value;
+    return bf16 ? (bits == 4 ? mx_dequantize_kernel<__nv_bfloat16, 4, QT> : mx_dequantize_kernel<__nv_bfloat16, 8, QT>)
+                : (bits == 4 ? mx_dequantize_kernel<float, 4, QT> : mx_dequantize_kernel<float, 8, QT>);
+  };
+  auto kernel = wide ? pick(std::integral_constant<int, QT_WIDE>()) : pick(std::integral_constant<int, QT_DEEP>());
+  return launch_status(mx_launch(kernel, dim3((unsigned)grid), wide ? QT_WIDE : QT_DEEP, 0, 0, static_cast<cudaStream_t>(stream), p),
                        "oq_mx_dequantize");
 }
 
