@@ -69,21 +69,29 @@ __global__ void __launch_bounds__(QT) mx_quantize_kernel(const __grid_constant__
   const T* __restrict__ const src = static_cast<const T*>(p.x) + t.row0 * d + t.col;
   dependency_wait();
   Vec8<T> in[QROWS];
+  if (t.live >= MX_ROWS - t.sub && (t.ct + 1) * MX_COLS <= d) {   // a whole tile
 #pragma unroll
-  for (int i = 0; i < QROWS; ++i) {
-    if (in_cols && i * QSTEP < t.live) in[i].load(src + (int64_t)i * QSTEP * d);
-    else in[i].zero();
+    for (int i = 0; i < QROWS; ++i) in[i].load(src + (int64_t)i * QSTEP * d);
+  } else {
+#pragma unroll
+    for (int i = 0; i < QROWS; ++i) {
+      if (in_cols && i * QSTEP < t.live) in[i].load(src + (int64_t)i * QSTEP * d);
+      else in[i].zero();
+    }
   }
   const int pitch = col_tiles * (MX_COLS * BITS / 8);
   uint8_t* dst = codes + t.row0 * pitch + t.col * BITS / 8;
 #pragma unroll
   for (int i = 0; i < QROWS; ++i) {
+    f32x2 v2[4];
     float v[8];
-    in[i].get(v);
+    in[i].get(v2);
+    unpack8(v2, v);
     const uint32_t code = mx_scale_code<BITS>(mx_block_max(v));
-    const float inv = mx_inverse_scale(code);
+    const f32x2 inv = pack2(mx_inverse_scale(code), mx_inverse_scale(code));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= inv;
+    for (int k = 0; k < 4; ++k) v2[k] = mul2(v2[k], inv);
+    unpack8(v2, v);
     uint32_t out[BITS / 4];
     mx_element_codes<BITS>(v, code, out);
     const uint32_t word = mx_scale_word(code);
@@ -225,7 +233,7 @@ __global__ void __launch_bounds__(QT) mx_dequantize_kernel(const __grid_constant
 //     its vectors of the next row into its own places in shared memory
 //     (cp.async) while it works on this one.  Loads are then in flight all the
 //     time without holding registers, and no barrier is about the data
-//     (32760 x 5120 bf16, residual kept: 225 us, 5.2 TB/s; 337 us with a CTA a row).
+//     (32760 x 5120 bf16, residual kept: 195 us, 6.0 TB/s; 337 us with a CTA a row).
 //   - few rows, or rows too long for two stages of shared memory: a CTA a row,
 //     straight from global memory.  NCH = 0 reads x and r a second time instead
 //     of keeping them (rows too long for the registers).
@@ -328,10 +336,10 @@ __device__ __forceinline__ double row_sum(double v, double* part, int warps, int
 
 // codes and scale of one vector from w = n / scale
 template <int BITS>
-__device__ __forceinline__ void norm_store(const float (&w)[8], uint32_t code, int col, bool own, uint8_t* codes,
+__device__ __forceinline__ void norm_store(const float (&w)[8], uint32_t code, int col, bool in, bool own, uint8_t* codes,
                                            uint8_t* scales) {
   uint32_t out[BITS / 4];
-  mx_element_codes<BITS>(w, code, out);
+  mx_element_codes<BITS>(w, in ? code : 255u, out);   // (255: zero elements)
   const uint32_t word = mx_scale_word(code);
   if (own) {
     uint8_t* q = codes + col * BITS / 8;
@@ -369,31 +377,31 @@ __device__ __forceinline__ void norm_vector_exact(const NormParams& p, const T* 
   const float inv = mx_inverse_scale(code);
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] *= inv;
-  norm_store<BITS>(w, code, col, own, codes, scales);
+  norm_store<BITS>(w, code, col, in, own, codes, scales);
 }
 
 // One vector of a row: its codes, its scale and the kept residual.  Every lane
-// of the warp takes part; `in`: the vector holds elements; `own`: it lies in the
-// row's padded length.  True (in all lanes) where the warp met a border between
-// codes and norm_vector_exact has to follow; with REDO it has, from x and r,
-// before the kept residual is written, which may lie over them.
+// of the warp takes part.  `in`: the vector holds elements (v and g are
+// anything, finite or not, where it does not: a block of 32 lies in or out as a
+// whole, so nothing of it reaches another); `own`: it lies in the row's padded
+// length.  True (in all lanes) where the warp met a border between codes and
+// norm_vector_exact has to follow; with REDO it has, from x and r, before the
+// kept residual is written, which may lie over them.
 template <typename T, int BITS, bool REDO>
-__device__ __forceinline__ bool norm_vector(const NormParams& p, const f32x2 (&v)[4], const T* x, const T* r, int col,
-                                            bool in, bool own, f32x2 rs2, double rs64, T* r_out, uint8_t* codes,
-                                            uint8_t* scales) {
+__device__ __forceinline__ bool norm_vector(const NormParams& p, const f32x2 (&v)[4], const f32x2 (&g)[4], const T* x,
+                                            const T* r, int col, bool in, bool own, f32x2 rs2, double rs64, T* r_out,
+                                            uint8_t* codes, uint8_t* scales) {
   f32x2 n[4];
-  if (in) {
-    load_gain(p, col, n);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) n[i] = 0ull;
-  }
   float w[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) n[i] = mul2(mul2(v[i], rs2), n[i]);
+  for (int i = 0; i < 4; ++i) n[i] = mul2(mul2(v[i], rs2), g[i]);
   unpack8(n, w);
-  const uint32_t top = mx_block_max(w), code = mx_scale_code<BITS>(top);
-  const f32x2 inv2 = pack2(mx_inverse_scale(code), mx_inverse_scale(code));
+  uint32_t top = mx_block_max(w);
+  top = in ? top : 0u;
+  const uint32_t code = mx_scale_code<BITS>(top);
+  // where there are no elements everything becomes 0 * finite: w is masked below
+  const float inv = in ? mx_inverse_scale(code) : 0.f;
+  const f32x2 inv2 = pack2(inv, inv);
 #pragma unroll
   for (int i = 0; i < 4; ++i) n[i] = mul2(n[i], inv2);
   unpack8(n, w);
@@ -414,10 +422,10 @@ __device__ __forceinline__ bool norm_vector(const NormParams& p, const f32x2 (&v
     }
     near = __vimin3_u32(near, at[0], at[1]);
   }
-  const bool border = in && top != 0u && (near <= (8u << SHIFT) || ((top + 4u) & 0x7FFFFFu) <= 8u);
+  const bool border = top != 0u && (near <= (8u << SHIFT) || ((top + 4u) & 0x7FFFFFu) <= 8u);
   const bool any = __any_sync(0xFFFFFFFFu, border);
   if (REDO && any) norm_vector_exact<T, BITS>(p, x, r, col, in, own, rs64, codes, scales);
-  else norm_store<BITS>(w, code, col, own, codes, scales);
+  else norm_store<BITS>(w, code, col, in, own, codes, scales);
   if (in && r_out) {
     float f[8];
     unpack8(v, f);
@@ -477,7 +485,9 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 1024 : 512) mx_norm_ker
   for (int k = 0; k < (NCH ? NCH : steps); ++k) {
     const int col = (k * p.tpr + t) * 8;
     if constexpr (NCH == 0) load(col, h[0]);
-    norm_vector<T, BITS, true>(p, h[NCH ? k : 0], x + col, r ? r + col : r, col, live && col < p.d,
+    f32x2 g[4];
+    load_gain(p, col < p.d ? col : 0, g);
+    norm_vector<T, BITS, true>(p, h[NCH ? k : 0], g, x + col, r ? r + col : r, col, live && col < p.d,
                          live && col < p.col_tiles * MX_COLS, rs2, rs64, r_out, codes, scales);
   }
 }
@@ -487,7 +497,7 @@ __device__ __forceinline__ void copy_async16(void* dst_smem, const void* src) {
                : "memory");
 }
 
-template <typename T, int BITS, int NCH>
+template <typename T, int BITS, int NCH, bool RES>
 __global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_constant__ NormParams p) {
   __shared__ double part[2][16];
   extern __shared__ __align__(16) unsigned char stage_mem[];
@@ -498,54 +508,56 @@ __global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_con
   }
   constexpr int VB = 8 * (int)sizeof(T);   // bytes of a vector
   const int t = threadIdx.x, tpr = blockDim.x;
-  const T* xs = static_cast<const T*>(p.x);
-  const T* rs_in = static_cast<const T*>(p.r);
   // a stage: the row's vectors of x, then of r; a thread uses its own places only
-  const int plane = p.d * (int)sizeof(T), stage = rs_in ? 2 * plane : plane;
-  unsigned char* mine = stage_mem + t * VB;
+  const int plane = p.d * (int)sizeof(T), stage = RES ? 2 * plane : plane;
   const int cols = p.col_tiles * MX_COLS;
   const int64_t step = (int64_t)p.row_ctas * p.d;
-  const T* x_next = xs + (int64_t)blockIdx.x * p.d;   // the next row to fetch
-  const T* r_next = rs_in ? rs_in + (int64_t)blockIdx.x * p.d : nullptr;
+  // this thread's columns; one without elements reads the row's first vector and drops it
+  int at[NCH];
+  bool in[NCH];
+  f32x2 gain[NCH == 2 ? 2 : 1][4];   // its gain, kept where the registers allow it
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int col = (k * tpr + t) * 8;
+    in[k] = col < p.d;
+    at[k] = in[k] ? col : 0;
+    if constexpr (NCH == 2) load_gain(p, at[k], gain[k]);
+  }
+  const T* x_next = static_cast<const T*>(p.x) + (int64_t)blockIdx.x * p.d;   // the next row to fetch
+  const T* r_next = RES ? static_cast<const T*>(p.r) + (int64_t)blockIdx.x * p.d : nullptr;
   auto fetch = [&](bool there, unsigned char* to) {
     if (there) {
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
-        const int col = (k * tpr + t) * 8;
-        if (col < p.d) {
-          unsigned char* q = to + k * tpr * VB;
+        if (in[k]) {
+          unsigned char* q = to + at[k] * (int)sizeof(T);
 #pragma unroll
-          for (int b = 0; b < VB; b += 16) copy_async16(q + b, reinterpret_cast<const unsigned char*>(x_next + col) + b);
-          if (rs_in) {
-#pragma unroll
-            for (int b = 0; b < VB; b += 16) copy_async16(q + plane + b, reinterpret_cast<const unsigned char*>(r_next + col) + b);
+          for (int b = 0; b < VB; b += 16) {
+            copy_async16(q + b, reinterpret_cast<const unsigned char*>(x_next + at[k]) + b);
+            if constexpr (RES) copy_async16(q + plane + b, reinterpret_cast<const unsigned char*>(r_next + at[k]) + b);
           }
         }
       }
       x_next += step;
-      if (rs_in) r_next += step;
+      if constexpr (RES) r_next += step;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int s = 0;
-  fetch(true, mine);
-  T* r_out = p.r_out ? static_cast<T*>(p.r_out) + (int64_t)blockIdx.x * p.d : nullptr;
+  fetch(true, stage_mem);
+  T* r_out = RES && p.r_out ? static_cast<T*>(p.r_out) + (int64_t)blockIdx.x * p.d : nullptr;
   for (int64_t row = blockIdx.x; row < p.rows; row += p.row_ctas, s ^= 1) {
-    fetch(row + p.row_ctas < p.rows, mine + (s ^ 1) * stage);
+    fetch(row + p.row_ctas < p.rows, stage_mem + (s ^ 1) * stage);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
-    const unsigned char* q = mine + s * stage;
+    const T* q = reinterpret_cast<const T*>(stage_mem + s * stage);
+    const T* qr = RES ? reinterpret_cast<const T*>(stage_mem + s * stage + plane) : nullptr;
     f32x2 h[NCH][4];
     double total = 0.0;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      const T* a = reinterpret_cast<const T*>(q + k * tpr * VB);
-      if ((k * tpr + t) * 8 < p.d) {
-        load_h(a, rs_in ? reinterpret_cast<const T*>(q + k * tpr * VB + plane) : nullptr, h[k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[k][i] = 0ull;
-      }
-      total += (double)sum_squares(h[k]);
+      load_h(q + at[k], RES ? qr + at[k] : nullptr, h[k]);
+      const float sq = sum_squares(h[k]);
+      total += in[k] ? (double)sq : 0.0;
     }
     const double rs64 = rsqrt64(row_sum(total, part[s], tpr >> 5, 0) * p.inv_d + (double)p.eps);
     const f32x2 rs2 = pack2((float)rs64, (float)rs64);
@@ -555,7 +567,10 @@ __global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_con
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int col = (k * tpr + t) * 8;
-      if (norm_vector<T, BITS, false>(p, h[k], nullptr, nullptr, col, col < p.d, col < cols, rs2, rs64, r_out, codes, scales))
+      f32x2 g[4];
+      if constexpr (NCH != 2) load_gain(p, at[k], g);
+      if (norm_vector<T, BITS, false>(p, h[k], NCH == 2 ? gain[k % 2] : g, nullptr, nullptr, col, in[k], col < cols, rs2, rs64,
+                                      r_out, codes, scales))
         redo |= 1u << k;
     }
     // the warp's vectors next to a border, again from the stage, which nothing
@@ -564,10 +579,8 @@ __global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_con
 #pragma unroll 1
       for (int k = 0; k < NCH; ++k) {
         const int col = (k * tpr + t) * 8;
-        const T* a = reinterpret_cast<const T*>(q + k * tpr * VB);
         if (redo >> k & 1u)
-          norm_vector_exact<T, BITS>(p, a, rs_in ? reinterpret_cast<const T*>(q + k * tpr * VB + plane) : nullptr, col,
-                                     col < p.d, col < cols, rs64, codes, scales);
+          norm_vector_exact<T, BITS>(p, q + col, RES ? qr + col : nullptr, col, col < p.d, col < cols, rs64, codes, scales);
       }
     }
     if (r_out) r_out += step;
@@ -575,17 +588,17 @@ __global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_con
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename T, int BITS, int NCH>
+template <typename T, int BITS, int NCH, bool RES>
 oq_status norm_stream_launch(NormParams& p, int threads, int sms, int device, size_t smem, cudaStream_t st) {
   static std::atomic<uint64_t> smem_set{0};
-  const oq_status ok = mx_allow_smem(reinterpret_cast<const void*>(mx_norm_stream_kernel<T, BITS, NCH>), NORM_SMEM, device,
+  const oq_status ok = mx_allow_smem(reinterpret_cast<const void*>(mx_norm_stream_kernel<T, BITS, NCH, RES>), NORM_SMEM, device,
                                      &smem_set);
   if (ok != OQ_OK) return ok;
   // CTAs an SM holds: 64 registers a thread, 228 KB of shared memory with 1 KB a CTA of the system's and 256 bytes of sums
   const int resident = std::max(1, std::min(1024 / threads, (int)(228 * 1024 / (smem + 1024 + 256))));
   p.row_ctas = (int)std::min<int64_t>(p.rows, (int64_t)sms * resident);
   const unsigned grid = (unsigned)p.row_ctas + (p.rows % MX_ROWS ? 1u : 0u);
-  return launch_status(mx_launch(mx_norm_stream_kernel<T, BITS, NCH>, dim3(grid), threads, smem, 0, st, p), "oq_rms_norm_mx");
+  return launch_status(mx_launch(mx_norm_stream_kernel<T, BITS, NCH, RES>, dim3(grid), threads, smem, 0, st, p), "oq_rms_norm_mx");
 }
 
 template <typename T, int BITS>
@@ -603,8 +616,10 @@ oq_status norm_launch(const NormParams& p0, cudaStream_t st) {
     const int threads = threads_for(nch);
     const size_t smem = (size_t)2 * p.d * sizeof(T) * (p.r ? 2 : 1);
     if (threads >= 128 && threads <= 512 && smem <= NORM_SMEM)
-      return nch == 2 ? norm_stream_launch<T, BITS, 2>(p, threads, sms, device, smem, st)
-                      : norm_stream_launch<T, BITS, 4>(p, threads, sms, device, smem, st);
+      return nch == 2 ? (p.r ? norm_stream_launch<T, BITS, 2, true>(p, threads, sms, device, smem, st)
+                             : norm_stream_launch<T, BITS, 2, false>(p, threads, sms, device, smem, st))
+                      : (p.r ? norm_stream_launch<T, BITS, 4, true>(p, threads, sms, device, smem, st)
+                             : norm_stream_launch<T, BITS, 4, false>(p, threads, sms, device, smem, st));
   }
   // A CTA a row: as many threads as fit, for the least latency
   int nch = 0;
