@@ -498,8 +498,8 @@ __device__ __forceinline__ void copy_async16(void* dst_smem, const void* src) {
 }
 
 template <typename T, int BITS, int NCH, bool RES>
-__global__ void __launch_bounds__(512, 2) mx_norm_stream_kernel(const __grid_constant__ NormParams p) {
-  __shared__ double part[2][16];
+__global__ void __launch_bounds__(1024, 1) mx_norm_stream_kernel(const __grid_constant__ NormParams p) {
+  __shared__ double part[2][32];
   extern __shared__ __align__(16) unsigned char stage_mem[];
   dependency_wait();
   if ((int)blockIdx.x >= p.row_ctas) {
@@ -594,8 +594,8 @@ oq_status norm_stream_launch(NormParams& p, int threads, int sms, int device, si
   const oq_status ok = mx_allow_smem(reinterpret_cast<const void*>(mx_norm_stream_kernel<T, BITS, NCH, RES>), NORM_SMEM, device,
                                      &smem_set);
   if (ok != OQ_OK) return ok;
-  // CTAs an SM holds: 64 registers a thread, 228 KB of shared memory with 1 KB a CTA of the system's and 256 bytes of sums
-  const int resident = std::max(1, std::min(1024 / threads, (int)(228 * 1024 / (smem + 1024 + 256))));
+  // CTAs an SM holds: 64 registers a thread, 228 KB of shared memory with 1 KB a CTA of the system's and 512 bytes of sums
+  const int resident = std::max(1, std::min(1024 / threads, (int)(228 * 1024 / (smem + 1024 + 512))));
   p.row_ctas = (int)std::min<int64_t>(p.rows, (int64_t)sms * resident);
   const unsigned grid = (unsigned)p.row_ctas + (p.rows % MX_ROWS ? 1u : 0u);
   return launch_status(mx_launch(mx_norm_stream_kernel<T, BITS, NCH, RES>, dim3(grid), threads, smem, 0, st, p), "oq_rms_norm_mx");
@@ -610,12 +610,13 @@ oq_status norm_launch(const NormParams& p0, cudaStream_t st) {
   auto threads_for = [&](int n) { return ((chunks + n - 1) / n + 31) / 32 * 32; };
   // the streaming kernel, where there are rows enough to walk over
   if (p.rows > 2 * sms) {
-    // vectors a thread holds: two where a CTA's threads allow it (64 registers
-    // without spills), four where they leave fewer idle places or must
-    const int nch = threads_for(2) <= 512 && (threads_for(2) <= 2 * threads_for(4) || threads_for(4) < 128) ? 2 : 4;
+    // Two vectors a thread, whose gains then stay in registers, where a CTA's
+    // threads allow it; four for longer rows (12288 wide: 72.5 us with two, 76
+    // with four).
+    const int nch = threads_for(2) <= 1024 ? 2 : 4;
     const int threads = threads_for(nch);
     const size_t smem = (size_t)2 * p.d * sizeof(T) * (p.r ? 2 : 1);
-    if (threads >= 128 && threads <= 512 && smem <= NORM_SMEM)
+    if (threads >= 128 && threads <= 1024 && smem <= NORM_SMEM)
       return nch == 2 ? (p.r ? norm_stream_launch<T, BITS, 2, true>(p, threads, sms, device, smem, st)
                              : norm_stream_launch<T, BITS, 2, false>(p, threads, sms, device, smem, st))
                       : (p.r ? norm_stream_launch<T, BITS, 4, true>(p, threads, sms, device, smem, st)

@@ -124,7 +124,10 @@ def test_read_back_of_every_code(env):
     (64, 256, "fp32", 8, True, "fp32"), (333, 2016, "bf16", 4, True, "bf16"), (1, 5120, "bf16", 8, True, "fp32"),
     (100, 5120, "fp32", 8, False, "fp32"), (17, 12288, "bf16", 8, True, None), (9, 13824, "fp32", 8, True, "bf16"),
     (3, 20032, "bf16", 8, True, "fp32"), (2, 28000, "fp32", 8, True, "fp32"), (2, 40992, "bf16", 8, True, "bf16"),
-    (3, 65504, "fp32", 4, False, "fp32")])
+    (3, 65504, "fp32", 4, False, "fp32"),
+    # rows enough for CTAs that walk over them, several rows each in the first two
+    (3000, 2080, "bf16", 8, True, "fp32"), (2500, 2016, "fp32", 4, True, "bf16"), (400, 5152, "fp32", 8, False, "bf16"),
+    (310, 2464, "bf16", 4, False, None), (300, 20032, "bf16", 8, True, "fp32"), (297, 13824, "fp32", 8, True, None)])
 def test_norm(env, rows, d, dtype, bits, residual, gain):
     torch, B = env
     rng = np.random.default_rng(d + rows)
@@ -165,11 +168,11 @@ def test_norm_degenerate_rows(env):
     assert abs(v[3, 9] - want) <= want / 16 and np.all(np.delete(v[3], 9) == 0)
 
 
-@pytest.mark.parametrize("d", [160, 5120, 40992])
-def test_norm_writes_the_residual_in_place(env, d):
+@pytest.mark.parametrize("rows,d", [(6, 160), (6, 5120), (6, 40992), (1500, 2080)])
+def test_norm_writes_the_residual_in_place(env, rows, d):
     torch, B = env
     rng = np.random.default_rng(d)
-    x, r = (_cuda(torch, _rows(rng, 6, d, "bf16"), "bf16") for _ in range(2))
+    x, r = (_cuda(torch, _rows(rng, rows, d, "bf16"), "bf16") for _ in range(2))
     want = B.oq_rms_norm_mx(x, residual=r)
     for which in ("x", "residual"):
         tx, tr = x.clone(), r.clone()
