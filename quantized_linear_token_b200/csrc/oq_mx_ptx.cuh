@@ -62,23 +62,21 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 
-// Block-scaled MMA, K of 32 bytes per row: F4 multiplies 64 e2m1 by 64 e2m1
-// with two scales a row, otherwise 32 elements of 8-bit containers (e4m3, or
-// e2m1 in the low half of each 16-byte group's padding layout) with one.
-template <int CG, bool F4>
+// Block-scaled MMA of one CTA, K of 32 bytes per row: F4 multiplies 64 e2m1 by
+// 64 e2m1 with two scales a row, otherwise 32 elements in 8-bit containers (e4m3,
+// or e2m1 as TMA spreads it: 8 bytes of codes in every 16) with one.
+template <bool F4>
 __device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-#define OQ_MX_MMA(CGS, KIND, VEC)                                                                       \
+#define OQ_MX_MMA(KIND, VEC)                                                                             \
   asm volatile(                                                                                          \
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                   \
-      "tcgen05.mma.cta_group::" CGS ".kind::" KIND ".block_scale.scale_vec::" VEC                        \
+      "tcgen05.mma.cta_group::1.kind::" KIND ".block_scale.scale_vec::" VEC                              \
       " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),                                            \
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                           \
       : "memory")
-  if constexpr (CG == 2 && F4) OQ_MX_MMA("2", "mxf4", "2X");
-  else if constexpr (CG == 2) OQ_MX_MMA("2", "mxf8f6f4", "1X");
-  else if constexpr (F4) OQ_MX_MMA("1", "mxf4", "2X");
-  else OQ_MX_MMA("1", "mxf8f6f4", "1X");
+  if constexpr (F4) OQ_MX_MMA("mxf4", "2X");
+  else OQ_MX_MMA("mxf8f6f4", "1X");
 #undef OQ_MX_MMA
 }
 

@@ -25,7 +25,8 @@ oq_status launch_status(cudaError_t e, const char* what) {
 // 256-byte (bf16) segments; a thread loads its rows' vectors before it uses the
 // first.  The tile's 512 scale bytes are gathered in shared memory
 // and leave as whole sectors.  Rows past the end read as zeros and get scale
-// code 0; columns past d get zero codes and scale code 0.
+// code 0; columns past d get zero codes and scale code 0.  Bound by HBM: 32760 x
+// 5120 bf16 in 4 bits 67 us, 6.4 TB/s (98 % of a copy's rate); a few tiles 2 us.
 //
 // 256 threads, or 512 with half as many rows each: where there are only a few
 // tiles for an SM (1001 x 2016 in 8 bits 2.8 -> 2.4 us), and for bf16 rows in 8
@@ -110,7 +111,8 @@ __global__ void __launch_bounds__(QT) mx_quantize_kernel(const __grid_constant__
 
 // ------------------------------------------------------------------ read-back
 // The same tiles: value = element * 2^(scale code - 127).  Scale code 0 is
-// 2^-127, a subnormal; code 255 is NaN.
+// 2^-127, a subnormal; code 255 is NaN.  Bound by HBM: 32760 x 5120 to bf16 66 us
+// from 4 bits, 79 from 8 (6.4, 6.5 TB/s).
 __device__ __forceinline__ float mx_scale_value(uint32_t code) {
   return code == 255u ? __uint_as_float(0x7FFFFFFFu) : code == 0u ? __uint_as_float(1u << 22) : __uint_as_float(code << 23);
 }

@@ -10,6 +10,12 @@
 // deep, loading the peers' sums instead took a third of the kernel.)  4-bit activations use kind::mxf4, 8-bit ones
 // kind::mxf8f6f4 with the weights' codes spread to 8-bit containers by TMA.
 //
+// Measured back to back, weights from HBM: one token 13824 -> 5120 (4 bits) 12.1
+// us, 3.1 TB/s of weights (5.7 us at the copy bandwidth; the rest is launch, first
+// loads and the 570 cycles that a stage's four scale copies and MMAs take to
+// issue); 16 tokens 5120 -> 5120 7.1 us; 256 tokens 13824 -> 5120 with 8-bit
+// activations 25 us (MMAs 10 us on 120 SMs, exchange and sums 6 us).
+//
 // Warps: 0-3 epilogue, 4 TMA producer, 5 tensor memory and MMAs.
 #include <algorithm>
 #include <cstring>
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = F4 ? k / 2 : 0;
-          tc_mma_mx<1, F4>(tmem, wd + 2 * k, xd + 2 * k, idesc | idesc_mx_sf(F4 ? 2u * (k & 1) : (uint32_t)k), sfw + 4 * c,
+          tc_mma_mx<F4>(tmem, wd + 2 * k, xd + 2 * k, idesc | idesc_mx_sf(F4 ? 2u * (k & 1) : (uint32_t)k), sfw + 4 * c,
                            sfx + 4 * c * C::RT, k > 0 ? 1u : acc);
         }
         tc_commit(&op_empty[s]);
