@@ -460,10 +460,10 @@ oq_status oq_linear_fused_host(const oq_layer* layer, const void* x_host, int32_
  *            Places of a tile that belong to no row or no block hold code 0.
  * oq_mx_codes_size and oq_mx_scales_size give the bytes of both arrays (0 for
  * arguments out of range).  Every call takes d % 32 == 0, d < 65536, bits 4
- * or 8 (else OQ_ERR_UNSUPPORTED), codes 32-byte and scales 16-byte aligned,
- * and no overlap between inputs and outputs except where stated.  rows = 0 is
- * a no-op.  No call holds state, allocates or waits on the host; calls may
- * overlap and be captured into graphs.
+ * or 8 (else OQ_ERR_UNSUPPORTED), codes 32-byte and scales 16-byte aligned;
+ * an output that overlaps another argument is refused (OQ_ERR_INVALID_ARG)
+ * except where stated.  rows = 0 is a no-op.  No call holds state, allocates or
+ * waits on the host; calls may overlap and be captured into graphs.
  *
  * oq_mx_quantize -- rows of bf16 or fp32 to codes and scales:
  *   E = floor(log2(max_i |x_i|)) - (2 for e2m1, 8 for e4m3), at least -127

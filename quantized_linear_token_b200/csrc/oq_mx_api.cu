@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 #include <new>
 #include <string>
 
@@ -38,6 +39,26 @@ oq_status check_codes(const std::string& who, const void* codes, const void* sca
   if (!codes || !scales || !aligned(codes, 32) || !aligned(scales, 16))
     return fail(OQ_ERR_INVALID_ARG, who + ": codes (32-byte) / scales (16-byte) pointers invalid");
   return OQ_OK;
+}
+
+// A written range against the call's others: any overlap is refused, but for
+// the same array given twice where `same` allows it.
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+}
+oq_status check_overlap(const char* who, const Range& written, std::initializer_list<Range> others, bool same = false) {
+  for (const Range& r : others)
+    if (overlap(written, r) && !(same && written.p == r.p))
+      return fail(OQ_ERR_INVALID_ARG, std::string(who) + ": an output overlaps another argument");
+  return OQ_OK;
+}
+size_t row_array(int64_t rows, int32_t d, int32_t dtype) {
+  return (size_t)rows * (size_t)d * (dtype == OQ_DTYPE_F32 ? 4 : 2);
 }
 
 oq_status unsupported(oq_status st, const char* who) {
@@ -122,6 +143,9 @@ oq_status oq_mx_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t d
   if (st != OQ_OK || (st = check_dtype(who, x_dtype)) != OQ_OK || rows == 0) return st;
   if (!x || !aligned(x, 16)) return fail(OQ_ERR_INVALID_ARG, "oq_mx_quantize: x must be a 16-byte aligned pointer");
   if ((st = check_codes(who, codes, scales)) != OQ_OK) return st;
+  const Range in{x, row_array(rows, d, x_dtype)};
+  const Range c{codes, oq_mx_codes_size(rows, d, bits)}, s{scales, oq_mx_scales_size(rows, d)};
+  if ((st = check_overlap(who, c, {in, s})) != OQ_OK || (st = check_overlap(who, s, {in})) != OQ_OK) return st;
   return unsupported(mx_quantize_launch(x, x_dtype, rows, d, bits, codes, scales, stream), who);
 }
 
@@ -132,6 +156,9 @@ oq_status oq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
   if (st != OQ_OK || (st = check_dtype(who, x_dtype)) != OQ_OK || rows == 0) return st;
   if (!x || !aligned(x, 16)) return fail(OQ_ERR_INVALID_ARG, "oq_mx_dequantize: x must be a 16-byte aligned pointer");
   if ((st = check_codes(who, codes, scales)) != OQ_OK) return st;
+  if ((st = check_overlap(who, {x, row_array(rows, d, x_dtype)},
+                          {{codes, oq_mx_codes_size(rows, d, bits)}, {scales, oq_mx_scales_size(rows, d)}})) != OQ_OK)
+    return st;
   return unsupported(mx_dequantize_launch(codes, scales, rows, d, bits, x, x_dtype, stream), who);
 }
 
@@ -149,6 +176,13 @@ oq_status oq_rms_norm_mx(const void* x, const void* residual, int32_t x_dtype, c
   if (residual_out && !residual)
     return fail(OQ_ERR_INVALID_ARG, "oq_rms_norm_mx: residual_out without a residual");
   if ((st = check_codes(who, codes, scales)) != OQ_OK) return st;
+  const size_t n = row_array(rows, d, x_dtype);
+  const Range in{x, n}, res{residual, n}, kept{residual_out, n}, g{gain, row_array(1, d, gain_dtype)};
+  const Range c{codes, oq_mx_codes_size(rows, d, bits)}, s{scales, oq_mx_scales_size(rows, d)};
+  if ((st = check_overlap(who, c, {in, res, kept, g, s})) != OQ_OK ||
+      (st = check_overlap(who, s, {in, res, kept, g})) != OQ_OK || (st = check_overlap(who, kept, {g})) != OQ_OK ||
+      (st = check_overlap(who, kept, {in, res}, true)) != OQ_OK)
+    return st;
   MxNormArgs a;
   a.x = x;
   a.residual = residual;
@@ -174,6 +208,12 @@ oq_status oq_linear_mx(const oq_layer* L, const uint8_t* codes, const uint8_t* s
   if (st != OQ_OK || (st = check_dtype(who, y_dtype)) != OQ_OK || T == 0) return st;
   if ((st = check_codes(who, codes, scales)) != OQ_OK || (st = check_codes(who, Wcodes, Wscales)) != OQ_OK) return st;
   if (!y || !aligned(y, 16)) return fail(OQ_ERR_INVALID_ARG, "oq_linear_mx: y must be a 16-byte aligned pointer");
+  if ((st = check_overlap(who, {y, row_array(T, L->d_out, y_dtype)},
+                          {{codes, oq_mx_codes_size(T, L->d_in, L->a_bits)},
+                           {scales, oq_mx_scales_size(T, L->d_in)},
+                           {Wcodes, oq_mx_codes_size(L->d_out, L->d_in, 4)},
+                           {Wscales, oq_mx_scales_size(L->d_out, L->d_in)}})) != OQ_OK)
+    return st;
   int dev = -1;
   cudaGetDevice(&dev);
   if (dev != L->device)

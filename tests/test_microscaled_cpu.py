@@ -130,6 +130,24 @@ def test_norm_refusals(lib):
     assert f(rows=0, x=None, r=None, ro=None, c=None, s=None) == 0
 
 
+def test_overlapping_outputs_are_refused(lib):
+    # 256 rows of 128 bf16 (64 KB): codes 16 KB (4 bits), scales 1 KB; nothing is launched
+    X, C, S, K = 1 << 30, 2 << 30, 3 << 30, 4 << 30
+
+    def norm(**k):
+        a = {"x": X, "r": K, "g": 5 << 30, "ro": 6 << 30, "c": C, "s": S, **k}
+        return lib.oq_rms_norm_mx(a["x"], a["r"], 1, a["g"], 0, 1e-6, 256, 128, 8, a["ro"], a["c"], a["s"], None)
+
+    assert lib.oq_mx_quantize(X, 1, 256, 128, 4, X + 65504, S, None) == 1      # codes begin in x's last row
+    assert lib.oq_mx_quantize(X, 1, 256, 128, 4, C, X - 16, None) == 1         # scales end in x's first
+    assert lib.oq_mx_quantize(X, 1, 256, 128, 4, C, C + 16368, None) == 1      # scales in the codes
+    assert lib.oq_mx_dequantize(C, S, 256, 128, 4, C + 16368, 1, None) == 1
+    assert lib.oq_mx_dequantize(C, S, 256, 128, 4, S + 1008, 1, None) == 1
+    assert norm(ro=X + 256) == 1 and norm(ro=K - 65520) == 1                   # a row off, not in place
+    assert norm(c=X + 32) == 1 and norm(s=K + 16) == 1 and norm(g=(6 << 30) + 16) == 1
+    assert b"overlaps" in lib.oq_last_error()
+
+
 def test_linear_refuses_a_null_layer(lib):
     assert lib.oq_linear_mx(None, P, P, 4, P, P, P, 0, None) == 1
 
