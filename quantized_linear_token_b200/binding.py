@@ -538,8 +538,8 @@ def oq_mx_dequantize(codes, scales, d: int, bits: int, dtype=None, x=None):
     """Codes and scales of a [rows, d] operand -> its values [rows, d] (fp32 by
     default, or bf16)."""
     torch = _torch()
-    if codes.dim() != 2 or bits not in (4, 8) or d <= 0 or d % 32:
-        raise ValueError("codes must be a matrix, bits 4 or 8 and d a positive multiple of 32")
+    if codes.dim() != 2 or scales is None or bits not in (4, 8) or d <= 0 or d % 32:
+        raise ValueError("codes must be a matrix with its scales, bits 4 or 8 and d a positive multiple of 32")
     rows, device = codes.shape[0], codes.device
     _, _, pc, ps = _mx_outputs(codes, scales, rows, d, bits, device)
     if x is None:
@@ -597,7 +597,7 @@ def oq_linear_mx(layer: Layer, codes, scales, Wcodes, Wscales, y=None, y_dtype=N
         y = torch.empty_strided((T, n), (n, 1), dtype=torch.float32 if y_dtype is None else y_dtype, device=device)
         py = y.data_ptr()
     else:
-        py = _mx_rows(y, (T, n), y.dtype, device, "y")
+        py = _mx_rows(y, (T, n), y.dtype if y_dtype is None else y_dtype, device, "y")
     ycode = _mx_dtype(y)
     _launch("oq_linear_mx", device, layer.handle, *pointers, py, ycode)
     return y

@@ -167,3 +167,9 @@ def test_binding_refuses_host_tensors_and_bad_shapes(lib):
         B.oq_rms_norm_mx(x)
     with pytest.raises(ValueError):
         B.oq_mx_dequantize(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(1, 1, 32, 4, 4, dtype=torch.uint8), 48, 4)
+
+
+def test_read_back_refuses_missing_scales():
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError, match="scales"):
+        B.oq_mx_dequantize(torch.zeros(3, 128, dtype=torch.uint8), None, 128, 8)
