@@ -469,3 +469,33 @@ def test_refusals_on_a_microscaled_layer(env):
         B.oq_rms_norm_mx(x, torch.ones(128, device="cuda"))
     with pytest.raises(TypeError):
         B.oq_mx_quantize(x.half(), 4)
+
+
+def test_overlapping_outputs_are_refused(env):
+    """Every call is refused before a launch; the arrays keep what they held."""
+    torch, B = env
+    layer = B.oq_layer_create(256, 256, 0, 8, 4, B.OQ_FLAG_MICROSCALED)
+    x = torch.randn(64, 256, device="cuda")
+    codes, scales = B.oq_mx_quantize(x, 8)
+    wc, wt = B.oq_mx_quantize(torch.randn(256, 256, device="cuda"), 4)
+    raw = torch.cat([codes.flatten(), torch.zeros(256 * 256 * 4, dtype=torch.uint8, device="cuda")])
+    held = raw[:64 * 256].view(64, 256)
+    inside = raw[64 * 256 - 16:][:64 * 256 * 4].view(torch.float32).view(64, 256)
+    before = raw.clone()
+    calls = (lambda: B.oq_linear_mx(layer, held, scales, wc, wt, y=inside),
+             lambda: B.oq_mx_dequantize(held, scales, 256, 8, x=inside),
+             lambda: B.oq_mx_quantize(inside, 8, codes=held),
+             lambda: B.oq_rms_norm_mx(inside, codes=held),
+             lambda: B.oq_rms_norm_mx(inside[:32], residual=x[:32], residual_out=inside[16:48]))
+    for call in calls:
+        with pytest.raises(B.OrbitQuantError) as e:
+            call()
+        assert e.value.status == 1
+    with pytest.raises(ValueError):
+        B.oq_linear_mx(layer, codes, scales, wc, wt, y=torch.empty(64, 256, device="cuda"), y_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    assert torch.equal(raw, before)
+    # side by side is no overlap
+    beside = raw[64 * 256:][:64 * 256 * 4].view(torch.float32).view(64, 256)
+    assert torch.equal(B.oq_linear_mx(layer, held, scales, wc, wt, y=beside),
+                       B.oq_linear_mx(layer, codes, scales, wc, wt))
