@@ -55,6 +55,10 @@ struct Cfg {
   static constexpr int RING = OS * STAGE > PART + RECV ? OS * STAGE : PART + RECV;
   static constexpr size_t SMEM = 1024 + (size_t)RING + 8 * (2 * OS + 2) + 16;
   static_assert(SMEM <= 227 * 1024, "shared memory");
+  // CTAs of a cluster wait for one another, so none may wait for tensor memory
+  // that another cluster's CTA holds: two CTAs of these kernels fit an SM only
+  // where their columns do too.
+  static_assert(SMEM > 76 * 1024 && (SMEM > 114 * 1024 || 2 * TMEM <= 512), "tensor memory of the CTAs an SM holds");
 };
 
 struct SmallParams {
