@@ -487,7 +487,7 @@ oq_status oq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
  * oq_rms_norm_mx -- the residual's addition, a root-mean-square norm and its
  * quantization in one pass over the rows:
  *   h = x + residual,  n_i = h_i g_i / sqrt(mean(h^2) + eps),  codes of n
- * in fp32 throughout, the norm from the unrounded h.
+ * in fp32 or better, the norm from the unrounded h.
  *   x, residual   device [rows, d], bf16 or fp32 (x_dtype for both); residual
  *                 may be NULL (h = x).
  *   gain          device [d], bf16 or fp32 (gain_dtype), or NULL (ones).
@@ -495,8 +495,10 @@ oq_status oq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
  *                 NULL (not kept); it may be x or residual itself.
  *   codes, scales of n, as oq_mx_quantize writes them (bits 8, or 4).
  * A row of zeros gives zeros (eps > 0).  A NaN or an infinity in a row makes
- * the whole row's norm NaN or 0 by the formula.  The sum of squares is fp32:
- * rows whose squares overflow it are outside the supported range.
+ * the whole row's norm NaN or 0 by the formula.  eps may be as small as 0: rows
+ * whose squares underflow fp32 are then formed in fp64.  With eps of 1e-35 or
+ * more the sum of squares is fp32: rows whose squares overflow it (elements
+ * above 1e19) are outside the supported range.
  * Errors: OQ_ERR_INVALID_ARG for a negative or non-finite eps, a residual_out
  * without a residual, a null or misaligned (16 bytes) pointer.
  */

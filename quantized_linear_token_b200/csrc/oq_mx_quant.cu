@@ -249,7 +249,14 @@ __global__ void __launch_bounds__(QT) mx_dequantize_kernel(const __grid_constant
 // two).  A warp that meets such an element (0.2 % of its steps) forms its
 // elements again in fp64, rounded to fp32 towards the odd neighbour, from which
 // the rounding to the element type is that of the fp64 value.
+//
+// All this holds while eps is at least NORM_EPS: then squares below 2^-126, and
+// what they round off (2^-150 each), do not count beside it.  A smaller eps
+// does not hide rows whose squares leave fp32's range, and such calls take the
+// second kernel, which forms those rows in fp64 throughout (norm_row_far; in the
+// first, a call in the loop would cost every row registers: 195 -> 254 us).
 constexpr size_t NORM_SMEM = 224 * 1024;   // stages of the streaming kernel
+constexpr float NORM_EPS = 1e-35f;
 
 struct NormParams {
   const void* x;
@@ -302,9 +309,10 @@ __device__ __forceinline__ float to_odd(double v) {
 }
 
 // 1 / sqrt(v) to 1e-13: an fp32 estimate and one Newton step
+__device__ __forceinline__ bool near_rsqrt64(double v) { return v > 1e-36 && v < 1e36; }
 __device__ __noinline__ double rsqrt64_far(double v) { return 1.0 / sqrt(v); }
 __device__ __forceinline__ double rsqrt64(double v) {
-  if (!(v > 1e-36 && v < 1e36)) return rsqrt64_far(v);
+  if (!near_rsqrt64(v)) return rsqrt64_far(v);
   float e;
   asm("rsqrt.approx.f32 %0, %1;" : "=f"(e) : "f"((float)v));   // 2 ulps: squared by the step
   const double y = (double)e, h = 0.5 * v;
@@ -436,6 +444,49 @@ __device__ __forceinline__ bool norm_vector(const NormParams& p, const f32x2 (&v
   return any;
 }
 
+// A row whose mean square is far (a root mean square below 1e-18 under an eps as
+// small, or above 1e18), all of it in fp64.  A thread reads and writes its own
+// vectors (t, t + tpr, ...).  All threads of the row call it; they meet at
+// barrier `bar`, because other rows of the CTA may not come this way.  Out of
+// line: it is rare, and its registers would be every row's.
+template <typename T, int BITS>
+__device__ __noinline__ void norm_row_far(const NormParams& p, const T* x, const T* r, T* r_out, uint8_t* codes,
+                                          uint8_t* scales, int t, int tpr, double* part, int w0, int bar) {
+  double v = 0.0;
+  for (int col = t * 8; col < p.d; col += tpr * 8) {
+    for (int i = 0; i < 8; ++i) {
+      double h = (double)(float)x[col + i];
+      if (r) h += (double)(float)r[col + i];
+      v += h * h;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  const int warps = tpr >> 5, lane = threadIdx.x & 31;
+  if (warps > 1) {
+    // (once all have read what part held)
+    asm volatile("barrier.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+    if (lane == 0) part[threadIdx.x >> 5] = v;
+    asm volatile("barrier.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+    v = 0.0;
+    for (int w = 0; w < warps; ++w) v += part[w0 + w];
+  }
+  const double rs64 = 1.0 / sqrt(v * p.inv_d + (double)p.eps);
+  const int cols = p.col_tiles * MX_COLS;
+  for (int c0 = (t - lane) * 8; c0 < cols; c0 += tpr * 8) {   // a warp's vectors together
+    const int col = c0 + lane * 8;
+    const bool in = col < p.d;
+    norm_vector_exact<T, BITS>(p, x + col, r ? r + col : r, col, in, col < cols, rs64, codes, scales);
+    if (in && r_out) {
+      f32x2 h[4];
+      float f[8];
+      load_h(x + col, r ? r + col : r, h);
+      unpack8(h, f);
+      store8(r_out + col, f);
+    }
+  }
+}
+
 // scales of the rows behind the last one, to the end of its tile: code 0 (one
 // CTA of at least 128 threads)
 __device__ __forceinline__ void norm_clear_padding(const NormParams& p) {
@@ -477,12 +528,16 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 1024 : 512) mx_norm_ker
     load((k * p.tpr + t) * 8, h[NCH ? k : 0]);
     total += (double)sum_squares(h[NCH ? k : 0]);
   }
-  const double rs64 = rsqrt64(row_sum(total, part, p.tpr >> 5, sub * (p.tpr >> 5)) * p.inv_d + (double)p.eps);
-  const f32x2 rs2 = pack2((float)rs64, (float)rs64);
-
+  const double mean = row_sum(total, part, p.tpr >> 5, sub * (p.tpr >> 5)) * p.inv_d + (double)p.eps;
   T* r_out = p.r_out ? static_cast<T*>(p.r_out) + base : nullptr;
   uint8_t* codes = p.codes + (live ? row : 0) * p.col_tiles * (MX_COLS * BITS / 8);
   uint8_t* scales = p.scales + (live ? row / MX_ROWS : 0) * p.col_tiles * MX_TILE_BYTES + 4 * mx_tile_word((int)(row % MX_ROWS));
+  if (!near_rsqrt64(mean)) {   // the same in all threads of a row
+    if (live) norm_row_far<T, BITS>(p, x, r, r_out, codes, scales, t, p.tpr, part, sub * (p.tpr >> 5), 1 + sub);
+    return;
+  }
+  const double rs64 = rsqrt64(mean);
+  const f32x2 rs2 = pack2((float)rs64, (float)rs64);
 #pragma unroll
   for (int k = 0; k < (NCH ? NCH : steps); ++k) {
     const int col = (k * p.tpr + t) * 8;
@@ -611,7 +666,7 @@ oq_status norm_launch(const NormParams& p0, cudaStream_t st) {
   const int chunks = p.col_tiles * 16;   // vectors of eight, padding included
   auto threads_for = [&](int n) { return ((chunks + n - 1) / n + 31) / 32 * 32; };
   // the streaming kernel, where there are rows enough to walk over
-  if (p.rows > 2 * sms) {
+  if (p.rows > 2 * sms && p.eps >= NORM_EPS) {
     // Two vectors a thread, whose gains then stay in registers, where a CTA's
     // threads allow it; four for longer rows (12288 wide: 72.5 us with two, 76
     // with four).

@@ -203,6 +203,92 @@ def test_norm_codes_are_those_of_the_exact_values(env, dtype, bits):
     R.check_quantized(n, e, s, bits, DELTA)
 
 
+FAR = 2.0 ** -40
+
+
+@pytest.mark.parametrize("rows,d,dtype,bits,residual,eps", [
+    # a CTA a row, or several narrow rows a CTA, whose sums take different ways
+    (26, 160, "fp32", 8, True, 0.0), (27, 512, "fp32", 4, False, 0.0), (26, 768, "bf16", 8, True, 0.0),
+    (30, 2080, "bf16", 8, True, 2.0 ** -140), (14, 12288, "fp32", 8, False, 0.0), (13, 20032, "bf16", 4, True, 0.0),
+    (13, 40992, "fp32", 8, True, 0.0),
+    # many rows
+    (320, 2080, "bf16", 8, True, 0.0), (1300, 2016, "fp32", 4, True, 2.0 ** -117), (310, 17312, "bf16", 8, True, 0.0),
+    # an eps beside which such rows do not count
+    (320, 2080, "bf16", 8, True, 2.0 ** -116), (1300, 2016, "fp32", 4, True, 2.0 ** -116),
+    (303, 17312, "fp32", 8, False, 1e-30)])
+def test_norm_of_rows_whose_squares_leave_fp32(env, rows, d, dtype, bits, residual, eps):
+    # Rows of every magnitude that the type holds, beside one another, with an
+    # eps that hides none of them.  Where the mean square is no ordinary fp32
+    # number (below 2^-121 or above 2^121 here) all is formed in fp64: at most
+    # 65504 additions, the root and two products, each 2^-53, are below 2^-40.
+    # (Squares that overflow are in range for no larger eps.)
+    torch, B = env
+    rng = np.random.default_rng(rows + d)
+    e = np.array([-130, -120, -100, -76, -73, -66, -61, -59, -40, 0, 40, 61, 64, 80, 126])
+    hidden = eps > 1e-35
+    if hidden:
+        e = np.minimum(e, 50)
+    mag = 2.0 ** np.roll(e, int(rng.integers(15)))[np.arange(rows) % 15]
+
+    def operand():
+        v = (rng.uniform(0.5, 1, (rows, d)) * rng.choice([-1.0, 1.0], (rows, d)) * mag[:, None]).astype(np.float32)
+        v[5::15, :] *= np.float32(2.0 ** -20)
+        v[5::15, d // 2] = 2.0 ** 30           # one large element, the others far below it
+        return R.bf16(v) if dtype == "bf16" else v
+
+    x, r = operand(), operand() if residual else None
+    g = (1 + 0.2 * rng.standard_normal(d)).astype(np.float32)
+    codes, scales, kept = B.oq_rms_norm_mx(_cuda(torch, x, dtype), _cuda(torch, g, "fp32"),
+                                           _cuda(torch, r, dtype) if residual else None, eps=eps, bits=bits)
+    h, n = R.norm(x.astype(np.float64), None if r is None else r.astype(np.float64), g.astype(np.float64),
+                  float(np.float32(eps)))
+    v = (h * h).mean(-1) + float(np.float32(eps))
+    far = (v < 2.0 ** -121) | (v > 2.0 ** 121)
+    assert hidden or far.sum() >= 3 and (~far).sum() >= 3
+    c, s = R.unpack(_np(codes), _np(scales), d, bits)
+    R.check_quantized(n, c, s, bits, DELTA)
+    if far.any():
+        R.check_quantized(n[far], c[far], s[far], bits, FAR)
+    if residual:
+        with np.errstate(over="ignore"):
+            sums = x + r
+        assert np.array_equal(_np(kept), R.bf16(sums) if dtype == "bf16" else sums)
+
+
+@pytest.mark.parametrize("rows", [6, 400])
+def test_norm_of_far_rows_in_place(env, rows):
+    torch, B = env
+    rng = np.random.default_rng(rows)
+    mag = 2.0 ** rng.choice([-120, -70, 0, 90], (rows, 1))
+    x, r = (_cuda(torch, rng.standard_normal((rows, 2080)) * mag, "bf16") for _ in range(2))
+    want = B.oq_rms_norm_mx(x, residual=r, eps=0.0)
+    for which in ("x", "residual"):
+        tx, tr = x.clone(), r.clone()
+        got = B.oq_rms_norm_mx(tx, residual=tr, eps=0.0, residual_out=tx if which == "x" else tr)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("rows,d", [(5, 160), (9, 512), (300, 2080)])
+def test_norm_of_tiny_and_infinite_rows(env, rows, d):
+    # a row far below eps is scaled by 1 / sqrt(eps); an infinity makes its
+    # block NaN and, by 1 / sqrt(inf) = 0, the rest of its row zeros
+    torch, B = env
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((rows, d)).astype(np.float32)
+    x[1] = 1e-30
+    x[3, 40], x[4, 33], x[4, 70] = np.inf, -np.inf, np.nan
+    codes, scales, _ = B.oq_rms_norm_mx(_cuda(torch, x, "fp32"), eps=1e-6)
+    c, s = R.unpack(_np(codes), _np(scales), d, 8)
+    fine = np.ones(rows, dtype=bool)
+    fine[3:5] = False
+    n = R.norm(x[fine].astype(np.float64), None, None, float(np.float32(1e-6)))[1]
+    R.check_quantized(n, c[fine], s[fine], 8, DELTA)
+    v = _np(B.oq_mx_dequantize(codes, scales, d, 8))
+    assert np.isnan(v[3, 32:64]).all() and np.all(np.delete(v[3], np.s_[32:64]) == 0)
+    assert np.isnan(v[4]).all()
+
+
+
 # ------------------------------------------------------------------ product
 def _operand(rng, rows, d, bits):
     x = rng.standard_normal((rows, d)) * np.exp(rng.standard_normal((rows, 1)))
