@@ -175,8 +175,8 @@ void oq_layer_destroy(oq_layer* layer);
 typedef struct {
   int32_t d_in, d_out, h, k, a_bits, w_bits, flags, reserved;
   uint64_t seed;
-  int64_t a_words_per_row;   /* d_in * a_bits / 32 */
-  int64_t w_words_per_row;   /* d_in * w_bits / 32 */
+  int64_t a_words_per_row;   /* d_in * a_bits / 32; OQ_FLAG_MICROSCALED: d_in rounded up to 128 */
+  int64_t w_words_per_row;   /* d_in * w_bits / 32; likewise */
   double a_scale, w_scale;   /* fp16 decode scale of each codebook's levels */
 } oq_layer_info;
 

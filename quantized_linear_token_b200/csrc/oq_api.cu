@@ -310,8 +310,10 @@ oq_status oq_layer_get_info(const oq_layer* L, oq_layer_info* out) {
   out->w_bits = L->w_bits;
   out->flags = L->flags;
   out->seed = L->seed;
-  out->a_words_per_row = (int64_t)L->d_in * L->a_bits / 32;
-  out->w_words_per_row = (int64_t)L->d_in * L->w_bits / 32;
+  // rows of microscaled codes are padded
+  const int64_t row = L->mx ? mx_padded_cols(L->d_in) : L->d_in;
+  out->a_words_per_row = row * L->a_bits / 32;
+  out->w_words_per_row = row * L->w_bits / 32;
   out->a_scale = L->a_scale;
   out->w_scale = L->w_scale;
   return OQ_OK;

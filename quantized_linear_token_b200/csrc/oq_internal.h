@@ -59,7 +59,8 @@ namespace oq {
 
 void set_error(const std::string& msg);
 
-// the microscaled layer (oq_mx_api.cu)
+// the microscaled layer (oq_mx_api.cu), and the elements of a row of its codes
+inline int64_t mx_padded_cols(int d) { return ((int64_t)d + 127) / 128 * 128; }
 oq_status create_mx_layer(int32_t d_in, int32_t d_out, uint64_t seed, int32_t a_bits, int32_t w_bits, int32_t flags,
                           oq_layer** out);
 // host math (oq_host.cpp)

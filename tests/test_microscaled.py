@@ -585,3 +585,13 @@ def test_overlapping_outputs_are_refused(env):
     beside = raw[64 * 256:][:64 * 256 * 4].view(torch.float32).view(64, 256)
     assert torch.equal(B.oq_linear_mx(layer, held, scales, wc, wt, y=beside),
                        B.oq_linear_mx(layer, codes, scales, wc, wt))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [32, 160, 2016, 5120])
+def test_layer_words_are_those_of_its_codes(env, d, bits):
+    # rows of codes are padded to 128 elements, and the layer says so
+    _, B = env
+    layer = B.oq_layer_create(d, 32, 0, bits, 4, B.OQ_FLAG_MICROSCALED)
+    assert 4 * layer.a_words_per_row * 7 == B.oq_mx_codes_size(7, d, bits)
+    assert 4 * layer.w_words_per_row * 32 == B.oq_mx_codes_size(32, d, 4)
