@@ -161,7 +161,7 @@ oq_status oq_rotation_build(int32_t d, uint64_t seed, int32_t flags, uint32_t* p
  *
  * With OQ_FLAG_MICROSCALED (alone in `flags`) the layer multiplies microscaled
  * operands (oq_linear_mx): a_bits 4 or 8, w_bits 4, d_in % 32 == 0,
- * d_in < 65536, d_out % 16 == 0; `seed` is not used.  Its operands come from
+ * d_in < 65536, d_out % 16 == 0, d_out <= 2^31 - 1024; `seed` is not used.  Its operands come from
  * oq_mx_quantize and oq_rms_norm_mx; every call that takes a rotation,
  * codebooks, norms or prepared weights returns OQ_ERR_UNSUPPORTED on it, and
  * the workspace sizes are 0.

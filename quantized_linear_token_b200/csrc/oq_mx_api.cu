@@ -19,7 +19,8 @@ oq_status fail(oq_status st, const std::string& msg) {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// row coordinates of the kernels' TMA boxes and grids are 32-bit
+// row and column coordinates of the kernels' tiles and grids are 32-bit, also
+// those behind the end of the last tile
 constexpr int64_t MAX_ROWS = ((int64_t)1 << 31) - 1024;
 
 oq_status check_shape(const std::string& who, int64_t rows, int32_t d, int32_t bits) {
@@ -96,6 +97,7 @@ oq_status create_mx_layer(int32_t d_in, int32_t d_out, uint64_t seed, int32_t a_
   if (d_in <= 0 || d_out <= 0) return fail(OQ_ERR_INVALID_ARG, "dimensions must be positive");
   if (d_in % MX_BLOCK || d_in > 65535 || d_out % 16)
     return fail(OQ_ERR_UNSUPPORTED, "the microscaled layer needs d_in % 32 == 0, d_in < 65536 and d_out % 16 == 0");
+  if (d_out > MAX_ROWS) return fail(OQ_ERR_UNSUPPORTED, "the microscaled layer takes d_out up to 2^31 - 1024");
   oq_layer* L = new (std::nothrow) oq_layer();
   if (!L) return fail(OQ_ERR_NOMEM, "host allocation failed");
   L->mx = true;

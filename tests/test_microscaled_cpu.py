@@ -173,3 +173,11 @@ def test_read_back_refuses_missing_scales():
     torch = pytest.importorskip("torch")
     with pytest.raises(ValueError, match="scales"):
         B.oq_mx_dequantize(torch.zeros(3, 128, dtype=torch.uint8), None, 128, 8)
+
+
+def test_layer_refuses_widths_past_32_bit_tiles(lib):
+    # tile origins are 32-bit: the last tile of such a width would pass them
+    h = ctypes.c_void_p()
+    for d_out in ((1 << 31) - 16, (1 << 31) - 1008):
+        assert lib.oq_layer_create(32, d_out, 0, 4, 4, B.OQ_FLAG_MICROSCALED, ctypes.byref(h)) == 2
+        assert not h.value
