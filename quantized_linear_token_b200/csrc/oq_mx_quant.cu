@@ -673,16 +673,17 @@ oq_status norm_launch(const NormParams& p0, cudaStream_t st) {
     const int nch = threads_for(2) <= 1024 ? 2 : 4;
     const int threads = threads_for(nch);
     const size_t smem = (size_t)2 * p.d * sizeof(T) * (p.r ? 2 : 1);
-    if (threads >= 128 && threads <= 1024 && smem <= NORM_SMEM)
-      return nch == 2 ? (p.r ? norm_stream_launch<T, BITS, 2, true>(p, threads, sms, device, smem, st)
-                             : norm_stream_launch<T, BITS, 2, false>(p, threads, sms, device, smem, st))
-                      : (p.r ? norm_stream_launch<T, BITS, 4, true>(p, threads, sms, device, smem, st)
-                             : norm_stream_launch<T, BITS, 4, false>(p, threads, sms, device, smem, st));
+    if (threads >= 128 && threads <= 1024 && smem <= NORM_SMEM) {
+      if (nch == 2)
+        return p.r ? norm_stream_launch<T, BITS, 2, true>(p, threads, sms, device, smem, st)
+                   : norm_stream_launch<T, BITS, 2, false>(p, threads, sms, device, smem, st);
+      if (!p.r) return norm_stream_launch<T, BITS, 4, false>(p, threads, sms, device, smem, st);
+      // (fp32 rows that long have no room for two stages of x and r)
+      if constexpr (sizeof(T) == 2) return norm_stream_launch<T, BITS, 4, true>(p, threads, sms, device, smem, st);
+    }
   }
   // A CTA a row: as many threads as fit, for the least latency
-  int nch = 0;
-  for (const int n : {1, 2, 4, 8})
-    if (!nch && threads_for(n) <= (n <= 2 ? 1024 : 512)) nch = n;
+  const int nch = threads_for(1) <= 1024 ? 1 : threads_for(2) <= 1024 ? 2 : threads_for(8) <= 512 ? 8 : 0;
   p.tpr = nch ? threads_for(nch) : 512;
   const int rpb = (127 + p.tpr) / p.tpr, threads = p.tpr * rpb;
   const int64_t grid = (p.rows + rpb - 1) / rpb;
@@ -690,7 +691,6 @@ oq_status norm_launch(const NormParams& p0, cudaStream_t st) {
   const unsigned ctas = (unsigned)grid + (p.rows % MX_ROWS ? 1u : 0u);
   auto kernel = nch == 1   ? mx_norm_kernel<T, BITS, 1>
                 : nch == 2 ? mx_norm_kernel<T, BITS, 2>
-                : nch == 4 ? mx_norm_kernel<T, BITS, 4>
                 : nch == 8 ? mx_norm_kernel<T, BITS, 8>
                            : mx_norm_kernel<T, BITS, 0>;
   return launch_status(mx_launch(kernel, dim3(ctas), threads, 0, 0, st, p), "oq_rms_norm_mx");
@@ -711,7 +711,7 @@ oq_status mx_quantize_launch(const void* x, int x_dtype, int64_t rows, int d, in
   const bool bf16 = x_dtype == OQ_DTYPE_BF16, wide = few_tiles(grid) || (bf16 && bits == 8);
   auto pick = [&](auto threads) {
     constexpr int QT = decltype(threads)::value;
-    return bf16 ? (bits == 4 ? mx_quantize_kernel<__nv_bfloat16, 4, QT> : mx_quantize_kernel<__nv_bfloat16, 8, QT>)
+    return bf16 ? (bits == 4 ? mx_quantize_kernel<__nv_bfloat16, 4, QT> : mx_quantize_kernel<__nv_bfloat16, 8, QT_WIDE>)
                 : (bits == 4 ? mx_quantize_kernel<float, 4, QT> : mx_quantize_kernel<float, 8, QT>);
   };
   auto kernel = wide ? pick(std::integral_constant<int, QT_WIDE>()) : pick(std::integral_constant<int, QT_DEEP>());
