@@ -334,6 +334,51 @@ def test_product_large_batches(env, T, d, n, y, bits):
     _product(env, T, d, n, bits, y)
 
 
+def _tile_width(T, n, sms):
+    """The large product's rule: the tile width whose waves over the CTA pairs cost least; and its waves."""
+    best = None
+    for w in (448, 320, 256, 192, 128):
+        waves = -(-(-(-T // 256) * -(-n // w)) // (sms // 2))
+        cost = waves * (16384 + 1024 + 72 * w)
+        if best is None or cost < best[0]:
+            best = (cost, w, waves)
+    return best[1:]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("y_dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,n,width,waves", [
+    (333, 1040, 128, 1), (500, 5104, 192, 1), (760, 5104, 256, 1), (1000, 5104, 320, 1), (5000, 1232, 448, 1),
+    # several tiles a pair: the accumulator is handed back, and the ring of stages goes on
+    (19001, 112, 128, 2), (19001, 368, 192, 3), (3000, 2864, 256, 2), (5000, 2000, 320, 2), (5000, 2480, 448, 2)])
+def test_product_of_every_tile_width(env, T, n, width, waves, y_dtype, bits):
+    # K of 17 column tiles: more stages than the ring holds at either width of
+    # codes, the last one of 4-bit codes half empty.  All of y against fp64
+    # products of the values that the codes stand for, in the module's bound.
+    torch, B = env
+    if torch.cuda.get_device_properties(0).multi_processor_count == 148:
+        assert _tile_width(T, n, 148) == (width, waves)
+    d = 2144
+    gen = torch.Generator(device="cuda").manual_seed(T + n)
+    x = torch.randn(T, d, generator=gen, device="cuda") * torch.exp(torch.randn(T, 1, generator=gen, device="cuda"))
+    x[:, 5] *= 30
+    w = torch.randn(n, d, generator=gen, device="cuda") * torch.exp(torch.randn(n, 1, generator=gen, device="cuda"))
+    args = (*B.oq_mx_quantize(x, bits), *B.oq_mx_quantize(w, 4))
+    layer = B.oq_layer_create(d, n, 0, bits, 4, B.OQ_FLAG_MICROSCALED)
+    y = torch.full((T, n), float("nan"), dtype=_dtype(torch, y_dtype), device="cuda")
+    assert B.oq_linear_mx(layer, *args, y=y) is y
+    a = B.oq_mx_dequantize(*args[:2], d, bits).double()
+    v = B.oq_mx_dequantize(*args[2:], d, 4).double()
+    exact = a @ v.T
+    tol = (d / 32 + 8) * 2.0 ** -23 * (a.abs() @ v.abs().T)
+    if y_dtype == "bf16":
+        tol += 2.0 ** -8 * exact.abs()
+    err = (y.double() - exact).abs()
+    assert bool((err <= tol).all()), f"worst {float((err / tol).max()):.3g} of the bound"
+    assert torch.equal(B.oq_linear_mx(layer, *args, y_dtype=_dtype(torch, y_dtype)), y)
+    B.oq_poll_error(layer)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("T", [1, 40, 200, 600])
 def test_product_is_exact_where_fp32_is(env, T, bits):
