@@ -252,9 +252,11 @@ __global__ void __launch_bounds__(QT) mx_dequantize_kernel(const __grid_constant
 //
 // All this holds while eps is at least NORM_EPS: then squares below 2^-126, and
 // what they round off (2^-150 each), do not count beside it.  A smaller eps
-// does not hide rows whose squares leave fp32's range, and such calls take the
-// second kernel, which forms those rows in fp64 throughout (norm_row_far; in the
-// first, a call in the loop would cost every row registers: 195 -> 254 us).
+// does not hide rows whose squares leave fp32's range; they are formed in fp64
+// throughout (norm_row_far).  The walking kernel has a form of its own for that
+// (FAR), because the looking costs every row: 195 us become 212, and a call
+// in the loop would make them 254 by its registers.  So it marks such rows, by
+// the scale code of their first block, and does them behind the loop.
 constexpr size_t NORM_SMEM = 224 * 1024;   // stages of the streaming kernel
 constexpr float NORM_EPS = 1e-35f;
 
@@ -554,9 +556,12 @@ __device__ __forceinline__ void copy_async16(void* dst_smem, const void* src) {
                : "memory");
 }
 
-template <typename T, int BITS, int NCH, bool RES>
+constexpr uint8_t FAR_ROW = 254;   // no block has it: scale codes end at 252
+
+template <typename T, int BITS, int NCH, bool RES, bool FAR>
 __global__ void __launch_bounds__(1024, 1) mx_norm_stream_kernel(const __grid_constant__ NormParams p) {
   __shared__ double part[2][32];
+  __shared__ int far_rows;   // FAR: this CTA has marked some (written before a barrier of the first row, and after)
   extern __shared__ __align__(16) unsigned char stage_mem[];
   dependency_wait();
   if ((int)blockIdx.x >= p.row_ctas) {
@@ -600,6 +605,7 @@ __global__ void __launch_bounds__(1024, 1) mx_norm_stream_kernel(const __grid_co
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  if (FAR && t == 0) far_rows = 0;
   int s = 0;
   fetch(true, stage_mem);
   T* r_out = RES && p.r_out ? static_cast<T*>(p.r_out) + (int64_t)blockIdx.x * p.d : nullptr;
@@ -616,7 +622,9 @@ __global__ void __launch_bounds__(1024, 1) mx_norm_stream_kernel(const __grid_co
       const float sq = sum_squares(h[k]);
       total += in[k] ? (double)sq : 0.0;
     }
-    const double rs64 = rsqrt64(row_sum(total, part[s], tpr >> 5, 0) * p.inv_d + (double)p.eps);
+    const double mean = row_sum(total, part[s], tpr >> 5, 0) * p.inv_d + (double)p.eps;
+    const bool far = FAR && !near_rsqrt64(mean);   // the same in all threads
+    const double rs64 = rsqrt64(mean);
     const f32x2 rs2 = pack2((float)rs64, (float)rs64);
     uint8_t* codes = p.codes + row * (cols * BITS / 8);
     uint8_t* scales = p.scales + (row >> 7) * (p.col_tiles * MX_TILE_BYTES) + 4 * mx_tile_word((int)row & (MX_ROWS - 1));
@@ -627,7 +635,7 @@ __global__ void __launch_bounds__(1024, 1) mx_norm_stream_kernel(const __grid_co
       f32x2 g[4];
       if constexpr (NCH != 2) load_gain(p, at[k], g);
       if (norm_vector<T, BITS, false>(p, h[k], NCH == 2 ? gain[k % 2] : g, nullptr, nullptr, col, in[k], col < cols, rs2, rs64,
-                                      r_out, codes, scales))
+                                      far ? nullptr : r_out, codes, scales))
         redo |= 1u << k;
     }
     // the warp's vectors next to a border, again from the stage, which nothing
@@ -641,21 +649,39 @@ __global__ void __launch_bounds__(1024, 1) mx_norm_stream_kernel(const __grid_co
       }
     }
     if (r_out) r_out += step;
+    if (far && t == 0) {   // (what the loop made of the row is overwritten)
+      *scales = FAR_ROW;
+      far_rows = 1;
+    }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if constexpr (FAR) {
+    __syncthreads();   // far_rows and the marks
+    if (!far_rows) return;
+    for (int64_t row = blockIdx.x; row < p.rows; row += p.row_ctas) {
+      uint8_t* scales = p.scales + (row >> 7) * (p.col_tiles * MX_TILE_BYTES) + 4 * mx_tile_word((int)row & (MX_ROWS - 1));
+      const bool marked = *scales == FAR_ROW;
+      __syncthreads();   // read by all before it is overwritten; part is free again
+      if (marked)
+        norm_row_far<T, BITS>(p, static_cast<const T*>(p.x) + row * p.d, RES ? static_cast<const T*>(p.r) + row * p.d : nullptr,
+                              RES && p.r_out ? static_cast<T*>(p.r_out) + row * p.d : nullptr,
+                              p.codes + row * (cols * BITS / 8), scales, t, tpr, part[0], 0, 1);
+    }
+  }
 }
 
 template <typename T, int BITS, int NCH, bool RES>
 oq_status norm_stream_launch(NormParams& p, int threads, int sms, int device, size_t smem, cudaStream_t st) {
-  static std::atomic<uint64_t> smem_set{0};
-  const oq_status ok = mx_allow_smem(reinterpret_cast<const void*>(mx_norm_stream_kernel<T, BITS, NCH, RES>), NORM_SMEM, device,
-                                     &smem_set);
+  static std::atomic<uint64_t> smem_set[2] = {};
+  const bool far = p.eps < NORM_EPS;
+  auto kernel = far ? mx_norm_stream_kernel<T, BITS, NCH, RES, true> : mx_norm_stream_kernel<T, BITS, NCH, RES, false>;
+  const oq_status ok = mx_allow_smem(reinterpret_cast<const void*>(kernel), NORM_SMEM, device, &smem_set[far]);
   if (ok != OQ_OK) return ok;
   // CTAs an SM holds: 64 registers a thread, 228 KB of shared memory with 1 KB a CTA of the system's and 512 bytes of sums
   const int resident = std::max(1, std::min(1024 / threads, (int)(228 * 1024 / (smem + 1024 + 512))));
   p.row_ctas = (int)std::min<int64_t>(p.rows, (int64_t)sms * resident);
   const unsigned grid = (unsigned)p.row_ctas + (p.rows % MX_ROWS ? 1u : 0u);
-  return launch_status(mx_launch(mx_norm_stream_kernel<T, BITS, NCH, RES>, dim3(grid), threads, smem, 0, st, p), "oq_rms_norm_mx");
+  return launch_status(mx_launch(kernel, dim3(grid), threads, smem, 0, st, p), "oq_rms_norm_mx");
 }
 
 template <typename T, int BITS>
@@ -666,7 +692,7 @@ oq_status norm_launch(const NormParams& p0, cudaStream_t st) {
   const int chunks = p.col_tiles * 16;   // vectors of eight, padding included
   auto threads_for = [&](int n) { return ((chunks + n - 1) / n + 31) / 32 * 32; };
   // the streaming kernel, where there are rows enough to walk over
-  if (p.rows > 2 * sms && p.eps >= NORM_EPS) {
+  if (p.rows > 2 * sms) {
     // Two vectors a thread, whose gains then stay in registers, where a CTA's
     // threads allow it; four for longer rows (12288 wide: 72.5 us with two, 76
     // with four).
