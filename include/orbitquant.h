@@ -473,8 +473,9 @@ oq_status oq_linear_fused_host(const oq_layer* layer, const void* x_host, int32_
  * weight rows are quantized by the same call.
  *
  * oq_mx_dequantize -- codes and scales back to x [rows, d] (bf16 or fp32,
- * 16-byte aligned): the values, exact in fp32, and in bf16 but for results
- * below its least normal number.
+ * 16-byte aligned): the values of what oq_mx_quantize and oq_rms_norm_mx write,
+ * exact in fp32, and in bf16 but for results below its least normal number.
+ * (Scales that no such call writes, codes 247 to 254, may overflow to infinities.)
  */
 size_t oq_mx_codes_size(int64_t rows, int32_t d, int32_t bits);
 size_t oq_mx_scales_size(int64_t rows, int32_t d);
@@ -516,7 +517,8 @@ oq_status oq_rms_norm_mx(const void* x, const void* residual, int32_t x_dtype, c
  *   y                device [T, d_out], fp32 or bf16 as y_dtype says (the fp32
  *                    sum rounded to nearest even), 16-byte aligned.
  * The tensor cores multiply the codes and apply the scales; sums are fp32 in
- * tensor memory.  Results repeat bit for bit.  A NaN block makes the rows (or
+ * tensor memory, where an addition may truncate instead of rounding (2^-23 of
+ * the magnitudes added).  Results repeat bit for bit.  A NaN block makes the rows (or
  * columns) of y that it enters NaN.  The layer must belong to the current
  * device.  A bounded wait that runs out is reported by oq_poll_error.
  */

@@ -262,9 +262,12 @@ oq_status mx_small_launch(const MxGemmArgs& g, void* stream);
 // Batches that take the small-batch kernel: up to 128 tokens, and up to 256
 // where K runs over more than 24 stages (of 256 4-bit or 128 8-bit elements), so
 // that splitting K pays for the exchange of 256 tokens' sums.  Measured at 256
-// tokens (us, small / pairs): 13824 -> 5120 17.1 / 24.7 (4 bits, 54 stages), 22.9
-// / 44.1 (8 bits, 108); 5120 -> 5120 13.0 / 12.0 (20), 15.3 / 20.0 (40); 2048 ->
-// 1040 10.2 / 7.4 (8), 10.9 / 10.2 (16).  At 300 tokens the pairs are even or ahead.
+// tokens (us, small / pairs): 13824 -> 5120 18.8 / 21.4 (4 bits, 54 stages), 25.0
+// / 38.5 (8 bits, 108); 5120 -> 5120 13.5 / 10.3 (20), 15.5 / 16.6 (40); 2048 ->
+// 1040 9.6 / 6.0 (8), 10.5 / 8.3 (16).  The rule does not look at the outputs'
+// width, which fills the pairs by itself: 5120 -> 13824 25.0 / 18.0 (8 bits, 40).
+// At 129 tokens the two are even where the rule takes pairs (5120 -> 5120, 4 bits
+// 9.7 / 10.2; 2048 -> 1040, 8 bits 7.8 / 8.2).
 inline bool mx_small_batch(int64_t T, int K, int a_bits) {
   return T <= 128 || (T <= 256 && mx_col_tiles(K) * a_bits / 8 > 24);
 }

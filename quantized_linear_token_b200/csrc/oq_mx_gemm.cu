@@ -22,9 +22,12 @@
 // for three stages at a time (about 230 cycles a check).  Measured: 881 cycles a
 // stage, and 2100 from one tile's last MMA issued to the next one's first.
 //
-// 32760 x 5120 -> 5120 with 4-bit activations: 288 us alone (6.0 PFLOP/s), 333 us
+// 32760 x 5120 -> 5120 with 4-bit activations: 291 us alone (5.9 PFLOP/s), 339 us
 // in a stream of such calls, where the 1000 W limit holds the clock at 1.46 GHz;
-// 4096 x 13824 -> 5120 with 8-bit activations: 195 and 229 us (3.0, 2.5).
+// 4096 x 13824 -> 5120 with 8-bit activations: 210 us with cold caches and 228 in
+// a stream (2.8, 2.5).  K is not split: between 257 and some 2000 tokens one tile
+// a pair leaves fill, mainloop and drain in series and pairs idle (512 x 5120 ->
+// 5120: 11.2 us at 4 bits, 17.4 at 8, on 54 of 74 pairs).
 //
 // Scales: a 512-byte tile (128 rows x 4 blocks) is one tcgen05.cp into four
 // tensor-memory columns.  The pair's weight rows start at a multiple of 64, so

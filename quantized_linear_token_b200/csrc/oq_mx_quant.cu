@@ -29,8 +29,10 @@ oq_status launch_status(cudaError_t e, const char* what) {
 // 5120 bf16 in 4 bits 67 us, 6.4 TB/s (98 % of a copy's rate); a few tiles 2 us.
 //
 // 256 threads, or 512 with half as many rows each: where there are only a few
-// tiles for an SM (1001 x 2016 in 8 bits 2.8 -> 2.4 us), and for bf16 rows in 8
-// bits (32760 x 5120 87 -> 81 us; in 4 bits 78 -> 81, fp32 32 -> 34 at 8192 x 5120).
+// tiles for an SM (bf16 in 4 bits, quantise / read back, 256 -> 512 threads: 200
+// tiles 4.3 -> 3.7 / 3.4 -> 3.2 us, 600 tiles 7.0 -> 6.2 / 7.0 -> 6.2, 1200 tiles
+// 10.8 -> 10.4 / 9.9 -> 10.3, 10240 tiles 66.4 -> 67.9 / 66.5 -> 68.1), and for
+// quantising bf16 rows to 8 bits (5000 tiles 38.2 -> 37.4, 10240 75.0 -> 73.8).
 constexpr int QT_WIDE = 512, QT_DEEP = 256;
 
 // the tile of this CTA: row tile, column tile, and how many of this thread's rows exist
@@ -231,14 +233,17 @@ __global__ void __launch_bounds__(QT) mx_dequantize_kernel(const __grid_constant
 // tpr threads own a row, each NCH vectors of eight neighbouring elements that
 // stay in registers between the sum and the quantisation (one pass over x and
 // r).  Two kernels:
-//   - rows by the hundred: CTAs stay and walk over rows, and every thread copies
+//   - many rows (more than two an SM) of more than 1536 columns (which make a
+//     CTA of 128 threads): CTAs stay and walk over rows, and every thread copies
 //     its vectors of the next row into its own places in shared memory
 //     (cp.async) while it works on this one.  Loads are then in flight all the
-//     time without holding registers, and no barrier is about the data
-//     (32760 x 5120 bf16, residual kept: 195 us, 6.0 TB/s; 337 us with a CTA a row).
-//   - few rows, or rows too long for two stages of shared memory: a CTA a row,
-//     straight from global memory.  NCH = 0 reads x and r a second time instead
-//     of keeping them (rows too long for the registers).
+//     time without holding registers, and no barrier is about the data (32760 x
+//     5120 bf16, residual kept: 195 us, 6.1 TB/s; 552 us with a CTA a row).
+//   - other rows (few, narrow, or too long for two stages of shared memory): a
+//     CTA a row, or as many as make 128 threads, straight from global memory
+//     (32760 rows of 768 columns 61 us, 2.9 TB/s; of 1664, walked over, 73 us,
+//     5.2).  NCH = 0 reads x and r a second time instead of keeping them (rows
+//     too long for the registers).
 // A thread re-reads only elements that it alone writes, so the kept residual may
 // overwrite either input everywhere.
 //
@@ -419,8 +424,8 @@ __device__ __forceinline__ bool norm_vector(const NormParams& p, const f32x2 (&v
   unpack8(n, w);
   // Borders between codes, in the bits of w = n / scale: for e4m3 the middle of
   // the low 20 mantissa bits; for e2m1 the zero of the low 21 (the borders of
-  // its least steps among them).  e4m3's subnormals, 2^-15 of the block's
-  // largest and less, are left out.
+  // its least steps among them).  e4m3's subnormals, below 2^-14 of the block's
+  // largest, are left out: they keep the codes of the fp32 n.
   constexpr int SHIFT = BITS == 4 ? 11 : 12;
   constexpr uint32_t OFFSET = (BITS == 4 ? 4u : 4u - 0x80000u) << SHIFT;
   uint32_t near = 0xFFFFFFFFu;

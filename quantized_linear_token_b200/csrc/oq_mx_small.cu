@@ -10,11 +10,14 @@
 // deep, loading the peers' sums instead took a third of the kernel.)  4-bit activations use kind::mxf4, 8-bit ones
 // kind::mxf8f6f4 with the weights' codes spread to 8-bit containers by TMA.
 //
-// Measured back to back, weights from HBM: one token 13824 -> 5120 (4 bits) 12.1
-// us, 3.1 TB/s of weights (5.7 us at the copy bandwidth; the rest is launch, first
-// loads and the 570 cycles that a stage's four scale copies and MMAs take to
-// issue); 16 tokens 5120 -> 5120 7.1 us; 256 tokens 13824 -> 5120 with 8-bit
-// activations 25 us (MMAs 10 us on 120 SMs, exchange and sums 6 us).
+// Measured back to back, weights from HBM (600 MB of them in turn): one token
+// 13824 -> 5120 (4 bits) 11.9 us, 3.2 TB/s of weights (5.7 us at the copy
+// bandwidth; the rest is launch, first loads, the 570 cycles that a stage's four
+// scale copies and MMAs take to issue, and the cluster's two barriers); 16 tokens
+// 5120 -> 5120 8.7 us (6.9 with the weights in L2); 256 tokens 13824 -> 5120 with
+// 8-bit activations 25 us.  Each of its 40 weight tiles brings in the whole batch:
+// 36 stages of 41.5 KB a CTA, 15 us at the 99 bytes a nanosecond that an SM takes
+// from L2, beside 10 us of MMAs on 120 SMs and 6 us of exchange and sums.
 //
 // Warps: 0-3 epilogue, 4 TMA producer, 5 tensor memory and MMAs.
 #include <algorithm>
@@ -300,8 +303,10 @@ __global__ void __launch_bounds__(NTHREADS, BN <= 64 ? 2 : 1) mx_small_kernel(co
   if (split > 1) cluster_wait();   // no CTA leaves before its sums have been copied out
 }
 
-// CTAs that split a weight tile's K range: as many as fill the SMs, each with
-// at least two stages
+// CTAs that split a weight tile's K range: as many as the SMs' slots hold, each
+// with at least two stages.  (Slots are counted, not clusters: whether all
+// clusters are resident at once also depends on how their CTAs fit the GPCs.
+// They need not be; clusters do not wait for one another.)
 int choose_split(int m_tiles, int64_t t_tiles, int nkb, int slots, int most) {
   int best = 1;
   for (int s = 2; s <= most; ++s)
