@@ -211,8 +211,10 @@ FAR = 2.0 ** -40
     (26, 160, "fp32", 8, True, 0.0), (27, 512, "fp32", 4, False, 0.0), (26, 768, "bf16", 8, True, 0.0),
     (30, 2080, "bf16", 8, True, 2.0 ** -140), (14, 12288, "fp32", 8, False, 0.0), (13, 20032, "bf16", 4, True, 0.0),
     (13, 40992, "fp32", 8, True, 0.0),
-    # many rows
+    # rows that CTAs walk over, one or several each
     (320, 2080, "bf16", 8, True, 0.0), (1300, 2016, "fp32", 4, True, 2.0 ** -117), (310, 17312, "bf16", 8, True, 0.0),
+    (1300, 2016, "bf16", 4, False, 0.0), (1501, 1568, "fp32", 8, False, 0.0), (450, 17312, "fp32", 8, False, 0.0),
+    (900, 5120, "fp32", 8, True, 1e-36),
     # an eps beside which such rows do not count
     (320, 2080, "bf16", 8, True, 2.0 ** -116), (1300, 2016, "fp32", 4, True, 2.0 ** -116),
     (303, 17312, "fp32", 8, False, 1e-30)])
@@ -255,7 +257,7 @@ def test_norm_of_rows_whose_squares_leave_fp32(env, rows, d, dtype, bits, residu
         assert np.array_equal(_np(kept), R.bf16(sums) if dtype == "bf16" else sums)
 
 
-@pytest.mark.parametrize("rows", [6, 400])
+@pytest.mark.parametrize("rows", [6, 400, 1500])
 def test_norm_of_far_rows_in_place(env, rows):
     torch, B = env
     rng = np.random.default_rng(rows)
