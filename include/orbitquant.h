@@ -525,6 +525,146 @@ oq_status oq_rms_norm_mx(const void* x, const void* residual, int32_t x_dtype, c
 oq_status oq_linear_mx(const oq_layer* layer, const uint8_t* codes, const uint8_t* scales, int64_t T,
                        const uint8_t* Wcodes, const uint8_t* Wscales, void* y, int32_t y_dtype, void* stream);
 
+/*
+ * Operators around attention (the pages have no counterpart: what a transformer
+ * block runs between its QKV projection and its output projection, for streams
+ * whose keys and values stay in memory in 4 bits).
+ *
+ * oq_qk_norm_rope -- the norm of queries and keys for each head and the rotation
+ * by position, in one pass:
+ *   n_i = x_i g_i / sqrt(mean(x^2) + eps) over a head's head_dim channels, then
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for the first `rot` channels, pairs
+ *   (i, i + rot / 2), or (2 i, 2 i + 1) with OQ_QK_INTERLEAVED.
+ *   q, k          device [T, heads, head_dim], bf16 or fp32 (dtype for both and
+ *                 their outputs); q_stride, k_stride are elements from one token
+ *                 to the next, so both may be views of a projection's output.
+ *                 Either may be left out (0 heads, null).
+ *   q_gain, k_gain  device [head_dim] of gain_dtype, or null (ones).
+ *                 With OQ_QK_NO_NORM n = x, and there are no gains.
+ *   table         device fp32 [table_rows, rot / 2, 2] (cos, sin), or null: no
+ *                 rotation.  positions: device int32 [T], the row for each token,
+ *                 or null: row t for token t.  A position outside the table makes
+ *                 the token's rotated channels NaN.
+ *   q_out, k_out  as q, k, with token strides of their own; an output may be its
+ *                 own input (same pointer and stride).
+ * head_dim % 8 == 0 up to 256; rot % 16 == 0 (interleaved: % 8); strides multiples
+ * of 16 bytes; pointers 16-byte aligned.  fp32 arithmetic, one rounding at the end;
+ * rows whose squares leave fp32's range are formed in fp64.
+ */
+enum { OQ_QK_INTERLEAVED = 1, OQ_QK_NO_NORM = 2 };
+oq_status oq_qk_norm_rope(const void* q, int64_t q_stride, int32_t q_heads, const void* k, int64_t k_stride, int32_t k_heads,
+                          int32_t dtype, int64_t T, int32_t head_dim, const void* q_gain, const void* k_gain,
+                          int32_t gain_dtype, float eps, const float* table, int64_t table_rows, int32_t rot,
+                          const int32_t* positions, int32_t flags, void* q_out, int64_t q_out_stride, void* k_out,
+                          int64_t k_out_stride, void* stream);
+
+/*
+ * oq_kv4 -- a shape of attention (heads query heads, kv_heads key heads, each
+ * read by heads / kv_heads query heads; head_dim 64 or 128) and the device error
+ * word of its calls.  The cache itself is the caller's:
+ *   cache       device, pages of 128 tokens, oq_kv4_cache_size(kv, pages) bytes,
+ *               32-byte aligned.  Microscaled e2m1 as oq_mx_quantize writes it:
+ *               one E8M0 scale for 32 channels of a token's head.  The heads of a
+ *               token lie side by side in groups of 128 channels (the last group's
+ *               missing head is zero); a page holds for each group 272 rows of 64
+ *               bytes:
+ *                 0-127    K codes, a token's 128 channels a row (even channel low)
+ *                 128-255  V codes, a channel's 128 tokens a row (even token low)
+ *                 256-263  K scales, byte [token % 32][token / 32][channel / 32]
+ *                 264-271  V scales, byte [token][channel / 32]
+ *   page_table  device int32 [B, table_width]: the page of tokens 128 i .. of a
+ *               sequence.  An entry outside [0, pages) is a page that is not
+ *               there: nothing is written to it, its tokens are not seen.
+ *   cu          device int32 [B + 1]: sequence b's tokens in this call are rows
+ *               cu[b] .. cu[b + 1] - 1 of q, k, v and y.
+ *   lens        device int32 [B]: tokens of the sequence in the cache, this call's
+ *               among them; those are its last ones.  (Sequences with more than
+ *               128 table_width tokens end there.)
+ * Pages may be shared by sequences that only read them.  Calls on one handle may
+ * overlap and be captured into graphs; calls that write a page must not overlap
+ * calls that use it.  oq_kv4_create allocates on the current device; the other
+ * calls must run on that device.
+ *
+ * oq_kv4_append -- this call's keys and values to the cache, with the norm and
+ * rotation of oq_qk_norm_rope on queries and keys:
+ *   q, k, v   device [T, heads or kv_heads, head_dim] of dtype with token strides;
+ *             q may be null (with q_out).
+ *   q_out     device bf16 [T, heads, head_dim], contiguous; may be q itself where
+ *             that is bf16 and contiguous.
+ *   positions null: each token's place in its sequence.
+ * The codes of a key are those of its value in exact arithmetic.  Tokens without a
+ * page, and those of a sequence whose lens is below its tokens, are not stored.
+ *
+ * oq_kv4_read -- the values that this call's tokens have in the cache, [T,
+ * kv_heads, head_dim] of dtype (exact; NaN where a page is not there).
+ *
+ * oq_kv4_attention -- y = softmax(scale q K^T + mask) V over the cache:
+ *   q         device bf16 [T, heads, head_dim] with a token stride.
+ *   max_q     at least the largest number of tokens of a sequence in this call;
+ *             tokens past it get no output.
+ *   max_len   about the longest sequence: how the work is split depends on it,
+ *             the values only by rounding.
+ *   scale     positive.
+ *   flags     OQ_ATTN_CAUSAL: a token sees its sequence up to itself; otherwise
+ *             all of it.  window > 0: only tokens less than `window` before it.
+ *   y         device bf16 [T, heads, head_dim].  A token that sees nothing gets 0.
+ *   workspace device scratch of oq_kv4_attention_workspace_size bytes (may be 0),
+ *             256-byte aligned; calls that share it must not overlap.
+ * Queries enter exactly, softmax and sums are fp32, the weights are rounded to 8
+ * bits like bf16's (relative to the largest of 32 neighbouring tokens).  |V| from
+ * 2^-90 to 2^90, or 0.  A NaN in a key or value reaches the queries that see it.
+ * Results repeat bit for bit.  A bounded wait that runs out is reported by
+ * oq_kv4_poll_error.
+ */
+typedef struct oq_kv4 oq_kv4;
+enum { OQ_ATTN_CAUSAL = 1 };
+oq_status oq_kv4_create(int32_t heads, int32_t kv_heads, int32_t head_dim, oq_kv4** out);
+void oq_kv4_destroy(oq_kv4* kv);
+size_t oq_kv4_cache_size(const oq_kv4* kv, int64_t pages);
+oq_status oq_kv4_append(const oq_kv4* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, int32_t dtype, int64_t T, const void* q_gain, const void* k_gain,
+                        int32_t gain_dtype, float eps, const float* table, int64_t table_rows, int32_t rot,
+                        const int32_t* positions, int32_t flags, void* q_out, uint8_t* cache, int64_t pages,
+                        const int32_t* page_table, int32_t table_width, const int32_t* cu, const int32_t* lens, int32_t B,
+                        void* stream);
+oq_status oq_kv4_read(const oq_kv4* kv, const uint8_t* cache, int64_t pages, const int32_t* page_table, int32_t table_width,
+                      const int32_t* cu, const int32_t* lens, int32_t B, int64_t T, void* k, void* v, int32_t dtype,
+                      void* stream);
+size_t oq_kv4_attention_workspace_size(const oq_kv4* kv, int64_t T, int32_t B, int32_t max_q, int32_t max_len);
+oq_status oq_kv4_attention(const oq_kv4* kv, const void* q, int64_t q_stride, int64_t T, const uint8_t* cache, int64_t pages,
+                           const int32_t* page_table, int32_t table_width, const int32_t* cu, const int32_t* lens, int32_t B,
+                           int32_t max_q, int32_t max_len, float scale, int32_t flags, int32_t window, void* y,
+                           void* workspace, size_t workspace_bytes, void* stream);
+/* Reads and clears the handle's device error word, as oq_poll_error does a layer's. */
+oq_status oq_kv4_poll_error(const oq_kv4* kv);
+
+/*
+ * Products with 4-bit weights that have a scale for each group of neighbours in a
+ * row (the INT4 weight-only layer has one a row), for few tokens:
+ *   y[t, o] = sum_g s[o, g] sum_{i in g} (c[o, i] - z[o, g]) x[t, i]
+ *   group   32, 64 or 128, a divisor of d_in.
+ *   codes   device [d_out, d_in rounded up to 128, / 2] bytes.  In each run of 128
+ *           elements (64 bytes) the 32-bit word 4 q + s holds elements 32 s + 8 q
+ *           to + 7, and its nibble p the element 2 (p % 4) + p / 4 of those.
+ *   scales  device bf16 [d_out, d_in / group].
+ *   zeros   device uint8 [d_out, d_in / group], 0 to 15, or null: 8 throughout.
+ *
+ * oq_w4g_prepare -- codes W [d_out, d_in] (fp32 or bf16), in fp32 with IEEE
+ * division: without zeros s = bf16(max|w| / 7), c = clamp(round(w / s) + 8); with
+ * zeros s = bf16((max(w, 0) - min(w, 0)) / 15), z = round(-min(w, 0) / s), c =
+ * clamp(round(w / s) + z), all clamped to 0 .. 15, halves to even.  A group that
+ * holds an infinity or a NaN gets scale NaN; one whose scale is 0 reads as zeros.
+ *
+ * oq_linear_w4g -- x [T, d_in], y [T, d_out], each bf16 or fp32.  Products are
+ * exact (fp32 tokens too), sums fp32.  Results repeat bit for bit.  A call streams
+ * the weights once for 32 tokens (10 in fp32).
+ */
+oq_status oq_w4g_prepare(const void* W, int32_t W_dtype, int32_t d_out, int32_t d_in, int32_t group, uint8_t* codes,
+                         void* scales, uint8_t* zeros, void* stream);
+oq_status oq_linear_w4g(const void* x, int32_t x_dtype, int64_t T, int32_t d_in, int32_t d_out, int32_t group,
+                        const uint8_t* codes, const void* scales, const uint8_t* zeros, void* y, int32_t y_dtype,
+                        void* stream);
+
 /* Reads and clears the layer's device error word.  Synchronizes the device.
  * Returns OQ_OK or OQ_ERR_TIMEOUT (OQ_ERR_DEVICE for a bit this version does
  * not define). */

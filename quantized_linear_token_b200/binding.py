@@ -24,6 +24,10 @@ OQ_FLAG_GAUSSIAN_MARGINAL = 2
 OQ_FLAG_WEIGHT_ONLY_INT4 = 4
 OQ_FLAG_FP8_CONTRACTION = 8
 OQ_FLAG_MICROSCALED = 16
+OQ_QK_INTERLEAVED = 1
+OQ_QK_NO_NORM = 2
+OQ_ATTN_CAUSAL = 1
+OQ_KV4_PAGE = 128      # tokens of a page of the 4-bit cache
 # oq_linear_fused decodes the weight codes once per call from this many tokens
 # on (bf16 x, d_out % 256 == 0, a workspace of oq_linear_fused_workspace_size)
 W16_MIN_T = 1024
@@ -37,6 +41,8 @@ EXPORTS = (
     "oq_rotate_quantize_levels", "oq_linear_levels", "oq_weight_levels", "oq_linear_decoded",
     "oq_linear_fused_static", "oq_linear_fused_host_workspace_size", "oq_linear_fused_host",
     "oq_mx_codes_size", "oq_mx_scales_size", "oq_mx_quantize", "oq_mx_dequantize", "oq_rms_norm_mx", "oq_linear_mx",
+    "oq_qk_norm_rope", "oq_kv4_create", "oq_kv4_destroy", "oq_kv4_cache_size", "oq_kv4_append", "oq_kv4_read",
+    "oq_kv4_attention_workspace_size", "oq_kv4_attention", "oq_kv4_poll_error", "oq_w4g_prepare", "oq_linear_w4g",
     "oq_poll_error", "oq_check_wait_timeout", "oq_last_error", "oq_status_string",
 )
 
@@ -107,6 +113,20 @@ def load_library(path: str = LIB_PATH):
         "oq_mx_dequantize": (i32, [vp, vp, i64, i32, i32, vp, i32, vp]),
         "oq_rms_norm_mx": (i32, [vp, vp, i32, vp, i32, ctypes.c_float, i64, i32, i32, vp, vp, vp, vp]),
         "oq_linear_mx": (i32, [vp, vp, vp, i64, vp, vp, vp, i32, vp]),
+        "oq_qk_norm_rope": (i32, [vp, i64, i32, vp, i64, i32, i32, i64, i32, vp, vp, i32, ctypes.c_float, vp, i64, i32, vp,
+                                  i32, vp, i64, vp, i64, vp]),
+        "oq_kv4_create": (i32, [i32, i32, i32, ctypes.POINTER(vp)]),
+        "oq_kv4_destroy": (None, [vp]),
+        "oq_kv4_cache_size": (sz, [vp, i64]),
+        "oq_kv4_append": (i32, [vp, vp, i64, vp, i64, vp, i64, i32, i64, vp, vp, i32, ctypes.c_float, vp, i64, i32, vp, i32,
+                                vp, vp, i64, vp, i32, vp, vp, i32, vp]),
+        "oq_kv4_read": (i32, [vp, vp, i64, vp, i32, vp, vp, i32, i64, vp, vp, i32, vp]),
+        "oq_kv4_attention_workspace_size": (sz, [vp, i64, i32, i32, i32]),
+        "oq_kv4_attention": (i32, [vp, vp, i64, i64, vp, i64, vp, i32, vp, vp, i32, i32, i32, ctypes.c_float, i32, i32, vp,
+                                   vp, sz, vp]),
+        "oq_kv4_poll_error": (i32, [vp]),
+        "oq_w4g_prepare": (i32, [vp, i32, i32, i32, i32, vp, vp, vp, vp]),
+        "oq_linear_w4g": (i32, [vp, i32, i64, i32, i32, i32, vp, vp, vp, vp, i32, vp]),
         "oq_poll_error": (i32, [vp]),
         "oq_check_wait_timeout": (i32, [vp, ctypes.c_uint32, vp]),
         "oq_last_error": (ctypes.c_char_p, []),
@@ -600,6 +620,273 @@ def oq_linear_mx(layer: Layer, codes, scales, Wcodes, Wscales, y=None, y_dtype=N
         py = _mx_rows(y, (T, n), y.dtype if y_dtype is None else y_dtype, device, "y")
     ycode = _mx_dtype(y)
     _launch("oq_linear_mx", device, layer.handle, *pointers, py, ycode)
+    return y
+
+
+# ------------------------------------------------------------------ operators around attention
+def _heads(t, heads, D: int, device, name: str):
+    """(address, token stride) of a [T, heads, D] tensor whose tokens' heads are contiguous."""
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads) or t.device != device:
+        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {D}] on {device}")
+    s = t.stride()
+    if t.numel() and ((D > 1 and s[2] != 1) or (t.shape[1] > 1 and s[1] != D)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), s[0] if t.shape[0] > 1 else t.shape[1] * D
+
+
+def _ints(t, shape, device, name: str) -> int:
+    """The address of a contiguous int32 tensor of this shape on `device`."""
+    if t.dtype is not _torch().int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _qk_args(q_gain, k_gain, table, positions, T: int, D: int, interleaved: bool, norm: bool, device):
+    """The arguments that norm and rotation share: gains .. gain type; table .. flags."""
+    torch = _torch()
+    gdt, gains = OQ_DTYPE_F32, [None, None]
+    for i, g in enumerate((q_gain, k_gain)):
+        if g is not None:
+            if g.dtype is not (q_gain if q_gain is not None else k_gain).dtype:
+                raise ValueError("q_gain and k_gain must have one type")
+            gdt, gains[i] = _mx_dtype(g), _mx_rows(g, (D,), g.dtype, device, "qk"[i] + "_gain")
+    pt, rows, rot, pp = None, 0, 0, None
+    if table is not None:
+        if table.dim() != 3 or table.shape[2] != 2 or table.dtype is not torch.float32 or table.device != device \
+                or not table.is_contiguous():
+            raise ValueError(f"table must be contiguous float32 [positions, rot / 2, 2] on {device}")
+        pt, rows, rot = table.data_ptr(), table.shape[0], 2 * table.shape[1]
+        if positions is not None:
+            pp = _ints(positions, (T,), device, "positions")
+    elif positions is not None:
+        raise ValueError("positions without a table")
+    flags = (OQ_QK_INTERLEAVED if interleaved else 0) | (0 if norm else OQ_QK_NO_NORM)
+    return (gains[0], gains[1], gdt), (pt, rows, rot, pp, flags)
+
+
+def oq_qk_norm_rope(q, k=None, q_gain=None, k_gain=None, eps: float = 1e-6, table=None, positions=None,
+                    interleaved: bool = False, norm: bool = True, q_out=None, k_out=None):
+    """Norm for each head and rotation by position of q [T, heads, D] and k
+    [T, kv_heads, D] (bf16/fp32, CUDA; a token's heads contiguous, tokens at any
+    stride) -> (q_out, k_out) of the same types.  table: fp32 [positions, rot / 2,
+    2] (cos, sin); positions: int32 [T], its row for each token (default: t).
+    An output may be its input."""
+    torch = _torch()
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [T, heads, D]")
+    T, H, D = q.shape
+    device, dt = q.device, _mx_dtype(q)
+    pq, sq = _heads(q, None, D, device, "q")
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=q.dtype, device=device)
+    elif q_out.dtype is not q.dtype or q_out.shape != q.shape:
+        raise ValueError("q_out must have q's type and shape")
+    pqo, sqo = _heads(q_out, H, D, device, "q_out")
+    pk = pko = None
+    sk = sko = KH = 0
+    if k is not None:
+        if k.dtype is not q.dtype or k.dim() != 3 or k.shape[0] != T:
+            raise ValueError("k must have q's type and tokens")
+        KH = k.shape[1]
+        pk, sk = _heads(k, None, D, device, "k")
+        if k_out is None:
+            k_out = torch.empty((T, KH, D), dtype=k.dtype, device=device)
+        elif k_out.dtype is not k.dtype or k_out.shape != k.shape:
+            raise ValueError("k_out must have k's type and shape")
+        pko, sko = _heads(k_out, KH, D, device, "k_out")
+    elif k_out is not None or k_gain is not None:
+        raise ValueError("k_out or k_gain without k")
+    gains, turn = _qk_args(q_gain, k_gain, table, positions, T, D, interleaved, norm, device)
+    _launch("oq_qk_norm_rope", device, pq, sq, H, pk, sk, KH, dt, T, D, *gains, eps, *turn, pqo, sqo, pko, sko)
+    return q_out, k_out
+
+
+class Kv4:
+    """Owns an oq_kv4* (a shape of attention over a 4-bit cache and its error word)."""
+
+    def __init__(self, handle: int, lib, heads: int, kv_heads: int, head_dim: int):
+        self._h = ctypes.c_void_p(handle)
+        self._lib = lib
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        self.groups = (kv_heads * head_dim + 127) // 128
+
+    @property
+    def handle(self):
+        return self._h
+
+    def cache(self, pages: int, device=None):
+        """A new cache of so many pages of 128 tokens, zeroed: uint8 [pages, groups, 272, 64]."""
+        torch = _torch()
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        return torch.zeros((pages, self.groups, 272, 64), dtype=torch.uint8, device=device)
+
+    def close(self):
+        if self._h:
+            self._lib.oq_kv4_destroy(self._h)
+            self._h = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def oq_kv4_create(heads: int, kv_heads: int, head_dim: int) -> Kv4:
+    L = load_library()
+    h = ctypes.c_void_p()
+    _check(L.oq_kv4_create(heads, kv_heads, head_dim, ctypes.byref(h)), "oq_kv4_create")
+    return Kv4(h.value, L, heads, kv_heads, head_dim)
+
+
+def oq_kv4_destroy(kv: Kv4) -> None:
+    kv.close()
+
+
+def oq_kv4_cache_size(kv: Kv4, pages: int) -> int:
+    return int(load_library().oq_kv4_cache_size(kv.handle, pages))
+
+
+def _kv4_view(kv: Kv4, cache, page_table, cu, lens, device):
+    """cache, pages, page table, its width, cu, lens, B as the C calls take them."""
+    if cache.dim() != 4:
+        raise ValueError("cache must be [pages, groups, 272, 64]")
+    pages = cache.shape[0]
+    pc = _mx_ptr(cache, (pages, kv.groups, 272, 64), device, "cache")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, pages of a sequence]")
+    B, width = page_table.shape
+    return (pc, pages, _ints(page_table, (B, width), device, "page_table"), width, _ints(cu, (B + 1,), device, "cu"),
+            _ints(lens, (B,), device, "lens"), B)
+
+
+def oq_kv4_append(kv: Kv4, q, k, v, cache, page_table, cu, lens, q_gain=None, k_gain=None, eps: float = 1e-6, table=None,
+                  positions=None, interleaved: bool = False, norm: bool = True, q_out=None):
+    """Keys and values [T, kv_heads, D] of new tokens to the cache, with the norm
+    and rotation of oq_qk_norm_rope on queries and keys; q [T, heads, D] (or None)
+    -> q_out bf16 [T, heads, D].  positions: default, each token's place in its
+    sequence.  See include/orbitquant.h for cache, page_table, cu and lens."""
+    torch = _torch()
+    if k.dim() != 3 or not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor [T, kv_heads, D]")
+    T, D, device, dt = k.shape[0], kv.head_dim, k.device, _mx_dtype(k)
+    pk, sk = _heads(k, kv.kv_heads, D, device, "k")
+    pv, sv = _heads(v, kv.kv_heads, D, device, "v")
+    if v.dtype is not k.dtype or v.shape[0] != T:
+        raise ValueError("v must have k's type and tokens")
+    pq = pqo = None
+    sq = 0
+    if q is not None:
+        if q.dtype is not k.dtype or q.dim() != 3 or q.shape[0] != T:
+            raise ValueError("q must have k's type and tokens")
+        pq, sq = _heads(q, kv.heads, D, device, "q")
+        if q_out is None:
+            q_out = torch.empty((T, kv.heads, D), dtype=torch.bfloat16, device=device)
+            pqo = q_out.data_ptr()
+        else:
+            pqo = _mx_rows(q_out, (T, kv.heads, D), torch.bfloat16, device, "q_out")
+    elif q_out is not None or q_gain is not None:
+        raise ValueError("q_out or q_gain without q")
+    gains, turn = _qk_args(q_gain, k_gain, table, positions, T, D, interleaved, norm, device)
+    _launch("oq_kv4_append", device, kv.handle, pq, sq, pk, sk, pv, sv, dt, T, *gains, eps, *turn, pqo,
+            *_kv4_view(kv, cache, page_table, cu, lens, device))
+    return q_out
+
+
+def oq_kv4_read(kv: Kv4, cache, page_table, cu, lens, T: int, dtype=None, k=None, v=None):
+    """The values (fp32 by default, or bf16) that a call's T tokens have in the
+    cache -> (k, v) [T, kv_heads, D]."""
+    torch = _torch()
+    device, shape = cache.device, (T, kv.kv_heads, kv.head_dim)
+    if device.type != "cuda":
+        raise ValueError("cache must be a CUDA tensor")
+    dtype = dtype if dtype is not None else k.dtype if k is not None else torch.float32
+    out = []
+    for name, t in (("k", k), ("v", v)):
+        t = torch.empty(shape, dtype=dtype, device=device) if t is None else t
+        _mx_rows(t, shape, dtype, device, name)
+        out.append(t)
+    _launch("oq_kv4_read", device, kv.handle, *_kv4_view(kv, cache, page_table, cu, lens, device), T, out[0].data_ptr(),
+            out[1].data_ptr(), _mx_dtype(out[0]))
+    return out[0], out[1]
+
+
+def oq_kv4_attention_workspace_size(kv: Kv4, T: int, B: int, max_q: int, max_len: int) -> int:
+    return int(load_library().oq_kv4_attention_workspace_size(kv.handle, T, B, max_q, max_len))
+
+
+def oq_kv4_attention(kv: Kv4, q, cache, page_table, cu, lens, max_q: int, max_len: int = 0, scale=None, causal: bool = True,
+                     window: int = 0, y=None, workspace=None):
+    """softmax(scale q K^T + mask) V over the 4-bit cache: q [T, heads, D] bf16
+    (CUDA, any token stride) -> y bf16 [T, heads, D].  max_q: the most tokens of a
+    sequence in this call; max_len: about the longest sequence (default: what the
+    page table holds); scale: default D^-0.5; window: 0, or how many tokens, itself
+    among them, a token sees."""
+    torch = _torch()
+    if q.dim() != 3 or not q.is_cuda or q.dtype is not torch.bfloat16:
+        raise ValueError("q must be a bfloat16 CUDA tensor [T, heads, D]")
+    T, device, D = q.shape[0], q.device, kv.head_dim
+    pq, sq = _heads(q, kv.heads, D, device, "q")
+    view = _kv4_view(kv, cache, page_table, cu, lens, device)
+    max_len = max_len or min(view[3] * OQ_KV4_PAGE, 0x7FFFFFFF)
+    if y is None:
+        y = torch.empty((T, kv.heads, D), dtype=torch.bfloat16, device=device)
+        py = y.data_ptr()
+    else:
+        py = _mx_rows(y, (T, kv.heads, D), torch.bfloat16, device, "y")
+    if workspace is None:
+        with torch.cuda.device(device):   # (the split depends on the device's SMs)
+            need = oq_kv4_attention_workspace_size(kv, T, view[6], max_q, max_len)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _launch("oq_kv4_attention", device, kv.handle, pq, sq, T, *view, max_q, max_len, D ** -0.5 if scale is None else scale,
+            OQ_ATTN_CAUSAL if causal else 0, window, py, pw, nw)
+    return y
+
+
+def oq_kv4_poll_error(kv: Kv4) -> None:
+    _check(load_library().oq_kv4_poll_error(kv.handle), "oq_kv4_poll_error")
+
+
+# ------------------------------------------------------------------ 4-bit weights with group scales
+def oq_w4g_prepare(W, group: int, zeros: bool = False):
+    """W [d_out, d_in] (fp32/bf16, CUDA) -> (codes [d_out, d_in rounded up to 128, / 2]
+    uint8, scales [d_out, d_in / group] bf16, zeros uint8 or None)."""
+    torch = _torch()
+    if W.dim() != 2 or not W.is_cuda or not W.is_contiguous():
+        raise ValueError("W must be a contiguous CUDA matrix")
+    d_out, d_in = W.shape
+    if group not in (32, 64, 128) or d_in % group:
+        raise ValueError("group must be 32, 64 or 128 and divide W's width")
+    codes = torch.empty((d_out, (d_in + 127) // 128 * 64), dtype=torch.uint8, device=W.device)
+    scales = torch.empty((d_out, d_in // group), dtype=torch.bfloat16, device=W.device)
+    z = torch.empty((d_out, d_in // group), dtype=torch.uint8, device=W.device) if zeros else None
+    _launch("oq_w4g_prepare", W.device, W.data_ptr(), _mx_dtype(W), d_out, d_in, group, codes.data_ptr(), scales.data_ptr(),
+            None if z is None else z.data_ptr())
+    return codes, scales, z
+
+
+def oq_linear_w4g(x, codes, scales, zeros=None, group: int = 128, y=None, y_dtype=None):
+    """x [T, d_in] (bf16/fp32, CUDA) times 4-bit weights with group scales (from
+    oq_w4g_prepare) -> y [T, d_out] fp32 (or bf16)."""
+    torch = _torch()
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous CUDA matrix")
+    if codes.dim() != 2 or group not in (32, 64, 128) or x.shape[1] % group:
+        raise ValueError("codes must be a matrix, group 32, 64 or 128 and divide x's width")
+    T, d = x.shape
+    n, device = codes.shape[0], x.device
+    pc = _mx_ptr(codes, (n, (d + 127) // 128 * 64), device, "codes")
+    ps = _mx_rows(scales, (n, d // group), torch.bfloat16, device, "scales")
+    pz = None if zeros is None else _mx_ptr(zeros, (n, d // group), device, "zeros")
+    if y is None:
+        y = torch.empty_strided((T, n), (n, 1), dtype=torch.float32 if y_dtype is None else y_dtype, device=device)
+        py = y.data_ptr()
+    else:
+        py = _mx_rows(y, (T, n), y.dtype if y_dtype is None else y_dtype, device, "y")
+    _launch("oq_linear_w4g", device, x.data_ptr(), _mx_dtype(x), T, d, n, group, pc, ps, pz, py, _mx_dtype(y))
     return y
 
 
