@@ -21,103 +21,14 @@ namespace {
 
 constexpr int NT = 256;   // threads of a CTA
 
-// cos and sin of this lane's channels.  Interleaved pairs: c[j], s[j] for pair j
-// of the four; halves: for each of the eight channels, s negated in the first half.
+// What a lane multiplies its eight channels x and their partners xp in the
+// rotation by, gains included:  n sqrt(mean + eps) = x c + xp s.
 template <bool INTER>
-struct Turn {
-  float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
+struct Coef {
+  f32x2 c[4], s[4];
   bool on;        // these channels are rotated
-  int partner;    // halves: lane distance of the other half (signed)
+  int from;       // halves: the lane that holds the partners
 };
-
-template <bool INTER>
-__device__ __forceinline__ Turn<INTER> load_turn(const float* table, int64_t rows, int64_t pos, int rot, int ch) {
-  Turn<INTER> t;
-  t.on = table != nullptr && ch < rot;
-  t.partner = 0;
-  if (!t.on) return t;
-  const bool ok = pos >= 0 && pos < rows;   // a place outside the table makes the channels NaN
-  const float* row = table + (ok ? pos : 0) * rot;
-  const int half = rot >> 1;
-  if constexpr (INTER) {
-    const float4* p = reinterpret_cast<const float4*>(row + ch);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    t.c[0] = a.x, t.s[0] = a.y, t.c[1] = a.z, t.s[1] = a.w;
-    t.c[2] = b.x, t.s[2] = b.y, t.c[3] = b.z, t.s[3] = b.w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (!ok) t.c[i] = t.s[i] = __int_as_float(0x7FC00000);
-  } else {
-    const bool second = ch >= half;
-    const float4* p = reinterpret_cast<const float4*>(row + 2 * (second ? ch - half : ch));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 a = __ldg(p + i);
-      t.c[2 * i] = a.x, t.s[2 * i] = second ? a.y : -a.y, t.c[2 * i + 1] = a.z, t.s[2 * i + 1] = second ? a.w : -a.w;
-    }
-    t.partner = second ? -(half >> 3) : half >> 3;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (!ok) t.c[i] = t.s[i] = __int_as_float(0x7FC00000);
-  }
-  return t;
-}
-
-template <typename F>
-__device__ __forceinline__ F group_sum(F v, int lanes) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1)
-    if (o < lanes) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
-// the rotation in F (fp32 or fp64) of this lane's eight channels, in place
-template <bool INTER, typename F>
-__device__ __forceinline__ void rotate(F (&n)[8], const Turn<INTER>& t) {
-  if constexpr (INTER) {
-    if (t.on) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const F a = n[2 * j], b = n[2 * j + 1], c = (F)t.c[j], s = (F)t.s[j];
-        n[2 * j] = a * c - b * s;
-        n[2 * j + 1] = b * c + a * s;
-      }
-    }
-  } else {
-    const int lane = threadIdx.x & 31, from = lane + t.partner;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const F o = __shfl_sync(0xFFFFFFFFu, n[j], from);
-      if (t.on) n[j] = n[j] * (F)t.c[j] + o * (F)t.s[j];
-    }
-  }
-}
-
-// Whether the sum of squares in fp32 is good to fp32's precision: it neither
-// overflowed nor lost squares that eps does not hide.
-__device__ __forceinline__ bool plain_range(float ss, float eps) { return ss < 3e38f && (ss > 1e-30f || eps > 1e-24f); }
-
-// n = x g inv of a row held by `lanes` lanes; rows out of fp32's range in fp64
-__device__ __forceinline__ void head_norm(float (&n)[8], const float (&g)[8], float eps, float inv_d, int lanes, bool norm) {
-  if (!norm) return;
-  float ss = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) ss = fmaf(n[j], n[j], ss);
-  ss = group_sum(ss, lanes);
-  if (__all_sync(0xFFFFFFFFu, plain_range(ss, eps))) {
-    const float inv = 1.0f / sqrtf(fmaf(ss, inv_d, eps));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) n[j] = n[j] * inv * g[j];
-  } else {
-    double sd = 0.0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sd += (double)n[j] * (double)n[j];
-    sd = group_sum(sd, lanes);
-    const double inv = 1.0 / sqrt(sd * (double)inv_d + (double)eps);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) n[j] = (float)((double)n[j] * inv * (double)g[j]);
-  }
-}
 
 __device__ __forceinline__ void load_gain(float (&g)[8], const void* gain, bool bf16, int ch, bool in) {
   if (gain && in && bf16) {
@@ -134,72 +45,253 @@ __device__ __forceinline__ void load_gain(float (&g)[8], const void* gain, bool 
   }
 }
 
-// Heads sub, sub + step, .. of a token: first those of x[0], then those of x[1].
-// All lanes of a warp make the same number of turns.
-template <typename T, typename OUT, bool INTER>
-__device__ __forceinline__ void rope_token(const RopeArgs& p, int64_t t, bool token, int sub, int step, int lanes, int rows,
-                                           int64_t pos) {
-  const int vec = (int)threadIdx.x & (lanes - 1), ch = vec * 8;
-  const bool in = token && ch < p.D;
-  const Turn<INTER> turn = load_turn<INTER>(in ? p.table : nullptr, p.table_rows, pos, p.rot, ch);
-  float g0[8], g1[8];
-  load_gain(g0, p.gain[0], p.gain_bf16, ch, in);
-  load_gain(g1, p.gain[1], p.gain_bf16, ch, in);
-  const float inv_d = 1.0f / (float)p.D;
-  auto at = [&](int r, int& which) -> int64_t {
-    which = r >= p.heads[0];
-    return t * p.in_stride[which] + (int64_t)(which ? r - p.heads[0] : r) * p.D + ch;
-  };
-  Vec8<T> next;
-  next.zero();
-  int which = 0;
-  if (in && sub < rows) {
-    const int64_t a = at(sub, which);
-    next.load(static_cast<const T*>(p.x[which]) + a);
-  }
-  const int turns = (rows + step - 1) / step;
-#pragma unroll 1
-  for (int i = 0; i < turns; ++i) {
-    const int r = sub + i * step;
-    float n[8];
-    next.get(n);
-    const int w = which;
-    if (in && r + step < rows) {
-      const int64_t a = at(r + step, which);
-      next.load(static_cast<const T*>(p.x[which]) + a);
-    } else {
-      next.zero();
-    }
-    float g[8];
+// cos and sin of the lane's channels in a table row; s as it multiplies the partner
+template <bool INTER>
+__device__ __forceinline__ void load_turn(float (&c)[8], float (&s)[8], const float* row, int half, int ch) {
+  if constexpr (INTER) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(row + ch)), b = __ldg(reinterpret_cast<const float4*>(row + ch) + 1);
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = w ? g1[j] : g0[j];
-    head_norm(n, g, p.eps, inv_d, lanes, p.norm);
-    rotate<INTER, float>(n, turn);
-    if (in && r < rows)
-      store8(static_cast<OUT*>(p.out[w]) + t * p.out_stride[w] + (int64_t)(w ? r - p.heads[0] : r) * p.D + ch, n);
+    for (int j = 0; j < 8; j += 2) {
+      c[j] = c[j + 1] = v[j];
+      s[j] = -v[j + 1], s[j + 1] = v[j + 1];
+    }
+  } else {
+    const bool second = ch >= half;
+    const float4* p = reinterpret_cast<const float4*>(row + 2 * (second ? ch - half : ch));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 a = __ldg(p + i);
+      c[2 * i] = a.x, s[2 * i] = second ? a.y : -a.y;
+      c[2 * i + 1] = a.z, s[2 * i + 1] = second ? a.w : -a.w;
+    }
   }
 }
 
+template <bool INTER>
+__device__ __forceinline__ Coef<INTER> make_coef(const RopeArgs& p, const void* gain, int64_t pos, int ch, bool in) {
+  Coef<INTER> k;
+  float g[8];
+  load_gain(g, gain, p.gain_bf16, ch, in);
+  k.on = in && p.table != nullptr && ch < p.rot;
+  k.from = (int)threadIdx.x & 31;
+  if (!k.on) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k.c[i] = pack2(g[2 * i], g[2 * i + 1]), k.s[i] = pack2(0.f, 0.f);
+    return k;
+  }
+  const int half = p.rot >> 1;
+  float c[8], s[8], o[8];
+  const bool ok = pos >= 0 && pos < p.table_rows;   // a place outside the table makes the channels NaN
+  load_turn<INTER>(c, s, p.table + (ok ? pos : 0) * p.rot, half, ch);
+  if constexpr (INTER) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = g[j ^ 1];
+  } else {
+    const int d = ch >= half ? -half : half;
+    load_gain(o, gain, p.gain_bf16, ch + d, true);
+    k.from += d / 8;
+  }
+  const float nan = ok ? 1.f : __int_as_float(0x7FC00000);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k.c[i] = pack2(g[2 * i] * c[2 * i] * nan, g[2 * i + 1] * c[2 * i + 1] * nan);
+    k.s[i] = pack2(o[2 * i] * s[2 * i], o[2 * i + 1] * s[2 * i + 1]);
+  }
+  return k;
+}
+
+template <int LANES, typename F>
+__device__ __forceinline__ F group_sum(F v) {
+#pragma unroll
+  for (int o = LANES / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ uint32_t shfl_word(uint32_t v, int from) { return __shfl_sync(0xFFFFFFFFu, v, from); }
+__device__ __forceinline__ void shfl_vec(Vec8<__nv_bfloat16>& v, int from) {
+  v.w = make_uint4(shfl_word(v.w.x, from), shfl_word(v.w.y, from), shfl_word(v.w.z, from), shfl_word(v.w.w, from));
+}
+__device__ __forceinline__ void shfl_vec(Vec8<float>& v, int from) {
+  float* f = &v.a.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __shfl_sync(0xFFFFFFFFu, f[i], from);
+  f = &v.b.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __shfl_sync(0xFFFFFFFFu, f[i], from);
+}
+
+// the partners of this lane's channels, 0 where they are not rotated
+template <bool INTER, typename T>
+__device__ __forceinline__ void partners(f32x2 (&xp)[4], const f32x2 (&x)[4], Vec8<T> raw, const Coef<INTER>& k) {
+  if constexpr (INTER) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpack2(x[i], lo, hi);
+      xp[i] = pack2(k.on ? hi : 0.f, k.on ? lo : 0.f);
+    }
+  } else {
+    shfl_vec(raw, k.from);
+    if (!k.on) raw.zero();
+    raw.get(xp);
+  }
+}
+
+__device__ __forceinline__ float square_sum(const f32x2 (&x)[4]) {
+  f32x2 s = mul2(x[0], x[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2(x[i], x[i], s);
+  float lo, hi;
+  unpack2(s, lo, hi);
+  return lo + hi;
+}
+
+// Whether the sum of squares in fp32 is good to fp32's precision: it neither
+// overflowed nor lost squares that eps does not hide (a NaN is not).
+__device__ __forceinline__ bool plain_range(float ss, float eps) { return ss < 3e38f && (ss > 1e-30f || eps > 1e-24f); }
+
+// A row's eight channels in fp64, from the inputs: norm, gains and rotation.
+// Every lane of the warp takes part.
+template <bool INTER, int LANES>
+__device__ __forceinline__ void exact_row(double (&d)[8], const RopeArgs& p, const void* gain, int64_t pos, int ch, bool in) {
+  float g[8];
+  load_gain(g, gain, p.gain_bf16, ch, in);
+  if (p.norm) {
+    double ss = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss += d[j] * d[j];
+    ss = group_sum<LANES>(ss);
+    const double root = sqrt(ss / (double)p.D + (double)p.eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = d[j] / root * (double)g[j];
+  }
+  const bool on = in && p.table != nullptr && ch < p.rot, ok = pos >= 0 && pos < p.table_rows;
+  const int half = p.rot >> 1;
+  float c[8], s[8];
+  if (on) load_turn<INTER>(c, s, p.table + (ok ? pos : 0) * p.rot, half, ch);
+  double o[8];
+  const int from = ((int)threadIdx.x & 31) + (INTER || !on ? 0 : (ch >= half ? -half : half) / 8);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = INTER ? d[j ^ 1] : __shfl_sync(0xFFFFFFFFu, d[j], from);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (on) d[j] = ok ? d[j] * (double)c[j] + o[j] * (double)s[j] : nan("");
+}
+
+// How the rows of one tensor (queries or keys) go to CTAs.
 struct RopeGrid {
-  int lanes;      // lanes of a row
   int per_token;  // rows of a token that a CTA does at once
   int tokens;     // tokens of a CTA
   int split;      // CTAs that share a token's rows
-};
-struct RopeParams {
-  RopeArgs a;
-  RopeGrid g;
+  int ctas;
 };
 
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ RopeParams p) {
+// Rows of x[which] by CTA `cta` of grid g.  All lanes of a warp make the same
+// number of turns, two at a time without a branch between them (their latencies
+// overlap; one at a time took 306 us for 237 at 32760 tokens of 40 + 40 heads).  The
+// first rows' loads leave before the token's place and its table row are known,
+// and PF rows stay in flight.  Rows out of fp32's range are
+// marked and done in fp64 behind each 32 turns (inside the loop they would cost
+// all rows registers).
+template <typename T, typename OUT, bool INTER, int LANES, typename POS>
+__device__ __forceinline__ void rope_rows(const RopeArgs& p, const RopeGrid& g, int which, int cta, POS&& place) {
+  constexpr int PF = sizeof(T) == 2 ? 4 : 2, PAIR = 2, MARKS = 32;
+  const int grp = (int)threadIdx.x / LANES, ch = ((int)threadIdx.x & (LANES - 1)) * 8;
+  const int64_t t = (int64_t)(cta / g.split) * g.tokens + grp / g.per_token;
+  const int sub = cta % g.split * g.per_token + grp % g.per_token, step = g.split * g.per_token;
+  const bool in = t < p.T && ch < p.D;
+  const int rows = p.heads[which], turns = (rows + step - 1) / step, hop = step * p.D;
+  const int mine = in && sub < rows ? (rows - sub + step - 1) / step : 0;   // this lane's rows
+  const T* x0 = static_cast<const T*>(p.x[which]) + t * p.in_stride[which] + sub * p.D + ch;
+  OUT* y0 = static_cast<OUT*>(p.out[which]) + t * p.out_stride[which] + sub * p.D + ch;
+  Vec8<T> raw[PF];
+  const T* xn = x0;   // the next row to load
+  int loaded = 0;
+  auto fetch = [&](Vec8<T>& v) {
+    if (loaded < mine) v.load(xn);
+    else v.zero();
+    ++loaded;
+    xn += hop;
+  };
+#pragma unroll
+  for (int u = 0; u < PF; ++u) fetch(raw[u]);
+  const int64_t pos = place(t);
+  const Coef<INTER> k = make_coef<INTER>(p, p.gain[which], pos, ch, in);
+  const float inv_d = 1.0f / (float)p.D;
+  OUT* y = y0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < turns; i0 += MARKS) {
+    uint32_t marks = 0u;
+#pragma unroll 1
+    for (int i1 = 0; i1 < MARKS && i0 + i1 < turns; i1 += PF) {
+#pragma unroll
+      for (int u = 0; u < PF; ++u) {
+        const int i = i0 + i1 + u;
+        if (u % PAIR == 0 && u > 0 && i >= turns) break;   // the same in all lanes
+        const Vec8<T> now = raw[u];
+        fetch(raw[u]);
+        f32x2 x[4], xp[4];
+        now.get(x);
+        partners<INTER, T>(xp, x, now, k);
+        float inv = 1.f, n[8];
+        bool good = true;
+        if (p.norm) {
+          const float ss = group_sum<LANES>(square_sum(x));
+          good = plain_range(ss, p.eps) || i >= turns;
+          inv = rsqrtf(fmaf(ss, inv_d, p.eps));
+        }
+        if (!good) marks |= 1u << (i1 + u);
+        const f32x2 i2 = pack2(inv, inv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = mul2(fma2(xp[j], k.s[j], mul2(x[j], k.c[j])), i2);
+        unpack8(x, n);
+        if (i < mine && good) store8(y, n);
+        y += hop;
+      }
+    }
+    const uint32_t all = __reduce_or_sync(0xFFFFFFFFu, marks);
+#pragma unroll 1
+    for (int j = 0; all >> j != 0u; ++j) {
+      if (!(all >> j & 1u)) {
+        if (j == MARKS - 1) break;
+        continue;
+      }
+      const int i = i0 + j;
+      const bool have = i < mine;
+      Vec8<T> now;
+      now.zero();
+      if (have) now.load(x0 + (int64_t)i * hop);
+      float n[8];
+      double d[8];
+      now.get(n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = (double)n[e];
+      exact_row<INTER, LANES>(d, p, p.gain[which], pos, ch, in);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n[e] = (float)d[e];
+      if (have && (marks >> j & 1u)) store8(y0 + (int64_t)i * hop, n);
+      if (j == MARKS - 1) break;
+    }
+  }
+}
+
+struct RopeParams {
+  RopeArgs a;
+  RopeGrid g[2];
+  bool both;      // a CTA does its tokens' queries, then their keys (the grids are alike); else CTAs of each
+};
+
+template <typename T, bool INTER, int LANES>
+__global__ void __launch_bounds__(NT, 3) rope_kernel(const __grid_constant__ RopeParams p) {
   dependency_wait();
-  const int grp = (int)threadIdx.x / p.g.lanes;
-  const int64_t t = (int64_t)blockIdx.x * p.g.tokens + grp / p.g.per_token;
-  const bool token = t < p.a.T;
-  const int64_t pos = !token ? 0 : p.a.positions ? (int64_t)p.a.positions[t] : t;
-  rope_token<T, T, INTER>(p.a, t, token, (int)blockIdx.y * p.g.per_token + grp % p.g.per_token, p.g.split * p.g.per_token,
-                          p.g.lanes, p.a.heads[0] + p.a.heads[1], pos);
+  int which = !p.both && (int)blockIdx.x >= p.g[0].ctas;
+  const int last = p.both ? 1 : which, cta = (int)blockIdx.x - (which ? p.g[0].ctas : 0);
+#pragma unroll 1
+  for (; which <= last; ++which)
+    rope_rows<T, T, INTER, LANES>(p.a, p.g[which], which, cta, [&](int64_t t) {
+      return t >= p.a.T ? (int64_t)0 : p.a.positions ? (int64_t)p.a.positions[t] : t;
+    });
 }
 
 int row_lanes(int D) {
@@ -208,19 +300,26 @@ int row_lanes(int D) {
   return l;
 }
 
-// A CTA takes one token (several where a token has few heads); few tokens are
-// shared by several CTAs, up to two for each SM.
-RopeGrid rope_grid(int64_t T, int rows, int D, int sms) {
+// Lane groups of a token: as few as still make two CTAs for each SM (what a token's
+// table row and gains cost is spent once for all its rows); few tokens are shared
+// by as many CTAs.  Measured: 1001 tokens of 24 + 8 fp32 rows of 96 channels, two
+// CTAs an SM 9.7 us, three 14.2, four 17.1; 32760 tokens of 80 bf16 rows of 128, one
+// group a token 237 us, two 237, four 248, sixteen 477.
+// False: more CTAs than a grid takes.
+bool rope_grid(int64_t T, int rows, int D, int sms, int threads, RopeGrid* out) {
   RopeGrid g;
-  g.lanes = row_lanes(D);
-  const int groups = NT / g.lanes;
+  const int groups = threads / row_lanes(D);
+  const int64_t want = 2 * (int64_t)sms * groups / T;
   g.per_token = 1;
-  while (g.per_token < groups && g.per_token < rows) g.per_token *= 2;
+  while (g.per_token < groups && g.per_token < rows && g.per_token < want) g.per_token *= 2;
   g.tokens = groups / g.per_token;
   const int64_t ctas = (T + g.tokens - 1) / g.tokens;
   const int turns = (rows + g.per_token - 1) / g.per_token;
   g.split = (int)std::max<int64_t>(1, std::min<int64_t>(turns, 2 * (int64_t)sms / ctas));
-  return g;
+  if (ctas * g.split > 0x3FFFFFFF) return false;
+  g.ctas = rows > 0 ? (int)(ctas * g.split) : 0;
+  *out = g;
+  return true;
 }
 
 oq_status launched(cudaError_t e, const char* what) {
@@ -240,20 +339,28 @@ oq_status launched(cudaError_t e, const char* what) {
 // off by less than DELTA of |a| + |b| (the pair it was turned from), and where
 // that could change a code or the block's scale, the row is formed again in fp64
 // and rounded once.  (The sum of squares takes 8 + 4 roundings, halved by the
-// root; the mean, the root, the quotient, two products and the rotation's three
-// operations add at most 9 half-ulps: below 16 * 2^-24, taken as 32 * 2^-24.)
+// root; the mean, halved too, the reciprocal root's two ulps, two products and the
+// rotation's three operations add at most 10: 16 * 2^-24, taken as 32 * 2^-24.)
 constexpr float DELTA = 32.f / 16777216.f;
 
 struct AppendParams {
   AppendArgs a;
   RopeGrid g;
-  int q_ctas, kv_units, kv_heads, D;
+  int kv_heads, parts;    // CTAs that share a window's groups of 128 channels
 };
+constexpr int ANT = 512;  // threads: 32 tokens of 16 lanes
 
 __device__ __forceinline__ float round_odd(double w) {
   float f = __double2float_rz(w);
   if ((double)f != w) f = __uint_as_float(__float_as_uint(f) | 1u);
   return f;
+}
+
+// the low four nibbles, one a byte
+__device__ __forceinline__ uint32_t spread_nibbles(uint32_t v) {
+  v &= 0xFFFFu;
+  v = (v | v << 8) & 0x00FF00FFu;
+  return (v | v << 4) & 0x0F0F0F0Fu;
 }
 
 // largest of four neighbouring lanes
@@ -262,151 +369,153 @@ __device__ __forceinline__ float max4(float v) {
   return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
 }
 
-// Eight channels of a key (norm, rotation) -> codes and the block's scale code.
-template <typename T, bool INTER>
-__device__ __forceinline__ uint32_t key_codes(const Vec8<T>& raw, const RopeArgs& p, const float (&g)[8],
-                                              const Turn<INTER>& turn, int lanes, float inv_d, uint32_t& scale) {
-  float n[8], mag[8], w[8];
-  raw.get(n);
-  float ss = 0.f;
+// The same in fp64: codes, and the block's scale code above them.
+template <typename T, bool INTER, int LANES>
+__device__ __forceinline__ uint64_t exact_codes(Vec8<T> raw, const RopeArgs* p, int64_t pos, int ch, bool in) {
+  float w[8];
+  double d[8], top = 0.0;
+  raw.get(w);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) ss = fmaf(n[j], n[j], ss);
-  ss = group_sum(ss, lanes);
-  bool doubt = p.norm && !plain_range(ss, p.eps);
-  if (p.norm) {
-    const float inv = 1.0f / sqrtf(fmaf(ss, inv_d, p.eps));
+  for (int j = 0; j < 8; ++j) d[j] = (double)w[j];
+  exact_row<INTER, LANES>(d, *p, p->gain[1], pos, ch, in);
+  bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) n[j] = n[j] * inv * g[j];
+  for (int j = 0; j < 8; ++j) {
+    bad |= !(fabs(d[j]) <= 3.4028234663852886e38);
+    top = fmax(top, fabs(d[j]));
   }
-  const float delta = p.norm || p.table ? DELTA : 0.f;
-  // |a| + |b|, scaled to the possible error
-  float most = 0.f;
-  if constexpr (INTER) {
+  const float f = max4(bad ? __int_as_float(0x7F800000) : __double2float_rz(top));
+  const uint32_t scale = mx_scale_code<4>(__float_as_uint(f));
+  const double s = (double)mx_inverse_scale(scale);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mag[j] = delta * (fabsf(n[j]) + (turn.on ? fabsf(n[j ^ 1]) : 0.f));
-  } else {
-    const int from = ((int)threadIdx.x & 31) + turn.partner;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float o = __shfl_sync(0xFFFFFFFFu, n[j], from);
-      mag[j] = delta * (fabsf(n[j]) + (turn.on ? fabsf(o) : 0.f));
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) most = fmaxf(most, mag[j]);
-  most = max4(most);
-  rotate<INTER, float>(n, turn);
-  const uint32_t block = mx_block_max(n);
-  scale = mx_scale_code<4>(block);
-  const float top = __uint_as_float(block);
-  doubt |= scale != 255u && (__float_as_uint(top + most) >> 23) != (__float_as_uint(fmaxf(top - most, 0.f)) >> 23);
-  const float inv_s = mx_inverse_scale(scale);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = n[j] * inv_s;
+  for (int j = 0; j < 8; ++j) w[j] = round_odd(d[j] * s);
   uint32_t out[1];
   mx_element_codes<4>(w, scale, out);
-  if (delta > 0.f) {
-    doubt |= top > 0.f && top < 1e-30f;   // products below fp32's normal numbers are off by more
-    float lo[8], hi[8];
+  return (uint64_t)scale << 32 | out[0];
+}
+
+// Eight channels of a key (norm, rotation) -> codes and the block's scale code.
+template <typename T, bool INTER, int LANES>
+__device__ __forceinline__ uint32_t key_codes(const Vec8<T>& raw, const RopeArgs& p, const Coef<INTER>& k, int64_t pos, int ch,
+                                              bool in, float inv_d, uint32_t& scale) {
+  f32x2 x[4], xp[4];
+  raw.get(x);
+  partners<INTER, T>(xp, x, raw, k);
+  bool doubt = false;
+  float inv = 1.f;
+  if (p.norm) {
+    const float ss = group_sum<LANES>(square_sum(x));
+    doubt = !plain_range(ss, p.eps);
+    inv = rsqrtf(fmaf(ss, inv_d, p.eps));
+  }
+  const f32x2 i2 = pack2(inv, inv);
+  float n[8], a[8], b[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo[j] = fmaxf(fabsf(w[j]) - mag[j] * inv_s, 0.f);
-      hi[j] = fabsf(w[j]) + mag[j] * inv_s;
+  for (int i = 0; i < 4; ++i) {
+    x[i] = mul2(mul2(x[i], k.c[i]), i2);
+    xp[i] = mul2(mul2(xp[i], k.s[i]), i2);
+  }
+  unpack8(x, a);
+  unpack8(xp, b);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) n[j] = a[j] + b[j];
+  const uint32_t block = mx_block_max(n);
+  scale = mx_scale_code<4>(block);
+  const float inv_s = mx_inverse_scale(scale);
+  float w[8];
+  uint32_t out[1];
+  if (!p.norm && !p.table) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = n[j] * inv_s;
+    mx_element_codes<4>(w, scale, out);
+  } else {
+    // what |a| + |b| lets the fp32 value be off: where the codes of both ends are
+    // one, it is the value's (ends around zero differ in its sign: looked at too)
+    const float top = __uint_as_float(block);
+    const f32x2 is2 = pack2(inv_s, inv_s), off = pack2(DELTA * inv_s, DELTA * inv_s);
+    const f32x2 noff = pack2(-DELTA * inv_s, -DELTA * inv_s);
+    float m[8], lo[8], hi[8];
+    f32x2 l2[4], h2[4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m[j] = fabsf(a[j]) + fabsf(b[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 wi = mul2(pack2(n[2 * i], n[2 * i + 1]), is2), mi = pack2(m[2 * i], m[2 * i + 1]);
+      l2[i] = fma2(mi, noff, wi);
+      h2[i] = fma2(mi, off, wi);
     }
-    doubt |= scale != 255u && cvt8_e2m1(lo) != cvt8_e2m1(hi);
+    unpack8(l2, lo);
+    unpack8(h2, hi);
+    mx_element_codes<4>(lo, scale, out);
+    float most = fmaxf(fmaxf(m[0], m[1]), m[2]);
+    most = fmaxf(fmaxf(most, m[3]), m[4]);
+    most = max4(fmaxf(fmaxf(fmaxf(most, m[5]), m[6]), m[7])) * DELTA;
+    doubt |= top > 0.f && top < 1e-30f;   // products below fp32's normal numbers are off by more
+    doubt |= scale != 255u && ((__float_as_uint(top + most) >> 23) != (__float_as_uint(fmaxf(top - most, 0.f)) >> 23) ||
+                               out[0] != cvt8_e2m1(hi));
     if (__any_sync(0xFFFFFFFFu, doubt)) {
-      double d[8], top_d = 0.0;
-      raw.get(n);
-      double sd = 0.0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        d[j] = (double)n[j];
-        sd += d[j] * d[j];
-      }
-      sd = group_sum(sd, lanes);
-      if (p.norm) {
-        const double root = sqrt(sd / (double)p.D + (double)p.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = d[j] / root * (double)g[j];
-      }
-      rotate<INTER, double>(d, turn);
-      bool bad = false;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        bad |= !(fabs(d[j]) <= 3.4028234663852886e38);
-        top_d = fmax(top_d, fabs(d[j]));
-      }
-      float f = bad ? __int_as_float(0x7F800000) : __double2float_rz(top_d);
-      f = max4(f);
-      scale = mx_scale_code<4>(__float_as_uint(f));
-      const double s = (double)mx_inverse_scale(scale);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = round_odd(d[j] * s);
-      mx_element_codes<4>(w, scale, out);
+      const uint64_t r = exact_codes<T, INTER, LANES>(raw, &p, pos, ch, in);
+      out[0] = (uint32_t)r;
+      scale = (uint32_t)(r >> 32);
     }
   }
   return out[0];
 }
 
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ int found[4];
-  __shared__ __align__(16) uint8_t tile[128 * 36];   // V codes, one a byte: [channel][token], rows 36 bytes apart
+template <typename T, bool INTER, int LANES>
+__global__ void __launch_bounds__(ANT, 1) append_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ int found[2];
+  __shared__ __align__(16) uint8_t tile[2][128 * 20];   // V codes: channel 8 s + j in row 16 j + s (no bank twice), 32 tokens
   const RopeArgs& r = p.a.rope;
   const KvView& kv = p.a.kv;
   dependency_wait();
-  if ((int)blockIdx.x < p.q_ctas) {
-    // the queries of one token
-    const int64_t t = blockIdx.x / p.g.split;
-    const int part = (int)(blockIdx.x % p.g.split);
-    int64_t pos = 0;
-    if (r.positions) {
-      pos = r.positions[t];
-    } else {
+  if ((int)blockIdx.x < p.g.ctas) {
+    rope_rows<T, __nv_bfloat16, INTER, LANES>(r, p.g, 0, (int)blockIdx.x, [&](int64_t t) {
+      if (!r.table) return (int64_t)0;
+      if (r.positions) return t < r.T ? (int64_t)r.positions[t] : (int64_t)0;
       // the token's sequence: how many of them end at or before it
       int ends = 0;
-      for (int b = threadIdx.x; b < kv.B; b += NT) ends += kv.cu[b + 1] <= t;
-      if (threadIdx.x == 0) found[0] = 0;
-      __syncthreads();
-      if (ends) atomicAdd(&found[0], ends);
-      __syncthreads();
-      const int b = min(found[0], kv.B - 1);
-      pos = (int64_t)kv.lens[b] - kv.cu[b + 1] + t;
-    }
-    const int grp = (int)threadIdx.x / p.g.lanes, groups = NT / p.g.lanes;
-    rope_token<T, __nv_bfloat16, INTER>(r, t, true, part * groups + grp, p.g.split * groups, p.g.lanes, r.heads[0], pos);
+      for (int b = (int)threadIdx.x & (LANES - 1); b < kv.B; b += LANES) ends += kv.cu[b + 1] <= t;
+      const int b = min(group_sum<LANES>(ends), kv.B - 1);
+      return (int64_t)kv.lens[b] - kv.cu[b + 1] + t;
+    });
     return;
   }
-  const int unit = ((int)blockIdx.x - p.q_ctas) / kv.groups, hg = ((int)blockIdx.x - p.q_ctas) % kv.groups;
+  const int unit = ((int)blockIdx.x - p.g.ctas) / p.parts, part = ((int)blockIdx.x - p.g.ctas) % p.parts;
   int b, first, count, place;
   if (!kv_window(kv, r.T, unit, found, b, first, count, place)) return;
   const int64_t page = kv.table[(int64_t)b * kv.width + (place >> 7)];
   if (page < 0 || page >= kv.pages) return;
+  constexpr int D = LANES * 8;
+  const int sub = (int)threadIdx.x & 15, ch = (sub & (LANES - 1)) * 8;   // 16 lanes hold a group's channels of a token
+  const int w0 = place & 127 & ~31;                                      // the window's first row in its page
+  const int row = (int)threadIdx.x >> 4, at = w0 + row, i = row - (place & 31);
+  const bool token = i >= 0 && i < count;
+  const int64_t t = first + i;
+  int hg = (int)((int64_t)kv.groups * part / p.parts);
+  const int hg_end = (int)((int64_t)kv.groups * (part + 1) / p.parts);
   uint8_t* base = kv.cache + (page * kv.groups + hg) * KV_GROUP_BYTES;
-  const int lanes = p.D / 8, sub = (int)threadIdx.x & 15, head = hg * (128 / p.D) + sub / lanes;
-  const int vec = sub & (lanes - 1), ch = vec * 8;   // 16 lanes hold the group's 128 channels of a token
-  const bool has = head < p.kv_heads;
-  float g[8];
-  load_gain(g, r.gain[1], r.gain_bf16, ch, has);
-  const float inv_d = 1.0f / (float)p.D;
-  const int w0 = place & 127 & ~31;                  // the window's first row in its page
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int row = half * 16 + ((int)threadIdx.x >> 4);   // of the window
-    const int i = row - (place & 31);
-    const bool token = i >= 0 && i < count;
-    const int64_t t = first + i;
-    Vec8<T> k, v;
-    k.zero();
-    v.zero();
-    if (token && has) {
-      k.load(static_cast<const T*>(r.x[1]) + t * r.in_stride[1] + (int64_t)head * p.D + ch);
-      v.load(static_cast<const T*>(p.a.v) + t * p.a.v_stride + (int64_t)head * p.D + ch);
-    }
-    const int64_t pos = !token ? 0 : r.positions ? (int64_t)r.positions[t] : (int64_t)(place + i);
-    const Turn<INTER> turn = load_turn<INTER>(token && has ? r.table : nullptr, r.table_rows, pos, r.rot, ch);
+  int head = hg * (128 / D) + sub / LANES;
+  const T* kp = static_cast<const T*>(r.x[1]) + t * r.in_stride[1] + head * D + ch;
+  const T* vp = static_cast<const T*>(p.a.v) + t * p.a.v_stride + head * D + ch;
+  Vec8<T> kn, vn;   // the next group's
+  auto fetch = [&]() {
+    if (token && head < p.kv_heads) kn.load(kp), vn.load(vp);
+    else kn.zero(), vn.zero();
+  };
+  fetch();
+  const int64_t pos = !token ? 0 : r.positions ? (int64_t)r.positions[t] : (int64_t)(place + i);
+  const Coef<INTER> coef = make_coef<INTER>(r, r.gain[1], pos, ch, token);
+#pragma unroll 1
+  for (int buf = 0; hg < hg_end; ++hg, buf ^= 1, base += KV_GROUP_BYTES) {
+    const Vec8<T> k = kn, v = vn;
+    const bool has = head < p.kv_heads;
+    head += 128 / D;
+    kp += 128;
+    vp += 128;
+    if (hg + 1 < hg_end) fetch();
     uint32_t ks, vs, kc, vc[1];
-    kc = key_codes<T, INTER>(k, r, g, turn, lanes, inv_d, ks);
+    kc = key_codes<T, INTER, LANES>(k, r, coef, pos, ch, token, 1.0f / D, ks);
     if (!has) kc = 0u, ks = 0u;
     float x[8];
     v.get(x);
@@ -417,43 +526,36 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ Appe
     mx_element_codes<4>(x, vs, vc);
     const uint32_t kw = mx_scale_word(ks), vw = mx_scale_word(vs);
     if (token) {
-      const int at = w0 + row;
       *reinterpret_cast<uint32_t*>(base + at * 64 + sub * 4) = kc;
       if (sub == 0) {
         *reinterpret_cast<uint32_t*>(base + KV_KS_ROW * 64 + mx_tile_word(at) * 4) = kw;
         *reinterpret_cast<uint32_t*>(base + KV_VS_ROW * 64 + at * 4) = vw;
       }
     }
+    // two tokens a byte: the lanes of a pair of rows take four channels each
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, vc[0], 16);
+    const bool odd = (row & 1) != 0;
+    const uint32_t even_row = spread_nibbles(odd ? other >> 16 : vc[0]), odd_row = spread_nibbles(odd ? vc[0] >> 16 : other);
+    const uint32_t pairs = even_row | odd_row << 4;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) tile[(sub * 8 + j) * 36 + row] = (uint8_t)((vc[0] >> (4 * j)) & 15u);
-  }
-  __syncthreads();
-  // a thread packs a channel's 32 tokens; tokens that are not the call's keep their codes
-  if (threadIdx.x < 128) {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(tile + threadIdx.x * 36);
-    uint4* dst = reinterpret_cast<uint4*>(base + (KV_V_ROW + threadIdx.x) * 64 + (w0 >> 5) * 16);
-    uint32_t out[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t x = src[2 * q], y = src[2 * q + 1];
-      x |= x >> 4;
-      y |= y >> 4;
-      out[q] = __byte_perm(x, y, 0x6420);
-    }
-    if (count != 32) {
-      const uint4 old = *dst;
-      const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-      const int lo = place & 31, hi = lo + count;   // nibbles [lo, hi) of the 32 are new
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int a = min(max(lo - 8 * q, 0), 8), e = min(max(hi - 8 * q, 0), 8);
-        const uint32_t below_e = e == 8 ? 0xFFFFFFFFu : (1u << (4 * e)) - 1u;
-        const uint32_t below_a = a == 8 ? 0xFFFFFFFFu : (1u << (4 * a)) - 1u;
-        const uint32_t mask = below_e & ~below_a;
-        out[q] = (out[q] & mask) | (o[q] & ~mask);
+    for (int j = 0; j < 4; ++j) tile[buf][((j + (odd ? 4 : 0)) * 16 + sub) * 20 + (row >> 1)] = (uint8_t)(pairs >> (8 * j));
+    __syncthreads();   // (the other tile's readers are past the barrier before)
+    // four threads write a channel's 32 tokens; tokens that are not the call's keep their codes
+    {
+      const int c = (int)threadIdx.x >> 2, q = (int)threadIdx.x & 3;
+      uint32_t out = reinterpret_cast<const uint32_t*>(tile[buf] + ((c & 7) * 16 + (c >> 3)) * 20)[q];
+      uint32_t* dst = reinterpret_cast<uint32_t*>(base + (KV_V_ROW + c) * 64 + (w0 >> 5) * 16) + q;
+      if (count != 32) {
+        const int lo = min(max((place & 31) - 8 * q, 0), 8), hi = min(max((place & 31) + count - 8 * q, 0), 8);
+        const uint32_t below_hi = hi == 8 ? 0xFFFFFFFFu : (1u << (4 * hi)) - 1u;
+        const uint32_t below_lo = lo == 8 ? 0xFFFFFFFFu : (1u << (4 * lo)) - 1u;
+        const uint32_t mask = below_hi & ~below_lo;   // nibbles [lo, hi) are new
+        if (mask != 0xFFFFFFFFu && mask != 0u) out = (out & mask) | (*dst & ~mask);
+        if (mask != 0u) *dst = out;
+      } else {
+        *dst = out;
       }
     }
-    *dst = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
@@ -508,6 +610,21 @@ __global__ void __launch_bounds__(NT) read_kernel(const __grid_constant__ ReadAr
   }
 }
 
+template <typename T, bool INTER>
+cudaError_t rope_launch_lanes(const RopeParams& p, dim3 grid, cudaStream_t st) {
+  switch (row_lanes(p.a.D)) {
+    case 4: return mx_launch(rope_kernel<T, INTER, 4>, grid, NT, 0, 0, st, p);
+    case 8: return mx_launch(rope_kernel<T, INTER, 8>, grid, NT, 0, 0, st, p);
+    case 16: return mx_launch(rope_kernel<T, INTER, 16>, grid, NT, 0, 0, st, p);
+    default: return mx_launch(rope_kernel<T, INTER, 32>, grid, NT, 0, 0, st, p);
+  }
+}
+template <typename T, bool INTER>
+cudaError_t append_launch_lanes(const AppendParams& p, dim3 grid, cudaStream_t st) {
+  return p.a.rope.D == 64 ? mx_launch(append_kernel<T, INTER, 8>, grid, ANT, 0, 0, st, p)
+                          : mx_launch(append_kernel<T, INTER, 16>, grid, ANT, 0, 0, st, p);
+}
+
 // units of kv_window that B sequences with T tokens may have
 int64_t window_units(int64_t T, int B) { return std::min<int64_t>(T, T / 32 + 2 * (int64_t)B); }
 
@@ -518,17 +635,21 @@ oq_status rope_launch(const RopeArgs& a, void* stream) {
   int dev = 0;
   RopeParams p;
   p.a = a;
-  p.g = rope_grid(a.T, a.heads[0] + a.heads[1], a.D, mx_sm_count(&dev));
-  const int64_t ctas = (a.T + p.g.tokens - 1) / p.g.tokens;
-  if (ctas > 0x7FFFFFFF) return OQ_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)ctas, (unsigned)p.g.split);
+  const int sms = mx_sm_count(&dev), most = std::max(a.heads[0], a.heads[1]);
+  if (!rope_grid(a.T, most, a.D, sms, NT, &p.g[0])) return OQ_ERR_UNSUPPORTED;
+  // Many tokens: a token's queries and keys, which lie side by side in a
+  // projection's output, are read by one CTA.  Few: a CTA has one or the other.
+  p.both = a.heads[0] > 0 && a.heads[1] > 0 && p.g[0].ctas >= 8 * sms;
+  p.g[1] = p.g[0];
+  if (!p.both)
+    for (int i = 0; i < 2; ++i)
+      if (!rope_grid(a.T, a.heads[i], a.D, sms, NT, &p.g[i])) return OQ_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(p.both ? p.g[0].ctas : p.g[0].ctas + p.g[1].ctas));
   cudaError_t e;
   if (a.dtype == OQ_DTYPE_BF16)
-    e = a.interleaved ? mx_launch(rope_kernel<__nv_bfloat16, true>, grid, NT, 0, 0, st, p)
-                      : mx_launch(rope_kernel<__nv_bfloat16, false>, grid, NT, 0, 0, st, p);
+    e = a.interleaved ? rope_launch_lanes<__nv_bfloat16, true>(p, grid, st) : rope_launch_lanes<__nv_bfloat16, false>(p, grid, st);
   else
-    e = a.interleaved ? mx_launch(rope_kernel<float, true>, grid, NT, 0, 0, st, p)
-                      : mx_launch(rope_kernel<float, false>, grid, NT, 0, 0, st, p);
+    e = a.interleaved ? rope_launch_lanes<float, true>(p, grid, st) : rope_launch_lanes<float, false>(p, grid, st);
   return launched(e, "norm and rotation");
 }
 
@@ -537,21 +658,22 @@ oq_status kv4_append_launch(const AppendArgs& a, void* stream) {
   int dev = 0;
   AppendParams p;
   p.a = a;
-  p.D = a.rope.D;
   p.kv_heads = a.rope.heads[1];
-  p.g = rope_grid(a.rope.T, std::max(a.rope.heads[0], NT / row_lanes(p.D)), p.D, mx_sm_count(&dev));
-  const int64_t q = a.rope.x[0] ? a.rope.T * p.g.split : 0, units = window_units(a.rope.T, a.kv.B);
-  if (q + units * a.kv.groups > 0x7FFFFFFF) return OQ_ERR_UNSUPPORTED;
-  p.q_ctas = (int)q;
-  p.kv_units = (int)units;
-  const dim3 grid((unsigned)(q + units * a.kv.groups));
+  const int D = a.rope.D;
+  const int64_t units = window_units(a.rope.T, a.kv.B);
+  const int sms = mx_sm_count(&dev);
+  // a window's groups: in one CTA (what a token's table row costs is spent once)
+  // where there are windows for two CTAs an SM, else shared
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(a.kv.groups, 2 * (int64_t)sms / units));
+  if (!rope_grid(a.rope.T, a.rope.heads[0], D, sms, ANT, &p.g) || p.g.ctas + units * p.parts > 0x7FFFFFFF)
+    return OQ_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(p.g.ctas + units * p.parts));
   cudaError_t e;
   if (a.rope.dtype == OQ_DTYPE_BF16)
-    e = a.rope.interleaved ? mx_launch(append_kernel<__nv_bfloat16, true>, grid, NT, 0, 0, st, p)
-                           : mx_launch(append_kernel<__nv_bfloat16, false>, grid, NT, 0, 0, st, p);
+    e = a.rope.interleaved ? append_launch_lanes<__nv_bfloat16, true>(p, grid, st)
+                           : append_launch_lanes<__nv_bfloat16, false>(p, grid, st);
   else
-    e = a.rope.interleaved ? mx_launch(append_kernel<float, true>, grid, NT, 0, 0, st, p)
-                           : mx_launch(append_kernel<float, false>, grid, NT, 0, 0, st, p);
+    e = a.rope.interleaved ? append_launch_lanes<float, true>(p, grid, st) : append_launch_lanes<float, false>(p, grid, st);
   return launched(e, "cache append");
 }
 
