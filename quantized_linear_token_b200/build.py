@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "liborbitquant.so")
 SOURCES = ["oq_api.cu", "oq_rotate_quantize.cu", "oq_rotate_quantize_tc.cu", "oq_gemm.cu", "oq_gemm_pair.cu", "oq_gemm_skinny.cu", "oq_gemm_w16.cu",
            "oq_levels.cu", "oq_host_io.cu", "oq_int4.cu",
            "oq_noalloc.cu", "oq_diag.cu", "oq_fused.cu", "oq_gemv.cu", "oq_mx_api.cu", "oq_mx_quant.cu", "oq_mx_gemm.cu",
-           "oq_mx_small.cu", "oq_rope.cu", "oq_kv4_attention.cu", "oq_w4g.cu", "oq_kv4_api.cu", "oq_weight_io.cpp", "oq_host.cpp"]
+           "oq_mx_small.cu", "oq_rope.cu", "oq_kv4_attention.cu", "oq_kv4_chunk.cu", "oq_w4g.cu", "oq_kv4_api.cu", "oq_weight_io.cpp", "oq_host.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17"]
 

@@ -83,6 +83,15 @@ struct AttentionArgs {
   size_t workspace_bytes;
   int* err;
 };
+// a call's split over parts of the cache, which a second kernel joins
+struct AttnSplit {
+  AttentionArgs a;
+  int splits, group;       // query heads per key head
+  float* part_o;           // [splits][T][heads][D], relative to the reference
+  float2* part_ml;         // [splits][T][heads]: log2 of the reference, sum
+};
+int kv4_chunk_splits(int kv_heads, int B, int group, int max_q, int64_t tiles, int sms);
+oq_status kv4_chunk_launch(const AttnSplit& p, cudaStream_t st, int device);
 size_t kv4_attention_workspace(const oq_kv4* kv, int64_t T, int B, int max_q, int max_len);
 oq_status kv4_attention_launch(const AttentionArgs& a, void* stream);
 

@@ -323,8 +323,8 @@ oq_status oq_kv4_attention(const oq_kv4* kv, const void* q, int64_t q_stride, in
   if (!(scale > 0.f) || std::isinf(scale)) return invalid(who, "scale must be positive and finite");
   if (flags & ~OQ_ATTN_CAUSAL) return invalid(who, "unknown flags");
   const int group = kv->heads / kv->kv_heads;
-  if (T * kv->heads > 0x7FFFFFFF || (int64_t)max_q * group > 0x7FFFFFFF - 64 || kv->groups > 1023)
-    return unsupported(who, "at most 2^31 rows of queries per call and 1023 groups of 128 channels");
+  if (T * kv->heads > 0x7FFFFFFF || (int64_t)max_q * group > 0x7FFFFFFF - 64 || kv->kv_heads > 1023)
+    return unsupported(who, "at most 2^31 rows of queries per call and 1023 key heads");
   if (T == 0 || B == 0 || max_q == 0) return OQ_OK;
   if ((st = check_heads(who, "q", q, kv->heads, kv->head_dim, q_stride, T, OQ_DTYPE_BF16)) != OQ_OK) return st;
   if (!y || !aligned(y, 16)) return invalid(who, "y must be a 16-byte aligned pointer");

@@ -63,12 +63,8 @@ struct Cfg {
   static_assert(SMEM <= 113 * 1024, "two CTAs an SM");
 };
 
-struct AttnParams {
+struct AttnParams : AttnSplit {
   CUtensorMap map;
-  AttentionArgs a;
-  int splits, group;       // query heads per key head
-  float* part_o;           // [splits][T][heads][D]
-  float2* part_ml;         // [splits][T][heads]: log2 of the reference, sum
 };
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
@@ -612,17 +608,18 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinP
 // ------------------------------------------------------------------ host
 int pick_cols(int64_t columns) { return columns <= 4 ? 4 : columns <= 8 ? 8 : 16; }
 
+// From this many queries a key head on keys and values are decoded (oq_kv4_chunk.cu).
+constexpr int64_t CHUNK = 48;
+
 // Parts of a cache: enough CTAs for two on every SM, each with two tiles at least.
-int pick_splits(int64_t ctas, int max_len, int window, int max_q, int sms) {
+int splits_of(int groups, int kv_heads, int B, int group, int max_q, int max_len, int window, int sms) {
+  const int64_t columns = (int64_t)max_q * group;
   const int64_t seen = window > 0 ? std::min<int64_t>(max_len, (int64_t)window + max_q) : max_len;
   const int64_t tiles = (seen + KV_PAGE - 1) / KV_PAGE;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(2 * (int64_t)sms) / std::max<int64_t>(ctas, 1), tiles / 2, 64}));
-}
-
-int splits_of(int groups, int B, int group, int max_q, int max_len, int window, int sms) {
-  const int64_t columns = (int64_t)max_q * group;
+  if (columns >= CHUNK) return kv4_chunk_splits(kv_heads, B, group, max_q, tiles, sms);
   const int cols = pick_cols(columns);
-  return pick_splits((columns + cols - 1) / cols * groups * B, max_len, window, max_q, sms);
+  const int64_t ctas = (columns + cols - 1) / cols * groups * B;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({(2 * (int64_t)sms) / std::max<int64_t>(ctas, 1), tiles / 2, 64}));
 }
 
 size_t part_bytes(int splits, int64_t T, int heads, int D) {
@@ -651,18 +648,18 @@ oq_status launch(AttnParams& p, cudaStream_t st, int device) {
 size_t kv4_attention_workspace(const oq_kv4* kv, int64_t T, int B, int max_q, int max_len) {
   // the window only lowers the number of parts
   int dev = 0;
-  return part_bytes(splits_of(kv->groups, B, kv->heads / kv->kv_heads, max_q, max_len, 0, mx_sm_count(&dev)), T, kv->heads,
+  return part_bytes(splits_of(kv->groups, kv->kv_heads, B, kv->heads / kv->kv_heads, max_q, max_len, 0, mx_sm_count(&dev)), T, kv->heads,
                     kv->head_dim);
 }
 
 oq_status kv4_attention_launch(const AttentionArgs& a, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   AttnParams p;
-  std::memset(&p, 0, sizeof(p));
+  std::memset(&p.map, 0, sizeof(p.map));
   p.a = a;
   p.group = a.heads / a.kv_heads;
   int dev = 0;
-  p.splits = splits_of(a.kv.groups, a.kv.B, p.group, a.max_q, a.max_len, a.window, mx_sm_count(&dev));
+  p.splits = splits_of(a.kv.groups, a.kv_heads, a.kv.B, p.group, a.max_q, a.max_len, a.window, mx_sm_count(&dev));
   if (a.workspace_bytes < part_bytes(p.splits, a.T, a.heads, a.D)) {
     set_error("oq_kv4_attention: the workspace is too small");
     return OQ_ERR_INVALID_ARG;
@@ -670,15 +667,20 @@ oq_status kv4_attention_launch(const AttentionArgs& a, void* stream) {
   const int64_t rows = a.T * a.heads;
   p.part_o = static_cast<float*>(a.workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.splits * rows * a.D);
-  const cuuint64_t dims[2] = {128, (cuuint64_t)(a.kv.pages * a.kv.groups * KV_ROWS)};
-  const cuuint64_t strides[1] = {64};
-  const cuuint32_t box[2] = {128, 128};
-  oq_status r = mx_encode(&p.map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, a.kv.cache, dims, strides, box,
-                          CU_TENSOR_MAP_SWIZZLE_128B, "the cache");
-  if (r != OQ_OK) return r;
-  const int cols = pick_cols((int64_t)a.max_q * p.group);
-  if (a.D == 128) r = cols == 4 ? launch<4, 1>(p, st, dev) : cols == 8 ? launch<8, 1>(p, st, dev) : launch<16, 1>(p, st, dev);
-  else r = cols == 4 ? launch<4, 2>(p, st, dev) : cols == 8 ? launch<8, 2>(p, st, dev) : launch<16, 2>(p, st, dev);
+  oq_status r;
+  if ((int64_t)a.max_q * p.group >= CHUNK) {
+    r = kv4_chunk_launch(p, st, dev);
+  } else {
+    const cuuint64_t dims[2] = {128, (cuuint64_t)(a.kv.pages * a.kv.groups * KV_ROWS)};
+    const cuuint64_t strides[1] = {64};
+    const cuuint32_t box[2] = {128, 128};
+    r = mx_encode(&p.map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, a.kv.cache, dims, strides, box,
+                  CU_TENSOR_MAP_SWIZZLE_128B, "the cache");
+    if (r != OQ_OK) return r;
+    const int cols = pick_cols((int64_t)a.max_q * p.group);
+    if (a.D == 128) r = cols == 4 ? launch<4, 1>(p, st, dev) : cols == 8 ? launch<8, 1>(p, st, dev) : launch<16, 1>(p, st, dev);
+    else r = cols == 4 ? launch<4, 2>(p, st, dev) : cols == 8 ? launch<8, 2>(p, st, dev) : launch<16, 2>(p, st, dev);
+  }
   if (r != OQ_OK || p.splits == 1) return r;
   JoinParams j;
   j.part_o = p.part_o;

@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(Cfg<NT, MT>::NWARP * 32, Cfg<NT, MT>::MIN_CTAS
       const int64_t at = (int64_t)min(o0 + m, a.N - 1) * groups + c0 * SUB;
 #pragma unroll 4
       for (int k = threadIdx.x % PER; k < n; k += PER) {
-        scales[k * TILE + m] = k < left ? __ldg(static_cast<const uint16_t*>(a.scales) + at + k) : (uint16_t)0;
-        if constexpr (ZEROS) zeros[k * TILE + m] = k < left ? __ldg(a.zeros + at + k) : (uint8_t)0;
+        scales[k * TILE + m] = k < left ? __ldcg(static_cast<const uint16_t*>(a.scales) + at + k) : (uint16_t)0;
+        if constexpr (ZEROS) zeros[k * TILE + m] = k < left ? __ldcg(a.zeros + at + k) : (uint8_t)0;
       }
     }
     copy_wait<0>();
