@@ -16,7 +16,8 @@
 // keys) and tokens (of values) lie permuted within each eight, and q's channels and
 // P's tokens are taken in the same order.
 //
-// Warps: 0-3 and 4-7 the two query tiles, 8-11 decoding, 12 tensor memory and MMAs.
+// Warps: 0-3 and 4-7 the two query tiles, 8-15 decoding, 16 tensor memory and MMAs
+// (17-19 only give up registers).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -29,7 +30,10 @@ namespace oq {
 namespace {
 
 constexpr int QT = 128;                       // queries of a tile
-constexpr int DEC_WARP = 8, MMA_WARP = 12, NTHREADS = 13 * 32;
+constexpr int DEC_WARP = 8, MMA_WARP = 16, NTHREADS = 20 * 32, DEC_THREADS = 256;
+// registers of a thread of each four warps; together the launch's 640 x 96
+constexpr int SOFTMAX_REGS = 136, DECODE_REGS = 80, MMA_REGS = 48;
+static_assert(2 * SOFTMAX_REGS + 2 * DECODE_REGS + MMA_REGS == 5 * 96, "more would wait for good");
 constexpr float LAZY = 8.f, NONE = -1e30f;    // as in oq_kv4_attention.cu
 
 template <int D>
@@ -37,9 +41,9 @@ struct Cfg {
   static constexpr int Q = QT * D * 2, KT = KV_PAGE * D * 2;        // a tile of queries; of keys or values
   static constexpr int K0 = 2 * Q, V0 = K0 + 2 * KT;
   static constexpr int VS = V0 + 2 * KT;                            // V's scales: [2][D / 32][128] bf16
-  static constexpr int NANS = VS + 2 * (D / 32) * 256;              // [2][128] bits of NaN blocks
-  static constexpr int BAR = NANS + 256;
-  static constexpr size_t SMEM = 1024 + BAR + 8 * 16 + 64;
+  static constexpr int NANS = VS + 2 * (D / 32) * 256;              // [4][2 x 128] bits of NaN blocks
+  static constexpr int BAR = NANS + 1024;
+  static constexpr size_t SMEM = 1024 + BAR + 8 * 18 + 64;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr uint32_t S = 0, O = 2 * 128;                     // tensor memory columns: S of both tiles, O
 };
@@ -111,26 +115,25 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::BAR);
-  uint64_t* v_full = k_full + 2;
+  uint64_t* k_free = k_full + 2;
+  uint64_t* v_full = k_free + 2;
   uint64_t* v_free = v_full + 2;
   uint64_t* s_full = v_free + 2;    // of each query tile
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* q_full = pv_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
-  int* failed = reinterpret_cast<int*>(tmem_slot + 1);
-  int* there = failed + 1;          // [2] the tile's page exists
-  int* any_nan = there + 2;         // [2] a NaN block among its values
+  int* any_nan = reinterpret_cast<int*>(tmem_slot + 1);   // [4] the last tile (from 1) with a NaN block among its values
 
   const AttentionArgs& a = p.a;
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 4), mbar_init(&v_full[i], 4), mbar_init(&v_free[i], 1);
+      mbar_init(&k_full[i], 8), mbar_init(&k_free[i], 1), mbar_init(&v_full[i], 8), mbar_init(&v_free[i], 1);
       mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&pv_done[i], 1);
     }
     mbar_init(q_full, 8);
-    *failed = 0;
+    any_nan[0] = any_nan[1] = any_nan[2] = any_nan[3] = 0;
     fence_mbar_init();
   }
   if (warp == MMA_WARP) {
@@ -161,7 +164,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
   const int nt = tile_lo + (int)((int64_t)tiles * (split + 1) / p.splits) - first;
   const int* table = a.kv.table + (int64_t)b * a.kv.width + first;
 
-  if (warp == MMA_WARP) {
+  if (warp >= MMA_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(MMA_REGS));
+    if (warp == MMA_WARP) {
     constexpr uint32_t idesc1 = idesc_bf16_f32(QT, KV_PAGE), idesc2 = idesc_bf16_f32(QT, D);
     const uint32_t lead = elect_one();
     const uint64_t base = smem_desc_sw128(smem_base);
@@ -201,6 +206,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
     if (ok) {
       mma_s(0, 0);
       if (qtiles == 2) mma_s(1, 0);
+      commit(&k_free[0]);
     }
     for (int t = 0; ok && t < nt; ++t) {
       wait(&v_full[t & 1], t >> 1);
@@ -217,88 +223,111 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
         if (!ok) break;
         mma_o(1, t);
       }
-      commit(&v_free[t & 1]);   // and the keys, which were multiplied before
-      if (qtiles == 2 && t + 1 < nt) mma_s(1, t + 1);
+      commit(&v_free[t & 1]);
+      if (t + 1 < nt) {
+        if (qtiles == 2) mma_s(1, t + 1);
+        commit(&k_free[(t + 1) & 1]);
+      }
     }
     __syncwarp();
-  } else if (warp >= DEC_WARP && nt > 0) {
-    // ---- decoding: a thread has a token's keys, and a channel's values (D = 64: half of its tokens)
-    const int th = (int)threadIdx.x - DEC_WARP * 32, w4 = warp - DEC_WARP;
-    constexpr int NW = D / 8;                  // words of a thread, of keys and of values
-    const int ch = D == 128 ? th : th & 63, part = D == 128 ? 0 : th >> 6;
+    }
+  } else if (warp >= DEC_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DECODE_REGS));
+    if (nt > 0) {
+    // ---- decoding: a thread has half of a token's keys, and a channel's values of 64 or 32 tokens
+    const int th = (int)threadIdx.x - DEC_WARP * 32;
+    constexpr int NW = D / 16;                 // words of a thread, of keys and of values
+    const int key = th & 127, kpart = th >> 7, ch = th % D, vpart = th / D;
     const int64_t page_bytes = a.kv.groups * KV_GROUP_BYTES, group_at = hg * KV_GROUP_BYTES;
     uint4 kr[NW / 4], vr[NW / 4];
     uint32_t ksr = 0u, vsr = 0u;
-    bool okr = false;
-    auto fetch = [&](int t) {
+    const uint8_t* page_k = nullptr;           // the fetched tile's group, or null: not there
+    auto find = [&](int t) -> const uint8_t* {
       const int page = t < nt ? table[t] : -1;
-      okr = page >= 0 && page < a.kv.pages;
-      if (okr) {
-        const uint8_t* g = a.kv.cache + page * page_bytes + group_at;
+      return page >= 0 && page < a.kv.pages ? a.kv.cache + page * page_bytes + group_at : nullptr;
+    };
+    auto fetch_k = [&](const uint8_t* g) {
+      ksr = vsr = 0u;
 #pragma unroll
-        for (int i = 0; i < NW / 4; ++i) {
-          kr[i] = __ldcg(reinterpret_cast<const uint4*>(g + th * 64 + half * 32) + i);
-          vr[i] = __ldcg(reinterpret_cast<const uint4*>(g + (KV_V_ROW + half * 64 + ch) * 64 + part * 32) + i);
-        }
-        ksr = __ldcg(reinterpret_cast<const uint32_t*>(g + KV_KS_ROW * 64) + mx_tile_word(th));
-        vsr = __ldcg(reinterpret_cast<const uint32_t*>(g + KV_VS_ROW * 64) + th);
-      } else {
+      for (int i = 0; i < NW / 4; ++i) kr[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (g) {
 #pragma unroll
-        for (int i = 0; i < NW / 4; ++i) kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
-        ksr = vsr = 0u;
+        for (int i = 0; i < NW / 4; ++i) kr[i] = __ldcg(reinterpret_cast<const uint4*>(g + key * 64 + half * 32 + kpart * (NW * 4)) + i);
+        ksr = __ldcg(reinterpret_cast<const uint32_t*>(g + KV_KS_ROW * 64) + mx_tile_word(key));
+        vsr = __ldcg(reinterpret_cast<const uint32_t*>(g + KV_VS_ROW * 64) + key);
       }
     };
-    fetch(0);
+    auto fetch_v = [&](const uint8_t* g) {
+#pragma unroll
+      for (int i = 0; i < NW / 4; ++i) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (g) {
+#pragma unroll
+        for (int i = 0; i < NW / 4; ++i)
+          vr[i] = __ldcg(reinterpret_cast<const uint4*>(g + (KV_V_ROW + half * 64 + ch) * 64 + vpart * (NW * 4)) + i);
+      }
+    };
+    page_k = find(0);
+    const uint8_t* page_next = find(1);
+    fetch_k(page_k);
+    fetch_v(page_k);
     for (int t = 0; t < nt; ++t) {
       const int buf = t & 1;
+      const uint8_t* page_after = find(t + 2);
+      bool ok = t < 2 || mbar_wait(&k_free[buf], (uint32_t)(t / 2 - 1) & 1u, a.err);
       // V's scales of this thread's token (0 where nobody sees it), NaN blocks apart
-      const bool seen = okr && (first + t) * KV_PAGE + th < len;
+      const bool seen = page_k && (first + t) * KV_PAGE + key < len;
       uint32_t nans = 0u;
       {
         uint16_t* vs = reinterpret_cast<uint16_t*>(smem + C::VS) + buf * BLK * 128;
-        const int at = (th & ~7) | (th & 3) << 1 | (th >> 2 & 1);   // tokens j, j + 4 side by side
-#pragma unroll
-        for (int g = 0; g < BLK; ++g) {
+        const int at = (key & ~7) | (key & 3) << 1 | (key >> 2 & 1);   // tokens j, j + 4 side by side
+        for (int g = kpart * (BLK / 2); g < (kpart + 1) * (BLK / 2); ++g) {
           const uint32_t code = vsr >> (8 * (g + 2 * half)) & 255u;
           if (seen && code == 255u) nans |= 1u << g;
           vs[g * 128 + at] = (uint16_t)(seen && code != 255u ? scale_bits(code) : 0u);
         }
       }
-      const bool ok = t < 2 || mbar_wait(&v_free[buf], (uint32_t)(t / 2 - 1) & 1u, a.err);
-      if (named_bar_or(2, 128, !ok)) break;   // (all of them, or none)
-      smem[C::NANS + buf * 128 + th] = (unsigned char)nans;
-      const int any = named_bar_or(1, 128, nans != 0u);
-      if (th == 0) any_nan[buf] = any, there[buf] = okr;
+      // The marks of four tiles are kept: S of tile t - 2 is done, so P of tile t - 3 is.
+      if (nans) any_nan[t & 3] = t + 1;        // (the tile's number, so that it need not be cleared)
+      smem[C::NANS + (t & 3) * 256 + th] = (unsigned char)nans;
       unsigned char* kt = smem + C::K0 + buf * C::KT;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
         const uint4& v = kr[i / 4];
         const uint32_t w = i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
-        const uint32_t s1 = scale_bits(ksr >> (8 * (i / 4 + 2 * half)) & 255u), s = s1 | s1 << 16;
-        *reinterpret_cast<uint4*>(kt + tile_at(th, i)) =
-            make_uint4(mul_bf2(mul_bf2(code_pair<0>(w), BIG), s), mul_bf2(mul_bf2(code_pair<1>(w), BIG), s),
-                       mul_bf2(mul_bf2(code_pair<2>(w), BIG), s), mul_bf2(mul_bf2(code_pair<3>(w), BIG), s));
+        const uint32_t s1 = scale_bits(ksr >> (8 * ((kpart * NW + i) / 4 + 2 * half)) & 255u), s = s1 | s1 << 16;
+        if (ok)
+          *reinterpret_cast<uint4*>(kt + tile_at(key, kpart * NW + i)) =
+              make_uint4(mul_bf2(mul_bf2(code_pair<0>(w), BIG), s), mul_bf2(mul_bf2(code_pair<1>(w), BIG), s),
+                         mul_bf2(mul_bf2(code_pair<2>(w), BIG), s), mul_bf2(mul_bf2(code_pair<3>(w), BIG), s));
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[buf]);
+      if (lane == 0 && ok) mbar_arrive(&k_full[buf]);
+      fetch_k(page_next);
+      ok = ok && (t < 2 || mbar_wait(&v_free[buf], (uint32_t)(t / 2 - 1) & 1u, a.err));
+      if (named_bar_or(2, DEC_THREADS, !ok)) break;   // (all of them, or none)
       unsigned char* vt = smem + C::V0 + buf * C::KT;
-      const uint4* sc = reinterpret_cast<const uint4*>(smem + C::VS + (buf * BLK + (D == 128 ? w4 : w4 & 1)) * 256) + part * 8;
+      const uint4* sc = reinterpret_cast<const uint4*>(smem + C::VS + (buf * BLK + ch / 32) * 256) + vpart * NW;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
         const uint4& v = vr[i / 4];
         const uint32_t w = i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
         const uint4 s = sc[i];
-        *reinterpret_cast<uint4*>(vt + rows_at<D>(ch, part * 8 + i)) =
+        *reinterpret_cast<uint4*>(vt + rows_at<D>(ch, vpart * NW + i)) =
             make_uint4(mul_bf2(mul_bf2(code_pair<0>(w), BIG), s.x), mul_bf2(mul_bf2(code_pair<1>(w), BIG), s.y),
                        mul_bf2(mul_bf2(code_pair<2>(w), BIG), s.z), mul_bf2(mul_bf2(code_pair<3>(w), BIG), s.w));
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full[buf]);
-      fetch(t + 1);
+      fetch_v(page_next);
+      page_k = page_next;
+      page_next = page_after;
     }
-  } else if (warp < 8 && work) {
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+    if (work) {
     // ---- a query a thread
     const int q = warp >> 2, r = (warp & 3) * 32 + lane, col = c0 + q * QT + r;
     const bool mine = col < columns;
@@ -338,33 +367,78 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
     float M = NONE, l = 0.f;
     uint32_t nan_blocks = 0u;
     bool ok = true;
+    int next_page = nt > 0 ? table[0] : -1;
 #pragma unroll 1
     for (int t = 0; t < nt && q < qtiles; ++t) {
-      const int buf = t & 1, j0 = (first + t) * KV_PAGE;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&v_full[buf], (uint32_t)(t >> 1) & 1u, a.err)) &&
-           __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[q], (uint32_t)t & 1u, a.err));
+      const int j0 = (first + t) * KV_PAGE;
+      const int page = next_page;
+      next_page = t + 1 < nt ? table[t + 1] : -1;
+      const bool there = page >= 0 && page < a.kv.pages;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[q], (uint32_t)t & 1u, a.err));
       if (!ok) break;
       tc_fence_after();
-      const bool whole = there[buf] && j0 >= all_lo && j0 + KV_PAGE <= all_hi;
-      const int lo_j = (there[buf] ? see_lo : 1 << 30) - j0, hi_j = see_hi - j0;
-      float top = -INFINITY;
+      const bool whole = there && j0 >= all_lo && j0 + KV_PAGE <= all_hi;
+      const int lo_j = (there ? see_lo : 1 << 30) - j0, hi_j = see_hi - j0;
+      // 16 scores from column 16 c on, hidden ones -inf
+      auto hide = [&](uint32_t (&v)[16], int c) {
+        if (!whole) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(t_s + 32 * c, v);
-        tmem_wait_ld();
-        if (whole) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * c + i >= lo_j && 32 * c + i < hi_j) top = fmaxf(top, __uint_as_float(v[i]));
+          for (int i = 0; i < 16; ++i)
+            if (!(16 * c + i >= lo_j && 16 * c + i < hi_j)) v[i] = 0xFF800000u;
         }
-      }
-      const float m = top * sl2;
-      if (__any_sync(0xFFFFFFFFu, m > M + LAZY)) {
-        const float to = m > M + LAZY ? ceilf(m) : M, keep = ex2(M - to);
+      };
+      // P and its sum relative to M, all of it in registers: S is still there if a
+      // weight turns out to exceed the reference
+      uint32_t w[64];
+      float most = 0.f, part_sum = 0.f;
+      auto weigh = [&]() {
+        f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+        const f32x2 c2 = pack2(sl2, sl2), m2 = pack2(-M, -M);
+        float top[2] = {0.f, 0.f};
+        uint32_t v[2][16];
+        tmem_ld16(t_s, v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          tmem_wait_ld();
+          if (c < 7) tmem_ld16(t_s + 16 * (c + 1), v[(c + 1) & 1]);
+          hide(v[c & 1], c);
+#pragma unroll
+          for (int g = 0; g < 2; ++g)   // tokens j, j + 4 of eight side by side
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float x, y;
+              unpack2(fma2(pack2(__uint_as_float(v[c & 1][8 * g + j]), __uint_as_float(v[c & 1][8 * g + j + 4])), c2, m2), x, y);
+              x = ex2(x), y = ex2(y);
+              top[j & 1] = fmaxf(fmaxf(top[j & 1], x), y);
+              sum[j & 1] = add2(sum[j & 1], pack2(x, y));
+              w[8 * c + 4 * g + j] = mx_pack_bf16(x, y);
+            }
+        }
+        float sx, sy;
+        unpack2(add2(sum[0], sum[1]), sx, sy);
+        part_sum = sx + sy;
+        most = fmaxf(top[0], top[1]);
+      };
+      bool move = M == NONE && max(lo_j, 0) < min(hi_j, KV_PAGE);   // the first token it sees
+      while (ok) {
+        if (!__any_sync(0xFFFFFFFFu, move)) {
+          weigh();
+          move = most > 256.f;   // 2^LAZY
+          if (!__any_sync(0xFFFFFFFFu, move)) break;
+        }
+        move = false;
+        // the reference moves, and with it what is summed so far
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[16];
+          tmem_ld16(t_s + 16 * c, v);
+          tmem_wait_ld();
+          hide(v, c);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+        }
+        const float m = top * sl2, to = m > M + LAZY ? ceilf(m) : M, keep = ex2(M - to);
         if (t > 0) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pv_done[q], (uint32_t)(t - 1) & 1u, a.err));
           if (!ok) break;
@@ -382,37 +456,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
         l *= keep;
         M = to;
       }
-      f32x2 sum = pack2(0.f, 0.f);
-      const f32x2 c2 = pack2(sl2, sl2), m2 = pack2(-M, -M);
+      if (!ok) break;
+      l += part_sum;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(t_s + 32 * c, v);
-        tmem_wait_ld();
-        if (!whole) {
+        uint32_t u[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(32 * c + i >= lo_j && 32 * c + i < hi_j)) v[i] = 0xFF800000u;
-        }
-        uint32_t w[16];
-#pragma unroll
-        for (int g = 0; g < 4; ++g)   // tokens j, j + 4 of eight side by side
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x2 e = fma2(pack2(__uint_as_float(v[8 * g + j]), __uint_as_float(v[8 * g + j + 4])), c2, m2);
-            float x, y;
-            unpack2(e, x, y);
-            x = ex2(x), y = ex2(y);
-            sum = add2(sum, pack2(x, y));
-            w[4 * g + j] = mx_pack_bf16(x, y);
-          }
-        tmem_st16(t_s + 16 * c, w);
+        for (int i = 0; i < 16; ++i) u[i] = w[16 * c + i];
+        tmem_st16(t_s + 16 * c, u);
       }
-      float sx, sy;
-      unpack2(sum, sx, sy);
-      l += sx + sy;
-      if (any_nan[buf]) {   // NaN blocks of values: noted for the queries that see them
-        for (int i = max(lo_j, 0); i < min(hi_j, KV_PAGE); ++i) nan_blocks |= smem[C::NANS + buf * 128 + i];
+      // NaN blocks of values are noted for the queries that see them
+      if (any_nan[t & 3] == t + 1) {
+        for (int i = max(lo_j, 0); i < min(hi_j, KV_PAGE); ++i) nan_blocks |= smem[C::NANS + (t & 3) * 256 + i] | smem[C::NANS + (t & 3) * 256 + 128 + i];
       }
       tmem_wait_st();
       tc_fence_before();
@@ -450,6 +505,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
         if (mine && p.splits > 1) p.part_ml[part] = make_float2(M, l);
       }
       tc_fence_before();
+    }
     }
   }
   __syncthreads();
