@@ -626,42 +626,56 @@ def oq_linear_mx(layer: Layer, codes, scales, Wcodes, Wscales, y=None, y_dtype=N
 # ------------------------------------------------------------------ operators around attention
 def _heads(t, heads, D: int, device, name: str):
     """(address, token stride) of a [T, heads, D] tensor whose tokens' heads are contiguous."""
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads) or t.device != device:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads) or t.device != device:
         raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {D}] on {device}")
-    s = t.stride()
-    if t.numel() and ((D > 1 and s[2] != 1) or (t.shape[1] > 1 and s[1] != D)):
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D > 1 or s1 != D and shape[1] > 1) and t.numel():
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), s[0] if t.shape[0] > 1 else t.shape[1] * D
+    return t.data_ptr(), s0 if shape[0] > 1 else shape[1] * D
 
 
 def _ints(t, shape, device, name: str) -> int:
     """The address of a contiguous int32 tensor of this shape on `device`."""
-    if t.dtype is not _torch().int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not _int32() or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 {list(shape)} on {device}")
     return t.data_ptr()
 
 
+_i32 = None
+
+
+def _int32():
+    global _i32
+    if _i32 is None:
+        _i32 = _torch().int32
+    return _i32
+
+
+def _new_heads(T: int, heads: int, D: int, dtype, device):
+    return _torch().empty_strided((T, heads, D), (heads * D, D, 1), dtype=dtype, device=device)
+
+
 def _qk_args(q_gain, k_gain, table, positions, T: int, D: int, interleaved: bool, norm: bool, device):
-    """The arguments that norm and rotation share: gains .. gain type; table .. flags."""
-    torch = _torch()
-    gdt, gains = OQ_DTYPE_F32, [None, None]
-    for i, g in enumerate((q_gain, k_gain)):
-        if g is not None:
-            if g.dtype is not (q_gain if q_gain is not None else k_gain).dtype:
-                raise ValueError("q_gain and k_gain must have one type")
-            gdt, gains[i] = _mx_dtype(g), _mx_rows(g, (D,), g.dtype, device, "qk"[i] + "_gain")
+    """The arguments that norm and rotation share: gains and their type; table .. flags."""
+    gdt, pq, pk = OQ_DTYPE_F32, None, None
+    if q_gain is not None:
+        gdt, pq = _mx_dtype(q_gain), _mx_rows(q_gain, (D,), q_gain.dtype, device, "q_gain")
+        if k_gain is not None and k_gain.dtype is not q_gain.dtype:
+            raise ValueError("q_gain and k_gain must have one type")
+    if k_gain is not None:
+        gdt, pk = _mx_dtype(k_gain), _mx_rows(k_gain, (D,), k_gain.dtype, device, "k_gain")
     pt, rows, rot, pp = None, 0, 0, None
     if table is not None:
-        if table.dim() != 3 or table.shape[2] != 2 or table.dtype is not torch.float32 or table.device != device \
-                or not table.is_contiguous():
+        rows, half, two = table.shape if table.dim() == 3 else (0, 0, 0)
+        if two != 2 or table.dtype is not _torch().float32 or table.device != device or not table.is_contiguous():
             raise ValueError(f"table must be contiguous float32 [positions, rot / 2, 2] on {device}")
-        pt, rows, rot = table.data_ptr(), table.shape[0], 2 * table.shape[1]
+        pt, rot = table.data_ptr(), 2 * half
         if positions is not None:
             pp = _ints(positions, (T,), device, "positions")
     elif positions is not None:
         raise ValueError("positions without a table")
-    flags = (OQ_QK_INTERLEAVED if interleaved else 0) | (0 if norm else OQ_QK_NO_NORM)
-    return (gains[0], gains[1], gdt), (pt, rows, rot, pp, flags)
+    return pq, pk, gdt, pt, rows, rot, pp, (OQ_QK_INTERLEAVED if interleaved else 0) | (0 if norm else OQ_QK_NO_NORM)
 
 
 def oq_qk_norm_rope(q, k=None, q_gain=None, k_gain=None, eps: float = 1e-6, table=None, positions=None,
@@ -671,33 +685,37 @@ def oq_qk_norm_rope(q, k=None, q_gain=None, k_gain=None, eps: float = 1e-6, tabl
     stride) -> (q_out, k_out) of the same types.  table: fp32 [positions, rot / 2,
     2] (cos, sin); positions: int32 [T], its row for each token (default: t).
     An output may be its input."""
-    torch = _torch()
     if q.dim() != 3 or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [T, heads, D]")
     T, H, D = q.shape
-    device, dt = q.device, _mx_dtype(q)
+    device, dtype, dt = q.device, q.dtype, _mx_dtype(q)
     pq, sq = _heads(q, None, D, device, "q")
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=q.dtype, device=device)
-    elif q_out.dtype is not q.dtype or q_out.shape != q.shape:
-        raise ValueError("q_out must have q's type and shape")
-    pqo, sqo = _heads(q_out, H, D, device, "q_out")
+        q_out = _new_heads(T, H, D, dtype, device)
+        pqo, sqo = q_out.data_ptr(), H * D
+    else:
+        if q_out.dtype is not dtype or q_out.shape != q.shape:
+            raise ValueError("q_out must have q's type and shape")
+        pqo, sqo = _heads(q_out, H, D, device, "q_out")
     pk = pko = None
     sk = sko = KH = 0
     if k is not None:
-        if k.dtype is not q.dtype or k.dim() != 3 or k.shape[0] != T:
+        if k.dtype is not dtype or k.dim() != 3 or k.shape[0] != T:
             raise ValueError("k must have q's type and tokens")
         KH = k.shape[1]
         pk, sk = _heads(k, None, D, device, "k")
         if k_out is None:
-            k_out = torch.empty((T, KH, D), dtype=k.dtype, device=device)
-        elif k_out.dtype is not k.dtype or k_out.shape != k.shape:
-            raise ValueError("k_out must have k's type and shape")
-        pko, sko = _heads(k_out, KH, D, device, "k_out")
+            k_out = _new_heads(T, KH, D, dtype, device)
+            pko, sko = k_out.data_ptr(), KH * D
+        else:
+            if k_out.dtype is not dtype or k_out.shape != k.shape:
+                raise ValueError("k_out must have k's type and shape")
+            pko, sko = _heads(k_out, KH, D, device, "k_out")
     elif k_out is not None or k_gain is not None:
         raise ValueError("k_out or k_gain without k")
-    gains, turn = _qk_args(q_gain, k_gain, table, positions, T, D, interleaved, norm, device)
-    _launch("oq_qk_norm_rope", device, pq, sq, H, pk, sk, KH, dt, T, D, *gains, eps, *turn, pqo, sqo, pko, sko)
+    g0, g1, gdt, pt, rows, rot, pp, flags = _qk_args(q_gain, k_gain, table, positions, T, D, interleaved, norm, device)
+    _launch("oq_qk_norm_rope", device, pq, sq, H, pk, sk, KH, dt, T, D, g0, g1, gdt, eps, pt, rows, rot, pp, flags, pqo, sqo,
+            pko, sko)
     return q_out, k_out
 
 
@@ -709,6 +727,8 @@ class Kv4:
         self._lib = lib
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.groups = (kv_heads * head_dim + 127) // 128
+        self.scale = head_dim ** -0.5
+        self.workspaces = {}   # bytes of attention's workspace by (device, T, B, max_q, max_len)
 
     @property
     def handle(self):
@@ -749,14 +769,14 @@ def oq_kv4_cache_size(kv: Kv4, pages: int) -> int:
 
 def _kv4_view(kv: Kv4, cache, page_table, cu, lens, device):
     """cache, pages, page table, its width, cu, lens, B as the C calls take them."""
-    if cache.dim() != 4:
+    shape, table = cache.shape, page_table.shape
+    if len(shape) != 4:
         raise ValueError("cache must be [pages, groups, 272, 64]")
-    pages = cache.shape[0]
-    pc = _mx_ptr(cache, (pages, kv.groups, 272, 64), device, "cache")
-    if page_table.dim() != 2:
+    if len(table) != 2:
         raise ValueError("page_table must be [B, pages of a sequence]")
-    B, width = page_table.shape
-    return (pc, pages, _ints(page_table, (B, width), device, "page_table"), width, _ints(cu, (B + 1,), device, "cu"),
+    B, width = table
+    return (_mx_ptr(cache, (shape[0], kv.groups, 272, 64), device, "cache"), shape[0],
+            _ints(page_table, table, device, "page_table"), width, _ints(cu, (B + 1,), device, "cu"),
             _ints(lens, (B,), device, "lens"), B)
 
 
@@ -781,14 +801,14 @@ def oq_kv4_append(kv: Kv4, q, k, v, cache, page_table, cu, lens, q_gain=None, k_
             raise ValueError("q must have k's type and tokens")
         pq, sq = _heads(q, kv.heads, D, device, "q")
         if q_out is None:
-            q_out = torch.empty((T, kv.heads, D), dtype=torch.bfloat16, device=device)
+            q_out = _new_heads(T, kv.heads, D, torch.bfloat16, device)
             pqo = q_out.data_ptr()
         else:
             pqo = _mx_rows(q_out, (T, kv.heads, D), torch.bfloat16, device, "q_out")
     elif q_out is not None or q_gain is not None:
         raise ValueError("q_out or q_gain without q")
-    gains, turn = _qk_args(q_gain, k_gain, table, positions, T, D, interleaved, norm, device)
-    _launch("oq_kv4_append", device, kv.handle, pq, sq, pk, sk, pv, sv, dt, T, *gains, eps, *turn, pqo,
+    g0, g1, gdt, pt, rows, rot, pp, flags = _qk_args(q_gain, k_gain, table, positions, T, D, interleaved, norm, device)
+    _launch("oq_kv4_append", device, kv.handle, pq, sq, pk, sk, pv, sv, dt, T, g0, g1, gdt, eps, pt, rows, rot, pp, flags, pqo,
             *_kv4_view(kv, cache, page_table, cu, lens, device))
     return q_out
 
@@ -801,14 +821,13 @@ def oq_kv4_read(kv: Kv4, cache, page_table, cu, lens, T: int, dtype=None, k=None
     if device.type != "cuda":
         raise ValueError("cache must be a CUDA tensor")
     dtype = dtype if dtype is not None else k.dtype if k is not None else torch.float32
-    out = []
-    for name, t in (("k", k), ("v", v)):
-        t = torch.empty(shape, dtype=dtype, device=device) if t is None else t
-        _mx_rows(t, shape, dtype, device, name)
-        out.append(t)
-    _launch("oq_kv4_read", device, kv.handle, *_kv4_view(kv, cache, page_table, cu, lens, device), T, out[0].data_ptr(),
-            out[1].data_ptr(), _mx_dtype(out[0]))
-    return out[0], out[1]
+    if k is None:
+        k = _new_heads(*shape, dtype, device)
+    if v is None:
+        v = _new_heads(*shape, dtype, device)
+    _launch("oq_kv4_read", device, kv.handle, *_kv4_view(kv, cache, page_table, cu, lens, device), T,
+            _mx_rows(k, shape, dtype, device, "k"), _mx_rows(v, shape, dtype, device, "v"), _mx_dtype(k))
+    return k, v
 
 
 def oq_kv4_attention_workspace_size(kv: Kv4, T: int, B: int, max_q: int, max_len: int) -> int:
@@ -830,18 +849,28 @@ def oq_kv4_attention(kv: Kv4, q, cache, page_table, cu, lens, max_q: int, max_le
     view = _kv4_view(kv, cache, page_table, cu, lens, device)
     max_len = max_len or min(view[3] * OQ_KV4_PAGE, 0x7FFFFFFF)
     if y is None:
-        y = torch.empty((T, kv.heads, D), dtype=torch.bfloat16, device=device)
+        y = _new_heads(T, kv.heads, D, torch.bfloat16, device)
         py = y.data_ptr()
     else:
         py = _mx_rows(y, (T, kv.heads, D), torch.bfloat16, device, "y")
+    pw, nw = None, 0
     if workspace is None:
-        with torch.cuda.device(device):   # (the split depends on the device's SMs)
-            need = oq_kv4_attention_workspace_size(kv, T, view[6], max_q, max_len)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+        sizes = (device.index, T, view[6], max_q, max_len)
+        nw = kv.workspaces.get(sizes)
+        if nw is None:
+            with torch.cuda.device(device):   # (the split depends on the device's SMs)
+                nw = oq_kv4_attention_workspace_size(kv, T, view[6], max_q, max_len)
+            if len(kv.workspaces) >= 4096:
+                kv.workspaces.clear()
+            kv.workspaces[sizes] = nw
+        if nw:
+            workspace = torch.empty_strided((nw,), (1,), dtype=torch.uint8, device=device)
+            pw = workspace.data_ptr()
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {device}")
-    pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _launch("oq_kv4_attention", device, kv.handle, pq, sq, T, *view, max_q, max_len, D ** -0.5 if scale is None else scale,
+    else:
+        pw, nw = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch("oq_kv4_attention", device, kv.handle, pq, sq, T, *view, max_q, max_len, kv.scale if scale is None else scale,
             OQ_ATTN_CAUSAL if causal else 0, window, py, pw, nw)
     return y
 
