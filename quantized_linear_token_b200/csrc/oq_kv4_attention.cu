@@ -33,13 +33,16 @@
 #include "oq_kv4.cuh"
 #include "oq_mx_ptx.cuh"
 
+#ifndef VC4
+#define VC4 3
+#define VU4 4
+#define VU8 5
+#endif
 namespace oq {
 namespace {
 
 constexpr int TMA_WARP = 4, MMA_WARP = 5, NTHREADS = 6 * 32;
-constexpr int UNIT = 17 * 1024;        // a tile of K (with its scales) or of V, spread to 8-bit containers
-constexpr int UNITS = 5;
-constexpr int KV_SCALES = 16 * 1024;   // offset of K's scales in a unit
+constexpr int UNIT = 16 * 1024;        // a tile of K or of V, spread to 8-bit containers
 constexpr float LAZY = 8.f;            // log2 of the largest weight relative to the running reference
 constexpr float NONE = -1e30f;         // reference of a query that has seen no token
 
@@ -47,6 +50,7 @@ constexpr float NONE = -1e30f;         // reference of a query that has seen no 
 template <int COLS, int HP>
 struct Cfg {
   static constexpr int HC = HP * COLS;                       // queries with their head of the group
+  static constexpr int CTAS = COLS == 4 ? VC4 : 2, UNITS = COLS > 4 ? VU8 : HP == 2 && VC4 == 3 ? 3 : VU4;   // CTAs an SM; units in the ring
   // columns of S, for each head: first terms, second terms.  Heads are multiplied
   // apart: a NaN among one's keys is nothing to the other.
   static constexpr int N1H = 2 * COLS < 16 ? 16 : 2 * COLS, N1 = HP * N1H;
@@ -56,11 +60,13 @@ struct Cfg {
   static constexpr int SB = N2 + 2 * N1 + SF <= 256 ? 2 : 1; // S buffers
   static constexpr uint32_t TMEM = N2 + SB * N1 + SF <= 128 ? 128 : 256;
   static_assert(N2 + SB * N1 + SF <= 256 && N2 <= 128 && HC <= 32, "tensor memory: two CTAs an SM");
-  static constexpr int P = UNITS * UNIT, Q = P + 128 * 128, SFQ = Q + N1 * 128, SFP = SFQ + HP * 512, ONES = SFP + 512;
-  static constexpr int RED = ONES + 512;                     // [4][32] floats
+  static constexpr int PITCH = N2;                           // bytes of a token in P: a swizzle's row
+  static constexpr int P = UNITS * UNIT, Q = P + 128 * PITCH, KS = Q + N1 * 128, SFQ = KS + UNITS * 512;
+  static constexpr int SFP = SFQ + HP * 512;
+  static constexpr int RED = SFP + 512, ONES = RED;          // [4][32] floats; before the first tile V's ones
   static constexpr int BAR = RED + 512;
   static constexpr size_t SMEM = 1024 + BAR + 8 * (2 * UNITS + 2 * SB + 3) + 64;
-  static_assert(SMEM <= 113 * 1024, "two CTAs an SM");
+  static_assert((SMEM + 1024) * CTAS <= 228 * 1024, "CTAs an SM");
 };
 
 struct AttnParams : AttnSplit {
@@ -101,9 +107,19 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const float* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// a K-major operand's other form, for P: [token][column], 128 bytes of columns a
-// token, swizzled as the K-major tiles are; groups of eight tokens 1024 bytes apart
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr) { return smem_desc_sw128(addr); }
+// P as the second product's B operand, columns contiguous: [token][PITCH bytes] in
+// the swizzle of that row length, groups of eight tokens 8 PITCH apart
+template <int PITCH>
+__device__ __forceinline__ uint64_t smem_desc_p(uint32_t addr) {
+  return (smem_desc_sw128(addr) & ~((uint64_t)0x3FFF << 32) & ~((uint64_t)7 << 61)) | (uint64_t)(8 * PITCH >> 4) << 32 |
+         (uint64_t)(PITCH == 128 ? 2 : PITCH == 64 ? 4 : 6) << 61;
+}
+// place of 16-byte chunk c of a token's columns
+template <int PITCH>
+__device__ __forceinline__ uint32_t p_at(int token, int c) {
+  const int turn = PITCH == 128 ? token & 7 : PITCH == 64 ? token >> 1 & 3 : token >> 2 & 1;
+  return (uint32_t)(token * PITCH + ((c ^ turn) << 4));
+}
 
 __device__ __forceinline__ float warp_max_nan(float v) {
   float r;
@@ -147,9 +163,9 @@ __device__ __forceinline__ float2 unpack_h2(uint32_t h) {
 }
 
 template <int COLS, int HP>
-__global__ void __launch_bounds__(NTHREADS, 2) attention_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_kernel(const __grid_constant__ AttnParams p) {
   using C = Cfg<COLS, HP>;
-  constexpr int HC = C::HC, N1 = C::N1, N2 = C::N2, SB = C::SB;
+  constexpr int HC = C::HC, N1 = C::N1, N2 = C::N2, SB = C::SB, UNITS = C::UNITS;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -224,7 +240,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) attention_kernel(const __grid_con
         const int64_t row = ((int64_t)page * a.kv.groups + hg) * KV_ROWS;
         mbar_arrive_expect_tx(&full[s], is_k ? 8192 + 512 : 8192);
         tma_load_2d(dst, &p.map, 0, (int32_t)(row + (is_k ? 0 : KV_V_ROW)), &full[s]);
-        if (is_k) bulk_g2s(dst + KV_SCALES, a.kv.cache + (row + KV_KS_ROW) * 64, 512, &full[s]);
+        if (is_k) bulk_g2s(smem + C::KS + s * 512, a.kv.cache + (row + KV_KS_ROW) * 64, 512, &full[s]);
       }
       // no copy may be in flight when the CTA leaves
       for (int g = u > UNITS ? u - UNITS : 0; g < u; ++g) mbar_wait(&full[g % UNITS], (uint32_t)(g / UNITS) & 1u, a.err);
@@ -234,7 +250,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) attention_kernel(const __grid_con
     constexpr uint32_t idesc1 = idesc_mx(128, C::N1H, 5, 0), idesc2 = idesc_mx(128, N2, 5, 0) | (1u << 16);
     const uint32_t lead = elect_one();
     const uint64_t unit0 = smem_desc_sw128(smem_base), q0 = smem_desc_sw128(smem_base + C::Q);
-    const uint64_t p0 = smem_desc_mn_sw128(smem_base + C::P), ks0 = smem_desc_scales(smem_base + KV_SCALES);
+    const uint64_t p0 = smem_desc_p<C::PITCH>(smem_base + C::P), ks0 = smem_desc_scales(smem_base + C::KS);
     bool ok = nt > 0 && __all_sync(0xFFFFFFFFu, mbar_wait(q_full, 0u, a.err));
     if (ok) {
       tc_fence_after();
@@ -255,7 +271,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) attention_kernel(const __grid_con
         if (lead) {
           const uint64_t off = (uint64_t)s * (UNIT >> 4);
           const uint32_t sfk = t_sf + C::SF_K + 4 * (t & 1);
-          tc_copy_scales<1>(sfk, ks0 + off);
+          tc_copy_scales<1>(sfk, ks0 + (uint64_t)(s * 512 >> 4));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int h = k * HP / 4;
@@ -278,7 +294,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) attention_kernel(const __grid_con
           tc_copy_scales<1>(t_sf + C::SF_P, smem_desc_scales(smem_base + C::SFP));
 #pragma unroll
           for (int k = 0; k < 4; ++k)   // 32 tokens: 32 bytes of V's rows, 32 rows of P
-            tc_mma_mx<false>(t_o, unit0 + off + 2 * k, p0 + (uint64_t)(k * 32 * 128 >> 4), idesc2 | idesc_mx_sf(k),
+            tc_mma_mx<false>(t_o, unit0 + off + 2 * k, p0 + (uint64_t)(k * 32 * C::PITCH >> 4), idesc2 | idesc_mx_sf(k),
                              t_sf + C::SF_ONE, t_sf + C::SF_P, t > 1 || k > 0);
           tc_commit(&empty[s]);
           tc_commit(p_free);
@@ -356,6 +372,32 @@ __global__ void __launch_bounds__(NTHREADS, 2) attention_kernel(const __grid_con
         next_vs = *reinterpret_cast<const uint32_t*>(a.kv.cache + next_page * page_bytes + vs_at);
       const int j0 = (first + t) * KV_PAGE, j = j0 + key;
       const int sb = t % SB;
+      // ---- what is hidden
+      const bool there = page >= 0 && page < a.kv.pages && j < len;
+      uint32_t seen = there ? 0xFFFFFFFFu : 0u;   // bit c: query c sees this token
+      if (steps && ((a.causal && j0 + KV_PAGE - 1 > past + i_first) || (a.window > 0 && j0 <= past + i_last - a.window))) {
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+          const int at = past + (c0 + c) / p.group;
+          if ((a.causal && j > at) || (a.window > 0 && j <= at - a.window)) {
+#pragma unroll
+            for (int h = 0; h < HP; ++h) seen &= ~(1u << (h * COLS + c));
+          }
+        }
+      }
+      // V's scales relative to the largest among the warp's seen tokens
+      const uint32_t codes = seen ? vs : 0u;
+      uint32_t ref[4], fac[4];
+      bool nan_block = false;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t code = codes >> (8 * g) & 255u;
+        nan_block |= code == 255u;
+        ref[g] = __reduce_max_sync(0xFFFFFFFFu, code == 255u ? 0u : code);
+        const int d = (int)(code == 255u ? 0u : code) - (int)ref[g];   // 2^d in fp16, 0 below its subnormals
+        const uint32_t f = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
+        fac[g] = f | f << 16;
+      }
       bool ok = mbar_wait(&s_full[sb], (uint32_t)(t / SB) & 1u, a.err);
       tc_fence_after();
       float s[HC];
@@ -373,19 +415,6 @@ __global__ void __launch_bounds__(NTHREADS, 2) attention_kernel(const __grid_con
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free[sb]);
-      // ---- what is hidden
-      const bool there = page >= 0 && page < a.kv.pages && j < len;
-      uint32_t seen = there ? 0xFFFFFFFFu : 0u;   // bit c: query c sees this token
-      if (steps && ((a.causal && j0 + KV_PAGE - 1 > past + i_first) || (a.window > 0 && j0 <= past + i_last - a.window))) {
-#pragma unroll
-        for (int c = 0; c < COLS; ++c) {
-          const int at = past + (c0 + c) / p.group;
-          if ((a.causal && j > at) || (a.window > 0 && j <= at - a.window)) {
-#pragma unroll
-            for (int h = 0; h < HP; ++h) seen &= ~(1u << (h * COLS + c));
-          }
-        }
-      }
       float m_own = -INFINITY, bias[HC];
       bool beyond = false;
 #pragma unroll
@@ -452,22 +481,8 @@ __global__ void __launch_bounds__(NTHREADS, 2) attention_kernel(const __grid_con
         hi2[c / 2] = h;
         lo2[c / 2] = pack_h2((w[0] - f.x) * 32.f, (w[1] - f.y) * 32.f);
       }
-      // V's scales relative to the largest among the warp's seen tokens
-      const uint32_t codes = seen ? vs : 0u;
-      uint32_t ref[4], fac[4];
-      bool nan_block = false;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint32_t code = codes >> (8 * g) & 255u;
-        nan_block |= code == 255u;
-        ref[g] = __reduce_max_sync(0xFFFFFFFFu, code == 255u ? 0u : code);
-        const int d = (int)(code == 255u ? 0u : code) - (int)ref[g];   // 2^d in fp16, 0 below its subnormals
-        const uint32_t f = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
-        fac[g] = f | f << 16;
-      }
       if (t > 0 && !mbar_wait(p_free, (uint32_t)(t - 1) & 1u, a.err)) *failed = 1;
       const bool any_nan = __any_sync(0xFFFFFFFFu, nan_block);
-      unsigned char* row = smem + C::P + key * 128;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int h0 = HP == 2 ? (g >> 1) * COLS : 0;
@@ -487,12 +502,12 @@ __global__ void __launch_bounds__(NTHREADS, 2) attention_kernel(const __grid_con
           }
         }
         if constexpr (COLS == 16) {
-          *reinterpret_cast<uint4*>(row + (((2 * g) ^ (key & 7)) << 4)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-          *reinterpret_cast<uint4*>(row + (((2 * g + 1) ^ (key & 7)) << 4)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+          *reinterpret_cast<uint4*>(smem + C::P + p_at<C::PITCH>(key, 2 * g)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          *reinterpret_cast<uint4*>(smem + C::P + p_at<C::PITCH>(key, 2 * g + 1)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
         } else if constexpr (COLS == 8) {
-          *reinterpret_cast<uint4*>(row + ((g ^ (key & 7)) << 4)) = make_uint4(w1[0], w1[1], w2[0], w2[1]);
+          *reinterpret_cast<uint4*>(smem + C::P + p_at<C::PITCH>(key, g)) = make_uint4(w1[0], w1[1], w2[0], w2[1]);
         } else {
-          *reinterpret_cast<uint2*>(row + (((g >> 1) ^ (key & 7)) << 4) + (g & 1) * 8) = make_uint2(w1[0], w2[0]);
+          *reinterpret_cast<uint2*>(smem + C::P + p_at<C::PITCH>(key, g >> 1) + (g & 1) * 8) = make_uint2(w1[0], w2[0]);
         }
       }
       // the block's scales: 2^(V's reference + the block's power of two - the query's reference), 2^-5 for second terms
@@ -619,7 +634,8 @@ int splits_of(int groups, int kv_heads, int B, int group, int max_q, int max_len
   if (columns >= CHUNK) return kv4_chunk_splits(kv_heads, B, group, max_q, tiles, sms);
   const int cols = pick_cols(columns);
   const int64_t ctas = (columns + cols - 1) / cols * groups * B;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(2 * (int64_t)sms) / std::max<int64_t>(ctas, 1), tiles / 2, 64}));
+  const int64_t slots = (cols == 4 ? VC4 : 2) * (int64_t)sms;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({slots / std::max<int64_t>(ctas, 1), tiles / 2, 64}));
 }
 
 size_t part_bytes(int splits, int64_t T, int heads, int D) {
