@@ -33,11 +33,6 @@
 #include "oq_kv4.cuh"
 #include "oq_mx_ptx.cuh"
 
-#ifndef VC4
-#define VC4 3
-#define VU4 4
-#define VU8 5
-#endif
 namespace oq {
 namespace {
 
@@ -50,7 +45,7 @@ constexpr float NONE = -1e30f;         // reference of a query that has seen no 
 template <int COLS, int HP>
 struct Cfg {
   static constexpr int HC = HP * COLS;                       // queries with their head of the group
-  static constexpr int CTAS = COLS == 4 ? VC4 : 2, UNITS = COLS > 4 ? VU8 : HP == 2 && VC4 == 3 ? 3 : VU4;   // CTAs an SM; units in the ring
+  static constexpr int CTAS = COLS <= 4 ? 3 : 2, UNITS = COLS > 4 ? 5 : HP == 2 ? 3 : 4;   // CTAs an SM; units in the ring
   // columns of S, for each head: first terms, second terms.  Heads are multiplied
   // apart: a NaN among one's keys is nothing to the other.
   static constexpr int N1H = 2 * COLS < 16 ? 16 : 2 * COLS, N1 = HP * N1H;
@@ -60,7 +55,7 @@ struct Cfg {
   static constexpr int SB = N2 + 2 * N1 + SF <= 256 ? 2 : 1; // S buffers
   static constexpr uint32_t TMEM = N2 + SB * N1 + SF <= 128 ? 128 : 256;
   static_assert(N2 + SB * N1 + SF <= 256 && N2 <= 128 && HC <= 32, "tensor memory: two CTAs an SM");
-  static constexpr int PITCH = N2;                           // bytes of a token in P: a swizzle's row
+  static constexpr int PITCH = N2 < 32 ? 32 : N2;            // bytes of a token in P: a swizzle's row
   static constexpr int P = UNITS * UNIT, Q = P + 128 * PITCH, KS = Q + N1 * 128, SFQ = KS + UNITS * 512;
   static constexpr int SFP = SFQ + HP * 512;
   static constexpr int RED = SFP + 512, ONES = RED;          // [4][32] floats; before the first tile V's ones
@@ -93,7 +88,11 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, float* v) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
-  if constexpr (N >= 8) {
+  if constexpr (N == 2) {
+    uint32_t r[2];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr) : "memory");
+    v[0] = __uint_as_float(r[0]), v[1] = __uint_as_float(r[1]);
+  } else if constexpr (N >= 8) {
 #pragma unroll
     for (int i = 0; i < N; i += 8) tmem_ld8(taddr + i, v + i);
   } else {
@@ -386,17 +385,17 @@ __global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_ker
         }
       }
       // V's scales relative to the largest among the warp's seen tokens
-      const uint32_t codes = seen ? vs : 0u;
+      // NaN codes apart: they are rare and dealt with where P is written
+      const uint32_t bad = seen ? __vcmpeq4(vs, 0xFFFFFFFFu) : 0u, codes = seen ? vs & ~bad : 0u;
+      const bool any_nan = __any_sync(0xFFFFFFFFu, bad != 0u);
       uint32_t ref[4], fac[4];
-      bool nan_block = false;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const uint32_t code = codes >> (8 * g) & 255u;
-        nan_block |= code == 255u;
-        ref[g] = __reduce_max_sync(0xFFFFFFFFu, code == 255u ? 0u : code);
-        const int d = (int)(code == 255u ? 0u : code) - (int)ref[g];   // 2^d in fp16, 0 below its subnormals
-        const uint32_t f = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
-        fac[g] = f | f << 16;
+        ref[g] = __reduce_max_sync(0xFFFFFFFFu, code);
+        // 2^(code - reference) in fp16, twice; nothing below 2^-30
+        const float f = __uint_as_float((uint32_t)(max((int)code - (int)ref[g], -30) + 127) << 23);
+        fac[g] = pack_h2(f, f);
       }
       bool ok = mbar_wait(&s_full[sb], (uint32_t)(t / SB) & 1u, a.err);
       tc_fence_after();
@@ -450,16 +449,14 @@ __global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_ker
         }
         if (t > 0) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
+          for (int n = 0; n < N2; n += 4) {
+            float o[4];
+            tmem_ld4(t_o + my + n, o);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < COLS; c += 4) {
-              float o[4];
-              tmem_ld4(t_o + my + g * COLS + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[i] *= keep[(HP == 2 ? (g >> 2) * COLS : 0) + c + i];
-              tmem_st4(t_o + my + g * COLS + c, o);
-            }
+            for (int i = 0; i < 4; ++i) o[i] *= keep[(HP == 2 ? ((n + i) / COLS >> 2) * COLS : 0) + (n + i) % COLS];
+            tmem_st4(t_o + my + n, o);
+          }
           tmem_wait_st();
         }
         named_bar_sync(1, 128);   // `red` is read
@@ -482,18 +479,24 @@ __global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_ker
         lo2[c / 2] = pack_h2((w[0] - f.x) * 32.f, (w[1] - f.y) * 32.f);
       }
       if (t > 0 && !mbar_wait(p_free, (uint32_t)(t - 1) & 1u, a.err)) *failed = 1;
-      const bool any_nan = __any_sync(0xFFFFFFFFu, nan_block);
+      uint32_t word[4];   // two queries: all of a token's columns
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int h0 = HP == 2 ? (g >> 1) * COLS : 0;
-        uint32_t w1[COLS / 4], w2[COLS / 4];
+        constexpr int W = COLS < 4 ? 1 : COLS / 4;
+        uint32_t w1[W], w2[W];
+        if constexpr (COLS == 2) {
+          w1[0] = cvt_e4m3_h2(mul_h2(hi2[h0 / 2], fac[g]));
+          w2[0] = cvt_e4m3_h2(mul_h2(lo2[h0 / 2], fac[g]));
+        } else {
 #pragma unroll
-        for (int c = 0; c < COLS; c += 4) {
-          const int at = (h0 + c) / 2;
-          w1[c / 4] = cvt_e4m3_h2(mul_h2(hi2[at], fac[g])) | cvt_e4m3_h2(mul_h2(hi2[at + 1], fac[g])) << 16;
-          w2[c / 4] = cvt_e4m3_h2(mul_h2(lo2[at], fac[g])) | cvt_e4m3_h2(mul_h2(lo2[at + 1], fac[g])) << 16;
+          for (int c = 0; c < COLS; c += 4) {
+            const int at = (h0 + c) / 2;
+            w1[c / 4] = cvt_e4m3_h2(mul_h2(hi2[at], fac[g])) | cvt_e4m3_h2(mul_h2(hi2[at + 1], fac[g])) << 16;
+            w2[c / 4] = cvt_e4m3_h2(mul_h2(lo2[at], fac[g])) | cvt_e4m3_h2(mul_h2(lo2[at + 1], fac[g])) << 16;
+          }
         }
-        if (any_nan && (codes >> (8 * g) & 255u) == 255u) {   // a NaN among V: in every query that sees it
+        if (any_nan && (vs >> (8 * g) & 255u) == 255u) {   // a NaN among V: in every query that sees it
 #pragma unroll
           for (int c = 0; c < COLS; ++c) {
             const uint32_t nan = 0x7Fu << (8 * (c & 3)), clear = ~(0xFFu << (8 * (c & 3)));
@@ -506,14 +509,18 @@ __global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_ker
           *reinterpret_cast<uint4*>(smem + C::P + p_at<C::PITCH>(key, 2 * g + 1)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
         } else if constexpr (COLS == 8) {
           *reinterpret_cast<uint4*>(smem + C::P + p_at<C::PITCH>(key, g)) = make_uint4(w1[0], w1[1], w2[0], w2[1]);
-        } else {
+        } else if constexpr (COLS == 4) {
           *reinterpret_cast<uint2*>(smem + C::P + p_at<C::PITCH>(key, g >> 1) + (g & 1) * 8) = make_uint2(w1[0], w2[0]);
+        } else {
+          word[g] = w1[0] | w2[0] << 16;
         }
       }
+      if constexpr (COLS == 2)
+        *reinterpret_cast<uint4*>(smem + C::P + p_at<C::PITCH>(key, 0)) = make_uint4(word[0], word[1], word[2], word[3]);
       // the block's scales: 2^(V's reference + the block's power of two - the query's reference), 2^-5 for second terms
 #pragma unroll
-      for (int i = 0; i < N2 / 32; ++i) {
-        const int at = i * 32 + lane, g = at / COLS;
+      for (int i = 0; i < (N2 + 31) / 32; ++i) {
+        const int at = i * 32 + lane, g = at / COLS;   // (with two queries the upper lanes write places of no column)
         const float d = __shfl_sync(0xFFFFFFFFu, m_own - M_own, (HP == 2 ? (g >> 2) * COLS : 0) + at % COLS);
         uint32_t r = ref[0];
 #pragma unroll
@@ -621,7 +628,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinP
 }
 
 // ------------------------------------------------------------------ host
-int pick_cols(int64_t columns) { return columns <= 4 ? 4 : columns <= 8 ? 8 : 16; }
+int pick_cols(int64_t columns) { return columns <= 2 ? 2 : columns <= 4 ? 4 : columns <= 8 ? 8 : 16; }
 
 // From this many queries a key head on keys and values are decoded (oq_kv4_chunk.cu).
 constexpr int64_t CHUNK = 48;
@@ -634,7 +641,7 @@ int splits_of(int groups, int kv_heads, int B, int group, int max_q, int max_len
   if (columns >= CHUNK) return kv4_chunk_splits(kv_heads, B, group, max_q, tiles, sms);
   const int cols = pick_cols(columns);
   const int64_t ctas = (columns + cols - 1) / cols * groups * B;
-  const int64_t slots = (cols == 4 ? VC4 : 2) * (int64_t)sms;
+  const int64_t slots = (cols <= 4 ? 3 : 2) * (int64_t)sms;
   return (int)std::max<int64_t>(1, std::min<int64_t>({slots / std::max<int64_t>(ctas, 1), tiles / 2, 64}));
 }
 
@@ -657,6 +664,16 @@ oq_status launch(AttnParams& p, cudaStream_t st, int device) {
     return OQ_ERR_CUDA;
   }
   return OQ_OK;
+}
+
+template <int HP>
+oq_status launch_cols(AttnParams& p, int cols, cudaStream_t st, int device) {
+  switch (cols) {
+    case 2: return launch<2, HP>(p, st, device);
+    case 4: return launch<4, HP>(p, st, device);
+    case 8: return launch<8, HP>(p, st, device);
+    default: return launch<16, HP>(p, st, device);
+  }
 }
 
 }  // namespace
@@ -694,8 +711,7 @@ oq_status kv4_attention_launch(const AttentionArgs& a, void* stream) {
                   CU_TENSOR_MAP_SWIZZLE_128B, "the cache");
     if (r != OQ_OK) return r;
     const int cols = pick_cols((int64_t)a.max_q * p.group);
-    if (a.D == 128) r = cols == 4 ? launch<4, 1>(p, st, dev) : cols == 8 ? launch<8, 1>(p, st, dev) : launch<16, 1>(p, st, dev);
-    else r = cols == 4 ? launch<4, 2>(p, st, dev) : cols == 8 ? launch<8, 2>(p, st, dev) : launch<16, 2>(p, st, dev);
+    r = a.D == 128 ? launch_cols<1>(p, cols, st, dev) : launch_cols<2>(p, cols, st, dev);
   }
   if (r != OQ_OK || p.splits == 1) return r;
   JoinParams j;
