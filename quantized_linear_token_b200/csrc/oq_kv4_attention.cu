@@ -609,22 +609,44 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinP
     start = __reduce_max_sync(0xFFFFFFFFu, at);
   }
   if (start < 0 || t - start >= p.max_q) return;
+  // the parts' factors: lane s has parts s and 32 + s (64 at most)
+  float2 ml[2];
   float top = NONE;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_ml[s * p.rows + row].x);
-  float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[s * p.rows + row];
-    if (ml.y == 0.f) continue;   // it saw nothing
-    const float f = ex2(ml.x - top);
-    sum = fmaf(ml.y, f, sum);
-    const float* src = p.part_o + (s * p.rows + row) * p.D;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k * 32 < p.D) o[k] = fmaf(src[k * 32 + lane], f, o[k]);
+  for (int i = 0; i < 2; ++i) {
+    const int s = 32 * i + lane;
+    ml[i] = s < p.splits ? p.part_ml[s * p.rows + row] : make_float2(NONE, 0.f);
+    top = fmaxf(top, ml[i].x);
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k * 32 < p.D) p.y[row * p.D + k * 32 + lane] = __float2bfloat16_rn(sum == 0.f ? 0.f : o[k] / sum);
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  float f[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) f[i] = ml[i].y == 0.f ? 0.f : ex2(ml[i].x - top);   // (0: it saw nothing)
+  // sums in the parts' order; a lane has four (or two) channels, eight loads in flight
+  float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  const bool wide = p.D == 128;
+#pragma unroll 8
+  for (int s = 0; s < p.splits; ++s) {
+    const float l = __shfl_sync(0xFFFFFFFFu, s < 32 ? ml[0].y : ml[1].y, s & 31);
+    const float w = __shfl_sync(0xFFFFFFFFu, s < 32 ? f[0] : f[1], s & 31);
+    const float* src = p.part_o + (s * p.rows + row) * p.D;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (wide) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    } else {
+      const float2 u = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+      v[0] = u.x, v[1] = u.y;
+    }
+    sum = fmaf(l, w, sum);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = l == 0.f ? o[k] : fmaf(v[k], w, o[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = sum == 0.f ? 0.f : o[k] / sum;
+  if (wide) *reinterpret_cast<uint2*>(p.y + row * 128 + lane * 4) = make_uint2(mx_pack_bf16(o[0], o[1]), mx_pack_bf16(o[2], o[3]));
+  else *reinterpret_cast<uint32_t*>(p.y + row * 64 + lane * 2) = mx_pack_bf16(o[0], o[1]);
 }
 
 // ------------------------------------------------------------------ host
@@ -633,16 +655,25 @@ int pick_cols(int64_t columns) { return columns <= 2 ? 2 : columns <= 4 ? 4 : co
 // From this many queries a key head on keys and values are decoded (oq_kv4_chunk.cu).
 constexpr int64_t CHUNK = 48;
 
-// Parts of a cache: enough CTAs for two on every SM, each with two tiles at least.
+// Parts of a cache.  A CTA costs what seven tiles do besides its tiles (its chain of
+// first loads, the first reference, the epilogue: 8 us at three CTAs an SM), joining
+// parts about three; the number of parts with the shortest sum of rounds is taken.
+// Measured (us): one token over 32760 x 40 heads 11 parts (one round) 37.7, 22 46.0, 32
+// 53.7; 64 streams of 4096 to 8192 tokens x 8 heads 1 part 103.5, 3 91.5, 4 90.5.
 int splits_of(int groups, int kv_heads, int B, int group, int max_q, int max_len, int window, int sms) {
   const int64_t columns = (int64_t)max_q * group;
   const int64_t seen = window > 0 ? std::min<int64_t>(max_len, (int64_t)window + max_q) : max_len;
-  const int64_t tiles = (seen + KV_PAGE - 1) / KV_PAGE;
+  const int64_t tiles = std::max<int64_t>((seen + KV_PAGE - 1) / KV_PAGE, 1);
   if (columns >= CHUNK) return kv4_chunk_splits(kv_heads, B, group, max_q, tiles, sms);
   const int cols = pick_cols(columns);
-  const int64_t ctas = (columns + cols - 1) / cols * groups * B;
-  const int64_t slots = (cols <= 4 ? 3 : 2) * (int64_t)sms;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({slots / std::max<int64_t>(ctas, 1), tiles / 2, 64}));
+  const int64_t ctas = (columns + cols - 1) / cols * groups * B, slots = (cols <= 4 ? 3 : 2) * (int64_t)sms;
+  int best = 1;
+  int64_t least = 0;
+  for (int s = 1; s <= 64 && s <= tiles; ++s) {
+    const int64_t cost = (ctas * s + slots - 1) / slots * (7 + (tiles + s - 1) / s) + (s > 1 ? 3 : 0);
+    if (s == 1 || cost < least) best = s, least = cost;
+  }
+  return best;
 }
 
 size_t part_bytes(int splits, int64_t T, int heads, int D) {
@@ -679,10 +710,10 @@ oq_status launch_cols(AttnParams& p, int cols, cudaStream_t st, int device) {
 }  // namespace
 
 size_t kv4_attention_workspace(const oq_kv4* kv, int64_t T, int B, int max_q, int max_len) {
-  // the window only lowers the number of parts
+  // (a window only lowers the number of parts: the call takes no more than without one)
   int dev = 0;
-  return part_bytes(splits_of(kv->groups, kv->kv_heads, B, kv->heads / kv->kv_heads, max_q, max_len, 0, mx_sm_count(&dev)), T, kv->heads,
-                    kv->head_dim);
+  return part_bytes(splits_of(kv->groups, kv->kv_heads, B, kv->heads / kv->kv_heads, max_q, max_len, 0, mx_sm_count(&dev)), T,
+                    kv->heads, kv->head_dim);
 }
 
 oq_status kv4_attention_launch(const AttentionArgs& a, void* stream) {
@@ -692,7 +723,10 @@ oq_status kv4_attention_launch(const AttentionArgs& a, void* stream) {
   p.a = a;
   p.group = a.heads / a.kv_heads;
   int dev = 0;
-  p.splits = splits_of(a.kv.groups, a.kv_heads, a.kv.B, p.group, a.max_q, a.max_len, a.window, mx_sm_count(&dev));
+  const int sms = mx_sm_count(&dev);
+  p.splits = splits_of(a.kv.groups, a.kv_heads, a.kv.B, p.group, a.max_q, a.max_len, 0, sms);
+  if (a.window > 0)
+    p.splits = std::min(p.splits, splits_of(a.kv.groups, a.kv_heads, a.kv.B, p.group, a.max_q, a.max_len, a.window, sms));
   if (a.workspace_bytes < part_bytes(p.splits, a.T, a.heads, a.D)) {
     set_error("oq_kv4_attention: the workspace is too small");
     return OQ_ERR_INVALID_ARG;
