@@ -111,8 +111,9 @@ oq_status w4g_prepare_launch(const void* W, int dtype, int N, int K, int group, 
 
 // The sequence and the range of a call's tokens that this CTA's index `i` stands
 // for, when every sequence has as many units as its tokens' places in it touch
-// aligned windows of 32.  All threads of the CTA get the same answer; `shared`
+// aligned windows of W tokens.  All threads of the CTA get the same answer; `shared`
 // is three ints.  False: there are fewer units.
+template <int W>
 __device__ __forceinline__ bool kv_window(const KvView& kv, int64_t T, int i, int* shared, int& b, int& first, int& count,
                                           int& place) {
   if (threadIdx.x < 32) {
@@ -123,7 +124,7 @@ __device__ __forceinline__ bool kv_window(const KvView& kv, int64_t T, int i, in
       int units = 0;
       if (bb < kv.B) {
         const int n = kv.cu[bb + 1] - kv.cu[bb], p0 = kv.lens[bb] - n;
-        if (n > 0 && p0 >= 0) units = ((p0 + n - 1) >> 5) - (p0 >> 5) + 1;
+        if (n > 0 && p0 >= 0) units = (p0 + n - 1) / W - p0 / W + 1;
       }
       int sum = units;
 #pragma unroll
@@ -146,8 +147,8 @@ __device__ __forceinline__ bool kv_window(const KvView& kv, int64_t T, int i, in
   b = shared[0];
   if (b < 0) return false;
   const int c0 = kv.cu[b], n = kv.cu[b + 1] - c0, p0 = kv.lens[b] - n;
-  const int w0 = ((p0 >> 5) + shared[1]) << 5;       // the window's first place
-  const int lo = w0 > p0 ? w0 : p0, hi = w0 + 32 < p0 + n ? w0 + 32 : p0 + n;
+  const int w0 = (p0 / W + shared[1]) * W;           // the window's first place
+  const int lo = w0 > p0 ? w0 : p0, hi = w0 + W < p0 + n ? w0 + W : p0 + n;
   place = lo;
   first = c0 + (lo - p0);
   count = hi - lo;

@@ -329,9 +329,9 @@ oq_status launched(cudaError_t e, const char* what) {
 }
 
 // ------------------------------------------------------------------ append
-// A CTA of the cache's part takes one group of 128 channels of up to 32 tokens
-// whose places share an aligned window of 32, so that no byte of V (two tokens)
-// and no sector of its transposed rows is written by two CTAs.  Keys go the way
+// A CTA of the cache's part takes up to AWIN tokens whose places share an aligned
+// window, so that no word of V's transposed rows (eight tokens) is written by two
+// CTAs, and walks over groups of 128 channels.  Keys go the way
 // of the queries and are then quantised; values are quantised as they are and
 // transposed through shared memory.
 //
@@ -348,7 +348,7 @@ struct AppendParams {
   RopeGrid g;
   int kv_heads, parts;    // CTAs that share a window's groups of 128 channels
 };
-constexpr int ANT = 512;  // threads: 32 tokens of 16 lanes
+constexpr int AWIN = 16, ANT = AWIN * 16;   // tokens of a window, 16 lanes each
 
 __device__ __forceinline__ float round_odd(double w) {
   float f = __double2float_rz(w);
@@ -463,9 +463,10 @@ __device__ __forceinline__ uint32_t key_codes(const Vec8<T>& raw, const RopeArgs
 }
 
 template <typename T, bool INTER, int LANES>
-__global__ void __launch_bounds__(ANT, 1) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(ANT, 3) append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ int found[2];
-  __shared__ __align__(16) uint8_t tile[2][128 * 20];   // V codes: channel 8 s + j in row 16 j + s (no bank twice), 32 tokens
+  constexpr int TP = AWIN / 2 + 4;                     // (rows' distance: no bank twice)
+  __shared__ __align__(16) uint8_t tile[2][128 * TP];  // V codes, two tokens a byte: channel 8 s + j in row 16 j + s
   const RopeArgs& r = p.a.rope;
   const KvView& kv = p.a.kv;
   dependency_wait();
@@ -483,13 +484,13 @@ __global__ void __launch_bounds__(ANT, 1) append_kernel(const __grid_constant__ 
   }
   const int unit = ((int)blockIdx.x - p.g.ctas) / p.parts, part = ((int)blockIdx.x - p.g.ctas) % p.parts;
   int b, first, count, place;
-  if (!kv_window(kv, r.T, unit, found, b, first, count, place)) return;
+  if (!kv_window<AWIN>(kv, r.T, unit, found, b, first, count, place)) return;
   const int64_t page = kv.table[(int64_t)b * kv.width + (place >> 7)];
   if (page < 0 || page >= kv.pages) return;
   constexpr int D = LANES * 8;
   const int sub = (int)threadIdx.x & 15, ch = (sub & (LANES - 1)) * 8;   // 16 lanes hold a group's channels of a token
-  const int w0 = place & 127 & ~31;                                      // the window's first row in its page
-  const int row = (int)threadIdx.x >> 4, at = w0 + row, i = row - (place & 31);
+  const int w0 = place & 127 & ~(AWIN - 1);                              // the window's first row in its page
+  const int row = (int)threadIdx.x >> 4, at = w0 + row, i = row - (place & (AWIN - 1));
   const bool token = i >= 0 && i < count;
   const int64_t t = first + i;
   int hg = (int)((int64_t)kv.groups * part / p.parts);
@@ -538,15 +539,16 @@ __global__ void __launch_bounds__(ANT, 1) append_kernel(const __grid_constant__ 
     const uint32_t even_row = spread_nibbles(odd ? other >> 16 : vc[0]), odd_row = spread_nibbles(odd ? vc[0] >> 16 : other);
     const uint32_t pairs = even_row | odd_row << 4;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) tile[buf][((j + (odd ? 4 : 0)) * 16 + sub) * 20 + (row >> 1)] = (uint8_t)(pairs >> (8 * j));
+    for (int j = 0; j < 4; ++j) tile[buf][((j + (odd ? 4 : 0)) * 16 + sub) * TP + (row >> 1)] = (uint8_t)(pairs >> (8 * j));
     __syncthreads();   // (the other tile's readers are past the barrier before)
-    // four threads write a channel's 32 tokens; tokens that are not the call's keep their codes
+    // AWIN / 8 threads write a channel's tokens; tokens that are not the call's keep their codes
     {
-      const int c = (int)threadIdx.x >> 2, q = (int)threadIdx.x & 3;
-      uint32_t out = reinterpret_cast<const uint32_t*>(tile[buf] + ((c & 7) * 16 + (c >> 3)) * 20)[q];
-      uint32_t* dst = reinterpret_cast<uint32_t*>(base + (KV_V_ROW + c) * 64 + (w0 >> 5) * 16) + q;
-      if (count != 32) {
-        const int lo = min(max((place & 31) - 8 * q, 0), 8), hi = min(max((place & 31) + count - 8 * q, 0), 8);
+      constexpr int PER = AWIN / 8;
+      const int c = (int)threadIdx.x / PER, q = (int)threadIdx.x % PER;
+      uint32_t out = reinterpret_cast<const uint32_t*>(tile[buf] + ((c & 7) * 16 + (c >> 3)) * TP)[q];
+      uint32_t* dst = reinterpret_cast<uint32_t*>(base + (KV_V_ROW + c) * 64 + w0 / 2) + q;
+      if (count != AWIN) {
+        const int lo = min(max((place & (AWIN - 1)) - 8 * q, 0), 8), hi = min(max((place & (AWIN - 1)) + count - 8 * q, 0), 8);
         const uint32_t below_hi = hi == 8 ? 0xFFFFFFFFu : (1u << (4 * hi)) - 1u;
         const uint32_t below_lo = lo == 8 ? 0xFFFFFFFFu : (1u << (4 * lo)) - 1u;
         const uint32_t mask = below_hi & ~below_lo;   // nibbles [lo, hi) are new
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(NT) read_kernel(const __grid_constant__ ReadAr
   dependency_wait();
   const int unit = (int)blockIdx.x / kv.groups, hg = (int)blockIdx.x % kv.groups;
   int b, first, count, place;
-  if (!kv_window(kv, p.T, unit, found, b, first, count, place)) return;
+  if (!kv_window<32>(kv, p.T, unit, found, b, first, count, place)) return;
   const int64_t page = kv.table[(int64_t)b * kv.width + (place >> 7)];
   const bool ok = page >= 0 && page < kv.pages;   // a page that is not there reads as NaN
   const uint8_t* base = kv.cache + ((ok ? page : 0) * kv.groups + hg) * KV_GROUP_BYTES;
@@ -625,8 +627,8 @@ cudaError_t append_launch_lanes(const AppendParams& p, dim3 grid, cudaStream_t s
                           : mx_launch(append_kernel<T, INTER, 16>, grid, ANT, 0, 0, st, p);
 }
 
-// units of kv_window that B sequences with T tokens may have
-int64_t window_units(int64_t T, int B) { return std::min<int64_t>(T, T / 32 + 2 * (int64_t)B); }
+// units of kv_window<W> that B sequences with T tokens may have
+int64_t window_units(int64_t T, int B, int W) { return std::min<int64_t>(T, T / W + 2 * (int64_t)B); }
 
 }  // namespace
 
@@ -660,11 +662,11 @@ oq_status kv4_append_launch(const AppendArgs& a, void* stream) {
   p.a = a;
   p.kv_heads = a.rope.heads[1];
   const int D = a.rope.D;
-  const int64_t units = window_units(a.rope.T, a.kv.B);
+  const int64_t units = window_units(a.rope.T, a.kv.B, AWIN);
   const int sms = mx_sm_count(&dev);
   // a window's groups: in one CTA (what a token's table row costs is spent once)
-  // where there are windows for two CTAs an SM, else shared
-  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(a.kv.groups, 2 * (int64_t)sms / units));
+  // where there are windows for four CTAs an SM, else shared
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(a.kv.groups, 4 * (int64_t)sms / units));
   if (!rope_grid(a.rope.T, a.rope.heads[0], D, sms, ANT, &p.g) || p.g.ctas + units * p.parts > 0x7FFFFFFF)
     return OQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)(p.g.ctas + units * p.parts));
@@ -679,7 +681,7 @@ oq_status kv4_append_launch(const AppendArgs& a, void* stream) {
 
 oq_status kv4_read_launch(const ReadArgs& a, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t ctas = window_units(a.T, a.kv.B) * a.kv.groups;
+  const int64_t ctas = window_units(a.T, a.kv.B, 32) * a.kv.groups;
   if (ctas > 0x7FFFFFFF) return OQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)ctas);
   const cudaError_t e = a.dtype == OQ_DTYPE_BF16 ? mx_launch(read_kernel<__nv_bfloat16>, grid, NT, 0, 0, st, a)

@@ -153,11 +153,12 @@ def test_binding_refuses_host_tensors_and_bad_shapes(lib):
 
 
 def test_units_cover_every_window():
-    """The launch's bound on aligned windows of 32 holds for every place and count."""
-    for n in range(1, 200):
-        for p0 in range(32):
-            w = (p0 + n - 1) // 32 - p0 // 32 + 1
-            assert w <= n and w <= n // 32 + 2
+    """The launches' bound on aligned windows of 32 and 16 holds for every place and count."""
+    for size in (32, 16):
+        for n in range(1, 200):
+            for p0 in range(size):
+                w = (p0 + n - 1) // size - p0 // size + 1
+                assert w <= n and w <= n // size + 2
 
 
 def test_query_terms_are_exact():
