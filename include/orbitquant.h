@@ -610,11 +610,13 @@ oq_status oq_qk_norm_rope(const void* q, int64_t q_stride, int32_t q_heads, cons
  *   y         device bf16 [T, heads, head_dim].  A token that sees nothing gets 0.
  *   workspace device scratch of oq_kv4_attention_workspace_size bytes (may be 0),
  *             256-byte aligned; calls that share it must not overlap.
- * Queries enter exactly, softmax and sums are fp32, the weights are rounded to 8
- * bits like bf16's (relative to the largest of 32 neighbouring tokens).  |V| from
- * 2^-90 to 2^90, or 0.  A NaN in a key or value reaches the queries that see it.
- * Results repeat bit for bit.  A bounded wait that runs out is reported by
- * oq_kv4_poll_error.
+ * Queries enter exactly, softmax and sums are fp32.  Weights are rounded to 8 bits,
+ * as bf16's are; with fewer than 48 queries a key head (max_q heads / kv_heads) also
+ * by up to 2^-16 of the largest weight times the largest |V| of 32 neighbouring
+ * tokens in 32 channels.  |V| from 2^-90 to 2^90, or 0.  A NaN in a key or value
+ * reaches the queries that see it (in values: their block of 32 channels), an
+ * infinite or NaN query its own row.  Results repeat bit for bit.  A bounded wait
+ * that runs out is reported by oq_kv4_poll_error.
  */
 typedef struct oq_kv4 oq_kv4;
 enum { OQ_ATTN_CAUSAL = 1 };

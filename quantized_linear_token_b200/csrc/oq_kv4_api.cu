@@ -344,7 +344,7 @@ oq_status oq_kv4_attention(const oq_kv4* kv, const void* q, int64_t q_stride, in
   a.D = kv->head_dim;
   a.max_q = max_q;
   a.max_len = max_len;
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 0;   // (a cache has fewer tokens: everything is within it)
   a.causal = (flags & OQ_ATTN_CAUSAL) != 0;
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;

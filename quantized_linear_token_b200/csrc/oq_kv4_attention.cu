@@ -54,7 +54,7 @@ struct Cfg {
   static constexpr int SF_K = 0, SF_Q = 8, SF_ONE = 16, SF_P = 20, SF = 24;
   static constexpr int SB = N2 + 2 * N1 + SF <= 256 ? 2 : 1; // S buffers
   static constexpr uint32_t TMEM = N2 + SB * N1 + SF <= 128 ? 128 : 256;
-  static_assert(N2 + SB * N1 + SF <= 256 && N2 <= 128 && HC <= 32, "tensor memory: two CTAs an SM");
+  static_assert(N2 + SB * N1 + SF <= TMEM && CTAS * TMEM <= 512 && N2 <= 128 && HC <= 32, "tensor memory of an SM's CTAs");
   static constexpr int PITCH = N2 < 32 ? 32 : N2;            // bytes of a token in P: a swizzle's row
   static constexpr int P = UNITS * UNIT, Q = P + 128 * PITCH, KS = Q + N1 * 128, SFQ = KS + UNITS * 512;
   static constexpr int SFP = SFQ + HP * 512;
@@ -653,7 +653,10 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinP
 int pick_cols(int64_t columns) { return columns <= 2 ? 2 : columns <= 4 ? 4 : columns <= 8 ? 8 : 16; }
 
 // From this many queries a key head on keys and values are decoded (oq_kv4_chunk.cu).
-constexpr int64_t CHUNK = 48;
+#ifndef CHUNKV
+#define CHUNKV 48
+#endif
+constexpr int64_t CHUNK = CHUNKV;
 
 // Parts of a cache.  A CTA costs what seven tiles do besides its tiles (its chain of
 // first loads, the first reference, the epilogue: 8 us at three CTAs an SM), joining
