@@ -24,6 +24,12 @@
 // Long caches are split over CTAs; a second kernel joins the parts in a fixed
 // order, so results repeat bit for bit.
 //
+// Bound: a tile's chain of load, first product, softmax, second product, which the CTAs
+// of an SM overlap.  Measured, one token over 32760 x 40 heads of 128: 38 us for 178 MB
+// (27 us at the copy's rate); the loads alone took 33, the MMAs alone 34, the softmax
+// alone 34.  64 streams of 4096 to 8192 tokens x 8 heads with 4 queries each: 91 us
+// for 64; alone 74, 81, 79.
+//
 // Warps: 0-3 softmax and epilogue, 4 TMA producer, 5 tensor memory and MMAs.
 #include <cuda_bf16.h>
 
@@ -653,10 +659,11 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinP
 int pick_cols(int64_t columns) { return columns <= 2 ? 2 : columns <= 4 ? 4 : columns <= 8 ? 8 : 16; }
 
 // From this many queries a key head on keys and values are decoded (oq_kv4_chunk.cu).
-#ifndef CHUNKV
-#define CHUNKV 48
-#endif
-constexpr int64_t CHUNK = CHUNKV;
+// Measured (us), this form and that one at 32, 48 and 64 queries: one sequence of 8192 x 40
+// heads 52 and 76, 67 and 77, 92 and 78; 8 of 4096 x 8 heads 40 and 61, 63 and 61, 63 and
+// 61; 16 of 2048 x 8 heads 37 and 56, 64 and 56, 71 and 57; 32 of 300 x 8 heads 30 and 40,
+// 44 and 40, 58 and 41; 4 of 4096 x 16 heads of 64 channels 50 and 43, 61 and 43, 75 and 43.
+constexpr int64_t CHUNK = 48;
 
 // Parts of a cache.  A CTA costs what seven tiles do besides its tiles (its chain of
 // first loads, the first reference, the epilogue: 8 us at three CTAs an SM), joining

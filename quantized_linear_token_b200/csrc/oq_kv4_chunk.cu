@@ -16,6 +16,11 @@
 // keys) and tokens (of values) lie permuted within each eight, and q's channels and
 // P's tokens are taken in the same order.
 //
+// Bound: issue slots, those of the softmax (an exponential and about four instructions
+// a score) with those of the decoding.  Measured, 1560 queries over 7800 tokens x 40 heads
+// of 128: 388 us, 640 TFLOP/s (154 us at the rate of a large library product).  Four
+// decoding warps and two passes over S took 448.
+//
 // Warps: 0-3 and 4-7 the two query tiles, 8-15 decoding, 16 tensor memory and MMAs
 // (17-19 only give up registers).
 #include <cuda_bf16.h>

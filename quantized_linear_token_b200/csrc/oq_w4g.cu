@@ -13,6 +13,13 @@
 // bits, exact), one MMA column each.  K is split over the CTAs of a cluster, so
 // that small CTAs fill all SMs evenly; warps' and CTAs' sums are added in a fixed
 // order through shared memory.
+//
+// Bound: issue slots of the decoding and the MMAs, at 12 to 24 warps an SM, and the
+// launch.  Measured, bf16 tokens: one token x 13824 inputs x 5120 outputs, groups of 128,
+// 14 us (the bytes alone 5.6); 13 tokens x 5120 x 13824, groups of 32 with zeros, 23.5 us
+// (6.5).  A form on the tensor cores that read shared memory (codes as e4m3 subnormals,
+// tokens in two e4m3 terms, 128 rows a CTA) took 19.5 and 52: tiles of 128 rows read 128
+// bytes of a row at a time, and each group's accumulators pass through tensor memory.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -105,12 +112,14 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 
 template <int NT, int MT>
 struct Cfg {
-  // Warps of a CTA, which split K, CTAs an SM and stages of a ring.  Measured (us):
-  // one token 13824 -> 5120, 8 warps and 3 CTAs 14.0, 4 CTAs 17.4, 4 warps and 8 CTAs
-  // 14.9 to 18.1; 13 tokens 5120 -> 13824, 4 warps, 4 CTAs and 6 stages 26.5, 4 stages
-  // 29.3, 8 warps and 2 CTAs 30.8.
-  static constexpr int NWARP = NT == 1 ? 8 : 4, MIN_CTAS = NT == 1 ? 3 : NT == 2 ? 4 : 2;
-  static constexpr int STAGE = MT * 1024, STAGES = NT == 1 ? 4 : 6;   // MT tiles of 16 rows x 64 bytes
+  // Warps of a CTA, which split K, CTAs an SM and stages of a ring; what the rings leave
+  // of an SM's shared memory decides how many runs' tokens are brought in at once.
+  // Measured (us): one token 13824 -> 5120, 8 warps and 3 CTAs 14.0, 4 CTAs 17.4, 4 warps
+  // and 8 CTAs 14.9 to 18.1; 13 tokens 5120 -> 13824, 4 warps, 3 CTAs and 4 stages 23.5,
+  // 2 stages 23.7, 6 stages 27.6, 5 or 3 (the remainders cost more) 28.4, 8 warps and 2
+  // CTAs 27.8 to 31; 32 tokens, 3 CTAs and 4 stages 38.4, 2 CTAs 41.6, with 6 stages 60.
+  static constexpr int NWARP = NT == 1 ? 8 : 4, MIN_CTAS = 3;
+  static constexpr int STAGE = MT * 1024, STAGES = 4;           // MT tiles of 16 rows x 64 bytes
   static constexpr int RING = NWARP * STAGES * STAGE;
   static constexpr int PART = NWARP * MT * NT * 512;            // the warps' sums, in the ring's place
   static constexpr int BYTES = RING > PART ? RING : PART;
@@ -406,6 +415,7 @@ cudaError_t launch_tiles(W4gParams& p, cudaStream_t st) {
   p.per_cta = p.a.T * TERMS <= 32 ? (int)p.a.T : 32 / TERMS;
   int dev = 0;
   // several column tiles: 32 weight rows a CTA share what is loaded of the tokens, where they still fill the SMs
+  // (13 tokens 5120 -> 13824 23.5 us, with 16 rows 29.0; 13824 -> 5120 32.6, 35.4)
   const bool two = p.a.N >= 32 * mx_sm_count(&dev);
   if (columns <= 8) return launch_one<X, GROUP, ZEROS, 1, 1>(p, st);
   if (columns <= 16) return two ? launch_one<X, GROUP, ZEROS, 2, 2>(p, st) : launch_one<X, GROUP, ZEROS, 2, 1>(p, st);
