@@ -110,16 +110,16 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
-template <int NT, int MT>
+// NW warps, which split K
+template <int NT, int MT, int NW>
 struct Cfg {
-  // Warps of a CTA, which split K, CTAs an SM and stages of a ring; what the rings leave
-  // of an SM's shared memory decides how many runs' tokens are brought in at once.
-  // Measured (us): one token 13824 -> 5120, 8 warps and 3 CTAs 14.0, 4 CTAs 17.4, 4 warps
-  // and 8 CTAs 14.9 to 18.1; 13 tokens 5120 -> 13824, 4 warps, 3 CTAs and 4 stages 23.5,
-  // 2 stages 23.7, 6 stages 27.6, 5 or 3 (the remainders cost more) 28.4, 8 warps and 2
-  // CTAs 27.8 to 31; 32 tokens, 3 CTAs and 4 stages 38.4, 2 CTAs 41.6, with 6 stages 60.
-  static constexpr int NWARP = NT == 1 ? 8 : 4, MIN_CTAS = 3;
-  static constexpr int STAGE = MT * 1024, STAGES = 4;           // MT tiles of 16 rows x 64 bytes
+  // CTAs an SM and stages of a warp's ring; what the rings leave of an SM's shared memory
+  // decides how many runs' tokens are brought in at once.  Measured (us): 13 tokens
+  // 5120 -> 13824, 4 warps, 3 CTAs and 4 stages 23.5, 2 stages 23.7, 6 stages 27.6, 5 or 3
+  // (the remainders cost more) 28.4, 8 warps and 2 CTAs 27.8 to 31; 32 tokens, 3 CTAs and
+  // 4 stages 38.4, 2 CTAs 41.6, with 6 stages 60.
+  static constexpr int NWARP = NW, MIN_CTAS = NT == 1 && NW == 4 ? 5 : 3;
+  static constexpr int STAGE = MT * 1024, STAGES = NT == 1 && MT == 2 ? 2 : 4;   // MT tiles of 16 rows x 64 bytes
   static constexpr int RING = NWARP * STAGES * STAGE;
   static constexpr int PART = NWARP * MT * NT * 512;            // the warps' sums, in the ring's place
   static constexpr int BYTES = RING > PART ? RING : PART;
@@ -129,9 +129,9 @@ struct Cfg {
 __host__ __device__ inline int x_pitch(int chunk, int size) { return chunk * RUN * size + 64; }
 
 // MT tiles of 16 weight rows a CTA, NT tiles of 8 MMA columns.
-template <typename X, int GROUP, bool ZEROS, int NT, int MT>
-__global__ void __launch_bounds__(Cfg<NT, MT>::NWARP * 32, Cfg<NT, MT>::MIN_CTAS) w4g_kernel(const __grid_constant__ W4gParams p) {
-  using C = Cfg<NT, MT>;
+template <typename X, int GROUP, bool ZEROS, int NT, int MT, int NW>
+__global__ void __launch_bounds__(Cfg<NT, MT, NW>::NWARP * 32, Cfg<NT, MT, NW>::MIN_CTAS) w4g_kernel(const __grid_constant__ W4gParams p) {
+  using C = Cfg<NT, MT, NW>;
   constexpr int TERMS = sizeof(X) == 2 ? 1 : 3, SUB = RUN / GROUP;   // groups in a run
   constexpr int NWARP = C::NWARP, TILE = ROWS * MT, NTHR = NWARP * 32;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -383,9 +383,9 @@ oq_status launched(cudaError_t e, const char* what) {
   return OQ_ERR_CUDA;
 }
 
-template <typename X, int GROUP, bool ZEROS, int NT, int MT>
+template <typename X, int GROUP, bool ZEROS, int NT, int MT, int NW>
 cudaError_t launch_one(W4gParams& p, cudaStream_t st) {
-  using C = Cfg<NT, MT>;
+  using C = Cfg<NT, MT, NW>;
   constexpr int NWARP = C::NWARP;
   int dev = 0;
   const int sms = mx_sm_count(&dev);
@@ -402,9 +402,9 @@ cudaError_t launch_one(W4gParams& p, cudaStream_t st) {
   const size_t smem = (size_t)C::BYTES + (size_t)p.per_cta * x_pitch(p.chunk, (int)sizeof(X)) +
                       (size_t)p.chunk * (RUN / GROUP) * ROWS * MT * (ZEROS ? 3 : 2);
   static std::atomic<uint64_t> smem_set{0};
-  if (mx_allow_smem(reinterpret_cast<const void*>(w4g_kernel<X, GROUP, ZEROS, NT, MT>), 227 * 1024, dev, &smem_set) != OQ_OK)
+  if (mx_allow_smem(reinterpret_cast<const void*>(w4g_kernel<X, GROUP, ZEROS, NT, MT, NW>), 227 * 1024, dev, &smem_set) != OQ_OK)
     return cudaErrorInvalidConfiguration;
-  return mx_launch(w4g_kernel<X, GROUP, ZEROS, NT, MT>, dim3((unsigned)(tiles * p.split), (unsigned)blocks), NWARP * 32, smem,
+  return mx_launch(w4g_kernel<X, GROUP, ZEROS, NT, MT, NW>, dim3((unsigned)(tiles * p.split), (unsigned)blocks), NWARP * 32, smem,
                    p.split, st, p);
 }
 template <typename X, int GROUP, bool ZEROS>
@@ -414,12 +414,24 @@ cudaError_t launch_tiles(W4gParams& p, cudaStream_t st) {
   const int columns = (int)std::min<int64_t>(p.a.T * TERMS, 32);
   p.per_cta = p.a.T * TERMS <= 32 ? (int)p.a.T : 32 / TERMS;
   int dev = 0;
-  // several column tiles: 32 weight rows a CTA share what is loaded of the tokens, where they still fill the SMs
-  // (13 tokens 5120 -> 13824 23.5 us, with 16 rows 29.0; 13824 -> 5120 32.6, 35.4)
-  const bool two = p.a.N >= 32 * mx_sm_count(&dev);
-  if (columns <= 8) return launch_one<X, GROUP, ZEROS, 1, 1>(p, st);
-  if (columns <= 16) return two ? launch_one<X, GROUP, ZEROS, 2, 2>(p, st) : launch_one<X, GROUP, ZEROS, 2, 1>(p, st);
-  return two ? launch_one<X, GROUP, ZEROS, 4, 2>(p, st) : launch_one<X, GROUP, ZEROS, 4, 1>(p, st);
+  const int sms = mx_sm_count(&dev);
+  // Up to eight columns.  Where CTAs of 16 rows need more than one round, 32 rows and 8 warps:
+  // one token 5120 -> 13824, groups of 128, 10.7 us, with 16 rows 13.4, eight tokens, groups
+  // of 64, 15.3 and 18.6; 8192 -> 28672 31.8 and 33.3, 45.0 and 51.4.  Otherwise 16 rows,
+  // whose CTAs read a row to its end: 4096 -> 6144 6.6 us and 7.1, 8.7 and 11.0; but long rows
+  // are split, over CTAs of 32 rows and 4 warps: 13824 -> 5120 13.3 and, with 16 rows, 14.0,
+  // 18.9 and 21.9; 4096 -> 4096 6.1 and 5.9, 9.9 and 7.7.
+  if (columns <= 8) {
+    const int64_t ctas = (p.a.N + ROWS - 1) / ROWS * ((p.a.T + p.per_cta - 1) / p.per_cta);
+    if (ctas > Cfg<1, 1, 8>::MIN_CTAS * (int64_t)sms) return launch_one<X, GROUP, ZEROS, 1, 2, 8>(p, st);
+    if (2 * ctas > Cfg<1, 1, 8>::MIN_CTAS * (int64_t)sms && p.a.K >= 64 * RUN) return launch_one<X, GROUP, ZEROS, 1, 2, 4>(p, st);
+    return launch_one<X, GROUP, ZEROS, 1, 1, 8>(p, st);
+  }
+  // more: 32 weight rows a CTA share what is loaded of the tokens, where they still fill the
+  // SMs (13 tokens 5120 -> 13824 23.5 us, with 16 rows 29.0; 13824 -> 5120 32.6, 35.4)
+  const bool two = p.a.N >= 32 * sms;
+  if (columns <= 16) return two ? launch_one<X, GROUP, ZEROS, 2, 2, 4>(p, st) : launch_one<X, GROUP, ZEROS, 2, 1, 4>(p, st);
+  return two ? launch_one<X, GROUP, ZEROS, 4, 2, 4>(p, st) : launch_one<X, GROUP, ZEROS, 4, 1, 4>(p, st);
 }
 template <typename X, int GROUP>
 cudaError_t launch_zeros(W4gParams& p, cudaStream_t st) {

@@ -640,6 +640,19 @@ def test_w4g_linear(env, x_dtype, y_dtype, T, N, d, group, zeros):
     assert torch.equal(y, B.oq_linear_w4g(x, c, s, z, group=group, y_dtype=_dt(torch, y_dtype)))
 
 
+@pytest.mark.parametrize("x_dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,N,d,group,zeros", [
+    (1, 7301, 160, 32, True), (8, 7500, 1088, 64, False), (2, 14400, 384, 128, True),    # rows in more than one round of CTAs
+    (1, 3601, 8320, 64, True), (7, 4000, 8224, 32, False), (2, 3700, 9216, 128, True),   # long rows, split
+    (13, 4801, 416, 32, True), (16, 4736, 2176, 64, False), (31, 4750, 672, 32, True)])  # 32 rows a CTA
+def test_w4g_linear_many_rows(env, x_dtype, T, N, d, group, zeros):
+    torch, B = env
+    rng = np.random.default_rng(T * N + d)
+    c, s, z = B.oq_w4g_prepare(torch.from_numpy(_weights(rng, N, d)).cuda(), group, zeros=zeros)
+    x = torch.from_numpy((rng.standard_normal((T, d)) * np.exp(rng.standard_normal((T, d)))).astype(np.float32)).cuda()
+    _check_w4g(torch, B, x.to(_dt(torch, x_dtype)), c, s, z, d, group, torch.float32)
+
+
 def test_w4g_linear_exact_and_special(env):
     """fp32 tokens enter exactly; infinities and NaN go where the formula says."""
     torch, B = env
