@@ -16,7 +16,7 @@
 //
 // Bound: issue slots of the decoding and the MMAs, at 12 to 24 warps an SM, and the
 // launch.  Measured, bf16 tokens: one token x 13824 inputs x 5120 outputs, groups of 128,
-// 14 us (the bytes alone 5.6); 13 tokens x 5120 x 13824, groups of 32 with zeros, 23.5 us
+// 13.3 us (the bytes alone 5.6); 13 tokens x 5120 x 13824, groups of 32 with zeros, 23.5 us
 // (6.5).  A form on the tensor cores that read shared memory (codes as e4m3 subnormals,
 // tokens in two e4m3 terms, 128 rows a CTA) took 19.5 and 52: tiles of 128 rows read 128
 // bytes of a row at a time, and each group's accumulators pass through tensor memory.
