@@ -109,7 +109,7 @@ oq_status check_cache(const char* who, const oq_kv4* kv, const void* cache, int6
   if (!cache || !aligned(cache, 32)) return invalid(who, "the cache must be a 32-byte aligned pointer");
   if ((!table && B * (int64_t)width > 0) || (B > 0 && (!cu || !lens)) || !aligned(table, 4) || !aligned(cu, 4) || !aligned(lens, 4))
     return invalid(who, "page_table, cu and lens must be 4-byte aligned pointers");
-  if (pages == 0 || pages * kv->groups > 0x7FFFFFFF / KV_ROWS)
+  if (pages == 0 || pages > 0x7FFFFFFF / KV_ROWS / kv->groups)
     return unsupported(who, "the cache must have a page and at most 2^31 / 272 groups of 128 channels in its pages");
   if (width > 0x7FFFFFFF / KV_PAGE || B > 65535) return unsupported(who, "table_width or B too large");
   int dev = -1;
@@ -232,7 +232,7 @@ oq_status oq_kv4_poll_error(const oq_kv4* kv) {
 }
 
 size_t oq_kv4_cache_size(const oq_kv4* kv, int64_t pages) {
-  if (!kv || pages <= 0 || pages * kv->groups > 0x7FFFFFFF / KV_ROWS) return 0;
+  if (!kv || pages <= 0 || pages > 0x7FFFFFFF / KV_ROWS / kv->groups) return 0;
   return (size_t)pages * kv->groups * KV_GROUP_BYTES;
 }
 
@@ -323,7 +323,7 @@ oq_status oq_kv4_attention(const oq_kv4* kv, const void* q, int64_t q_stride, in
   if (!(scale > 0.f) || std::isinf(scale)) return invalid(who, "scale must be positive and finite");
   if (flags & ~OQ_ATTN_CAUSAL) return invalid(who, "unknown flags");
   const int group = kv->heads / kv->kv_heads;
-  if (T * kv->heads > 0x7FFFFFFF || (int64_t)max_q * group > 0x7FFFFFFF - 64 || kv->kv_heads > 1023)
+  if (T > 0x7FFFFFFF / kv->heads || (int64_t)max_q * group > 0x7FFFFFFF - 64 || kv->kv_heads > 1023)
     return unsupported(who, "at most 2^31 rows of queries per call and 1023 key heads");
   if (T == 0 || B == 0 || max_q == 0) return OQ_OK;
   if ((st = check_heads(who, "q", q, kv->heads, kv->head_dim, q_stride, T, OQ_DTYPE_BF16)) != OQ_OK) return st;

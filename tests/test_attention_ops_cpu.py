@@ -50,6 +50,14 @@ def test_cache_size(lib, kv):
     assert lib.oq_kv4_cache_size(None, 3) == 0
 
 
+@pytest.mark.parametrize("n", [1 << 60, 1 << 61, 1 << 62, (1 << 62) + 3])
+def test_counts_whose_products_leave_64_bits(lib, kv, n):
+    h = ctypes.byref(kv)
+    assert lib.oq_kv4_cache_size(h, n) == 0
+    assert lib.oq_kv4_read(h, 64 * P, n, 5 * P, 4, 6 * P, 7 * P, 2, 3, P, 2 * P, 0, None) == 2
+    assert lib.oq_kv4_attention(h, P, 1024, n, 64 * P, 8, 5 * P, 4, 6 * P, 7 * P, 2, 2, 300, 0.1, 1, 0, 2 * P, None, 0, None) == 2
+
+
 def test_norm_rope_refusals(lib):
     def f(q=P, qs=512, qh=4, k=2 * P, ks=256, kh=2, dt=1, T=3, D=128, gq=4 * P, gk=4 * P, gdt=0, eps=1e-6, table=5 * P, rows=9,
           rot=128, pos=6 * P, flags=0, qo=7 * P, qos=512, ko=8 * P, kos=256):
