@@ -425,13 +425,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
         most = fmaxf(top[0], top[1]);
       };
       bool move = M == NONE && max(lo_j, 0) < min(hi_j, KV_PAGE);   // the first token it sees
+      // Weights are formed twice at most: what they are relative to a reference that has
+      // moved is taken as it is.  (The new reference comes from top * sl2 rounded, a weight
+      // from s * sl2 - M rounded once: at M + 8 one may see 2^8 exceeded and the other not,
+      // so that asking again could go on for ever.)
+      bool moved = false;
       while (ok) {
-        if (!__any_sync(0xFFFFFFFFu, move)) {
+        if (moved || !__any_sync(0xFFFFFFFFu, move)) {
           weigh();
           move = most > 256.f;   // 2^LAZY
-          if (!__any_sync(0xFFFFFFFFu, move)) break;
+          if (moved || !__any_sync(0xFFFFFFFFu, move)) break;
         }
-        move = false;
+        moved = true;
         // the reference moves, and with it what is summed so far
         float top = -INFINITY;
 #pragma unroll 1

@@ -1,0 +1,46 @@
+"""CPU restatement of how the attention kernels move the softmax reference: at which scores, how often, and what the
+weights become."""
+
+import numpy as np
+import pytest
+
+import softmax_emulation as S
+
+F = np.float32
+MANY = 50          # passes after which a rule counts as one that does not end
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_at_the_border_of_a_move_end(D):
+    """Scores that round to M + 8 and exceed it by less than a rounding, for every M from 8 to 400."""
+    c2 = S.log2e(D ** -0.5)
+    found = stuck = 0
+    for m in range(8, 401):
+        s = S.border_score(m, c2)
+        if s is None:
+            continue
+        found += 1
+        tile = np.array([s, F(0), F(1)], F)
+        stuck += S.chunk_tile(tile, c2, F(m), MANY)[2] == MANY      # asking until no weight exceeds 2^8
+        w, M, made = S.chunk_tile(tile, c2, F(m))
+        assert made <= 2 and M == m and 256 < w.max() < 256.1
+    assert found > 100 and stuck == found
+
+
+def test_large_scores_end():
+    """Normal scores times 1 to 10^10, several tiles."""
+    rng = np.random.default_rng(0)
+    c2 = S.log2e(128 ** -0.5)
+    stuck = 0
+    for e in range(11):
+        for _ in range(40):
+            M = old = S.NONE
+            for _ in range(8):
+                s = (rng.standard_normal(16) * 10.0 ** e).astype(F)
+                if old is not None:
+                    w, old, made = S.chunk_tile(s, c2, old, MANY)
+                    if made == MANY:
+                        stuck, old = stuck + 1, None
+                w, M, made = S.chunk_tile(s, c2, M)
+                assert made <= 2 and not np.isnan(w).any()
+    assert stuck > 10
