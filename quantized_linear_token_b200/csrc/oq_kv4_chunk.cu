@@ -40,6 +40,7 @@ constexpr int DEC_WARP = 8, MMA_WARP = 16, NTHREADS = 20 * 32, DEC_THREADS = 256
 constexpr int SOFTMAX_REGS = 136, DECODE_REGS = 80, MMA_REGS = 48;
 static_assert(2 * SOFTMAX_REGS + 2 * DECODE_REGS + MMA_REGS == 5 * 96, "more would wait for good");
 constexpr float LAZY = 8.f, NONE = -1e30f;    // as in oq_kv4_attention.cu
+constexpr float FAR = 4194304.f;              // 2^22: the last bit of a reference is half a unit of log2
 
 template <int D>
 struct Cfg {
@@ -398,7 +399,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
       float most = 0.f, part_sum = 0.f;
       auto weigh = [&]() {
         f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-        const f32x2 c2 = pack2(sl2, sl2), m2 = pack2(-M, -M);
+        // From references of FAR on the product s * sl2 is rounded by itself, as the reference
+        // was: in one step with the difference its error of half the reference's last bit
+        // would be the exponent (weights of 2^128 and 0 from 2^31 on).
+        const bool far = __any_sync(0xFFFFFFFFu, fabsf(M) > FAR && M != NONE);
+        const float factor = far ? 1.f : sl2;
+        const f32x2 c2 = pack2(factor, factor), m2 = pack2(-M, -M);
         float top[2] = {0.f, 0.f};
         uint32_t v[2][16];
         tmem_ld16(t_s, v[0]);
@@ -407,6 +413,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
           tmem_wait_ld();
           if (c < 7) tmem_ld16(t_s + 16 * (c + 1), v[(c + 1) & 1]);
           hide(v[c & 1], c);
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[c & 1][i] = __float_as_uint(__uint_as_float(v[c & 1][i]) * sl2);
+          }
 #pragma unroll
           for (int g = 0; g < 2; ++g)   // tokens j, j + 4 of eight side by side
 #pragma unroll

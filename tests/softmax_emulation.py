@@ -38,18 +38,22 @@ def border_score(m, c2):
     return None
 
 
-def weights(s, c2, M):
+FAR = F(2 ** 22)
+
+
+def weights(s, c2, M, far=True):
     with np.errstate(over="ignore"):
-        return np.exp2(fma(s, c2, -M).astype(np.float64)).astype(F)
+        x = F(F(s * c2) - M) if far and abs(M) > FAR and M != NONE else fma(s, c2, -M)
+        return np.exp2(x.astype(np.float64)).astype(F)
 
 
-def chunk_tile(s, c2, M, passes=2):
+def chunk_tile(s, c2, M, passes=2, far=True):
     """A tile's scores of one query relative to the reference M -> (weights, M, passes made).  `passes`: after so many
-    the weights are taken as they are."""
+    the weights are taken as they are; `far`: whether products are rounded by themselves from FAR on."""
     move, made = M == NONE, 0
     while True:
         if made == passes - 1 or not move:
-            w = weights(s, c2, M)
+            w = weights(s, c2, M, far)
             move = w.max() > 256
             if made == passes - 1 or not move:
                 return w, M, made + 1

@@ -44,3 +44,44 @@ def test_scores_at_the_border_of_a_move(env, D):
         s.np_cu = np.array([0, r], np.int32)
         s.cu.copy_(torch.from_numpy(s.np_cu))
         _check_attention(torch, B, kv, s, q[:r].contiguous(), causal=False)
+
+
+FAR = [2.0 ** 20, 2.0 ** 25, 2.0 ** 28 * 1.37, 2.0 ** 31 * 1.11, 2.0 ** 34 * 1.73, 2.0 ** 60 * 1.01, 2.0 ** 95 * 1.9]
+
+
+def _far(env, D, n, far):
+    """Keys of one channel times queries of magnitude `far`, each query its own: the tokens with the largest score share
+    the weight and all others have none; a query that sees one token gives its value.  Weights that are equal are rounded
+    alike, to 8 bits; the result is rounded to bf16; sums of few terms."""
+    torch, B = env
+    rng = np.random.default_rng(41)
+    kv = B.oq_kv4_create(1, 1, D)
+    s = Streams(torch, rng, kv, [n], [400])
+    q = np.zeros((n, 1, D))
+    q[:, 0, 7] = far * rng.uniform(1, 2, n) * rng.choice([-1, 1], n)
+    q = torch.from_numpy(q.astype(np.float32)).cuda().bfloat16()
+
+    def values(key):
+        for j in range(400):
+            k = np.zeros(D)
+            k[7] = key(j)
+            A.write_token(s.np_cache, s.pages[0, j // 128], j % 128, k, rng.standard_normal(D))
+        s.cache.copy_(torch.from_numpy(s.np_cache))
+        V = A.cache_values(s.np_cache)[1]
+        return np.stack([V[s.pages[0, j // 128], 0, j % 128, :D] for j in range(400)])
+
+    def check(y, want, V):
+        assert (np.abs(_np(y)[:, 0] - want) <= 2 * 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * np.abs(V).max()).all()
+
+    V = values(lambda j: {3: 1, 140: 1, 141: 0.5, 300: 1, 350: -1}.get(j, 0))
+    up = _np(q)[:, 0, 7:8] > 0
+    check(B.oq_kv4_attention(kv, q, *s.view, n, causal=False), np.where(up, (V[3] + V[140] + V[300]) / 3, V[350]), V)
+    V = values(lambda j: 1 - j % 2 * 0.5)
+    check(B.oq_kv4_attention(kv, q, *s.view, n, window=1), V[400 - n:], V)
+    B.oq_kv4_poll_error(kv)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", FAR)
+def test_far_scores_of_chunks(env, D, far):
+    _far(env, D, 60, far)

@@ -38,9 +38,28 @@ def test_large_scores_end():
             for _ in range(8):
                 s = (rng.standard_normal(16) * 10.0 ** e).astype(F)
                 if old is not None:
-                    w, old, made = S.chunk_tile(s, c2, old, MANY)
+                    w, old, made = S.chunk_tile(s, c2, old, MANY, far=False)
                     if made == MANY:
                         stuck, old = stuck + 1, None
                 w, M, made = S.chunk_tile(s, c2, M)
                 assert made <= 2 and not np.isnan(w).any()
     assert stuck > 10
+
+
+def test_weights_of_far_scores():
+    """From 2^22 on: no weight above 2^8, the largest score's not below 1 / 2, whatever the scores' magnitude."""
+    rng = np.random.default_rng(1)
+    c2 = S.log2e(128 ** -0.5)
+    wrong = 0
+    for e in range(4, 38):
+        for _ in range(20):
+            M = S.NONE
+            for t in range(4):
+                s = (rng.standard_normal(16) * 10.0 ** e).astype(F)
+                last, (w, M, _) = M, S.chunk_tile(s, c2, M)
+                assert w.max() <= 256.1
+                if M != last:
+                    assert w.max() >= 0.5
+                one = S.weights(s, c2, M, far=False)
+                wrong += not (one.max() <= 256.1 and (M == last or one.max() >= 0.5))
+    assert wrong > 100
