@@ -46,6 +46,7 @@ constexpr int TMA_WARP = 4, MMA_WARP = 5, NTHREADS = 6 * 32;
 constexpr int UNIT = 16 * 1024;        // a tile of K or of V, spread to 8-bit containers
 constexpr float LAZY = 8.f;            // log2 of the largest weight relative to the running reference
 constexpr float NONE = -1e30f;         // reference of a query that has seen no token
+constexpr float FAR = 4194304.f;       // 2^22: the last bit of a block's power of two is half a unit of log2
 
 // COLS queries; HP heads share a group of 128 channels
 template <int COLS, int HP>
@@ -467,7 +468,10 @@ __global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_ker
         }
         named_bar_sync(1, 128);   // `red` is read
       }
-      // ---- weights, times 2^8 / the block's power of two
+      // ---- weights, times 2^8 / the block's power of two.  From powers of FAR on the product
+      // s * sl2 is rounded by itself, as the power's was: rounded once with the difference it
+      // exceeds the power by up to half the last bit, and P / scale e4m3's range.
+      const bool far = __any_sync(0xFFFFFFFFu, fabsf(m_own) > FAR && m_own != -INFINITY);
       uint32_t hi2[HC / 2], lo2[HC / 2];
 #pragma unroll
       for (int c = 0; c < HC; c += 2) {
@@ -476,7 +480,9 @@ __global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_ker
         for (int i = 0; i < 2; ++i) {
           const float m = bias[c + i], d = m - M[c + i];
           // below 2^-60 of the reference a block adds nothing
-          w[i] = ex2(fmaf(s[c + i], sl2, d >= -60.f ? 8.f - m : NONE));
+          float x = fmaf(s[c + i], sl2, d >= -60.f ? 8.f - m : NONE);
+          if (far && fabsf(m) > FAR) x = d >= -60.f ? __fadd_rn(__fmul_rn(s[c + i], sl2), -m) + 8.f : NONE;
+          w[i] = ex2(x);
           l[c + i] = fmaf(w[i], ex2(d), l[c + i]);
         }
         const uint32_t h = cvt_h2_e4m3(cvt_e4m3(w[0], w[1]));

@@ -85,3 +85,10 @@ def _far(env, D, n, far):
 @pytest.mark.parametrize("far", FAR)
 def test_far_scores_of_chunks(env, D, far):
     _far(env, D, 60, far)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 7, 20, 47])
+@pytest.mark.parametrize("far", FAR)
+def test_far_scores_of_few_queries(env, D, n, far):
+    _far(env, D, n, far)

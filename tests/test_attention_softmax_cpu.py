@@ -63,3 +63,18 @@ def test_weights_of_far_scores():
                 one = S.weights(s, c2, M, far=False)
                 wrong += not (one.max() <= 256.1 and (M == last or one.max() >= 0.5))
     assert wrong > 100
+
+
+def test_weights_of_a_far_block_fit_e4m3():
+    """Few queries: a block's largest weight times 2^8 over its power of two, at most 2^8 (e4m3 ends at 448)."""
+    rng = np.random.default_rng(2)
+    c2 = S.log2e(128 ** -0.5)
+    beyond = 0
+    for e in np.arange(0, 37, 0.25):
+        s = (rng.uniform(1, 10, 400) * rng.choice([-1, 1], 400) * 10.0 ** e).astype(F)   # blocks of one token each
+        m = np.ceil(F(s * c2))
+        once = S.fma(s, c2, F(F(8) - m))
+        x = np.where(np.abs(m) > S.FAR, F(F(F(s * c2) - m) + F(8)), once)
+        assert x.max() <= 8.71 and x.min() >= 7 - 2.0 ** -20
+        beyond += (once > np.log2(448)).sum()
+    assert beyond > 100
