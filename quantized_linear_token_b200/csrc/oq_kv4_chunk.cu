@@ -415,8 +415,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float x, y;
-              const f32x2 s2 = pack2(__uint_as_float(v[c & 1][8 * g + j]), __uint_as_float(v[c & 1][8 * g + j + 4]));
-              unpack2(decltype(apart)::value ? add2(mul2(s2, c2), m2) : fma2(s2, c2, m2), x, y);
+              x = __uint_as_float(v[c & 1][8 * g + j]), y = __uint_as_float(v[c & 1][8 * g + j + 4]);
+              // (packed products and sums may be fused again; these are not)
+              if constexpr (decltype(apart)::value) x = __fadd_rn(__fmul_rn(x, sl2), -M), y = __fadd_rn(__fmul_rn(y, sl2), -M);
+              else unpack2(fma2(pack2(x, y), c2, m2), x, y);
               x = ex2(x), y = ex2(y);
               top[j & 1] = fmaxf(fmaxf(top[j & 1], x), y);
               sum[j & 1] = add2(sum[j & 1], pack2(x, y));
