@@ -363,6 +363,10 @@ __global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_ker
     for (int c = 0; c < HC; ++c) M[c] = NONE, l[c] = 0.f;
     const float sl2 = a.scale * 1.4426950408889634f;
     const bool steps = a.causal || a.window > 0;
+    // bits of the columns that are queries: a token that only the others would see is hidden
+    uint32_t exist = 0u;
+#pragma unroll
+    for (int h = 0; h < HP; ++h) exist |= (0xFFFFFFFFu >> (32 - min(COLS, columns - c0))) << (h * COLS);
     const int vs_at = (hg * KV_ROWS + KV_VS_ROW) * 64 + key * 4;
     const int64_t page_bytes = a.kv.groups * KV_GROUP_BYTES;
     int page = 0, next_page = nt > 0 ? table[0] : -1;
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_ker
       const int sb = t % SB;
       // ---- what is hidden
       const bool there = page >= 0 && page < a.kv.pages && j < len;
-      uint32_t seen = there ? 0xFFFFFFFFu : 0u;   // bit c: query c sees this token
+      uint32_t seen = there ? exist : 0u;   // bit c: query c sees this token
       if (steps && ((a.causal && j0 + KV_PAGE - 1 > past + i_first) || (a.window > 0 && j0 <= past + i_last - a.window))) {
 #pragma unroll
         for (int c = 0; c < COLS; ++c) {

@@ -92,3 +92,37 @@ def test_far_scores_of_chunks(env, D, far):
 @pytest.mark.parametrize("far", FAR)
 def test_far_scores_of_few_queries(env, D, n, far):
     _far(env, D, n, far)
+
+
+@pytest.mark.parametrize("D,H,KH", [(128, 2, 1), (128, 4, 4), (64, 8, 2), (64, 3, 3), (128, 12, 1), (64, 20, 1)])
+@pytest.mark.parametrize("n", [1, 3])
+def test_hidden_values_do_not_count(env, D, H, KH, n):
+    """A window's border inside 32 tokens, and the causal one: values that no query sees are 2^20 times larger, and the
+    result is as exact as without them."""
+    torch, B = env
+    rng = np.random.default_rng(42)
+    kv = B.oq_kv4_create(H, KH, D)
+    lens, window = [270, 413, 50], 75
+    s = Streams(torch, rng, kv, [n] * 3, lens)
+    for b, m in enumerate(lens):
+        for j in range(128 * s.pages.shape[1]):
+            if s.pages[b, j // 128] < len(s.np_cache):
+                big = j >= m or j < m - n - window + 1
+                A.write_token(s.np_cache, s.pages[b, j // 128], j % 128, rng.standard_normal(KH * D),
+                              rng.standard_normal(KH * D) * (2.0 ** 20 if big else 1))
+    s.cache.copy_(torch.from_numpy(s.np_cache))
+    q = torch.from_numpy(rng.standard_normal((s.T, H, D)).astype(np.float32)).cuda().bfloat16()
+    _check_attention(torch, B, kv, s, q, window=window)
+    # fewer queries than columns, the call's tokens among them larger than all: only the last token sees its own
+    for b, m in enumerate(lens):
+        A.write_token(s.np_cache, s.pages[b, (m - 1) // 128], (m - 1) % 128, rng.standard_normal(KH * D),
+                      rng.standard_normal(KH * D) * 2.0 ** 20)
+    s.cache.copy_(torch.from_numpy(s.np_cache))
+    y = _np(B.oq_kv4_attention(kv, q, *s.view, max(n - 1, 1), window=window))
+    ck, cv = A.cache_values(s.np_cache)
+    for b, m in enumerate(lens):
+        K, V, ok = A.sequence(ck, cv, s.pages[b], m - 1, KH, D)
+        if n > 1:
+            r = slice(s.np_cu[b], s.np_cu[b + 1] - 1)
+            want, tol = A.attention(_np(q)[r], K, V, ok, np.float64(np.float32(D ** -0.5)), True, window)
+            assert (np.abs(y[r] - want) <= tol).all()
