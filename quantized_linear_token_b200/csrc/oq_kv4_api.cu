@@ -24,7 +24,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 size_t size_of(int32_t dtype) { return dtype == OQ_DTYPE_F32 ? 4 : 2; }
 bool known(int32_t dtype) { return dtype == OQ_DTYPE_F32 || dtype == OQ_DTYPE_BF16; }
 
-// Rows of bytes at equal distances; one row where an array is contiguous.
+// Rows of bytes at equal distances; one row where an array is contiguous (its stride is its length).
 struct Rows {
   const void* p;
   size_t row, stride;
@@ -34,7 +34,7 @@ struct Rows {
 Rows flat(const void* p, size_t bytes) { return {p, bytes, bytes, 1}; }
 Rows heads_of(const void* p, int64_t T, int32_t heads, int32_t D, int64_t stride, int32_t dtype) {
   const size_t e = size_of(dtype);
-  return {p, (size_t)heads * D * e, (size_t)stride * e, T};
+  return {p, (size_t)heads * D * e, T > 1 ? (size_t)stride * e : (size_t)heads * D * e, T};   // (one token: any stride)
 }
 // whether they share a byte; rows with equal strides may lie in each other's gaps
 bool overlap(const Rows& a, const Rows& b) {
@@ -45,7 +45,7 @@ bool overlap(const Rows& a, const Rows& b) {
   const size_t d = y >= x ? (y - x) % a.stride : (a.stride - (x - y) % a.stride) % a.stride;
   return d < a.row || d + b.row > a.stride;
 }
-bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.row == b.row && (a.stride == b.stride || a.n <= 1); }
+bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.row == b.row && a.stride == b.stride; }
 
 struct QkIn {
   const char* who;

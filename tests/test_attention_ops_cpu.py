@@ -202,3 +202,27 @@ def test_attention_reference_of_one_token():
     y, tol = A.attention(q, K, V, np.array([True, False, True, True, True]), 0.3, True, 3)
     p = np.exp(0.3 * q[0, 1] @ K[[2, 3, 4], 0].T)
     assert np.allclose(y[0, 1], p @ V[[2, 3, 4], 0] / p.sum()) and (tol > 0).all()
+
+
+@pytest.mark.parametrize("stride", [0, -512, 8, 512, 1 << 40])
+def test_overlaps_of_one_token(lib, kv, stride):
+    """The stride of one token says nothing: any is taken, and overlaps are found."""
+    def rope(q=P, k=2 * P, qo=3 * P, ko=4 * P):
+        return lib.oq_qk_norm_rope(q, stride, 4, k, stride, 2, 1, 1, 128, None, None, 0, 1e-6, None, 0, 0, None, 0, qo, stride, ko,
+                                   stride, None)
+
+    def append(q=P, k=2 * P, v=3 * P, qo=4 * P, cache=64 * P):
+        return lib.oq_kv4_append(ctypes.byref(kv), q, stride, k, stride, v, stride, 1, 1, None, None, 0, 1e-6, None, 0, 0, None, 0,
+                                 qo, cache, 8, 5 * P, 4, 6 * P, 7 * P, 2, None)
+
+    def attend(q=P, y=2 * P):
+        return lib.oq_kv4_attention(ctypes.byref(kv), q, stride, 1, 64 * P, 8, 5 * P, 4, 6 * P, 7 * P, 2, 1, 300, 0.1, 1, 0, y, None,
+                                    0, None)
+
+    for f in (lambda: rope(qo=4 * P), lambda: rope(qo=2 * P + 256), lambda: rope(ko=P + 512), lambda: rope(ko=P),
+              lambda: append(qo=2 * P), lambda: append(qo=3 * P - 32), lambda: append(cache=P), lambda: attend(y=P),
+              lambda: attend(y=P + 1024)):
+        assert f() == 1
+        assert b"overlap" in lib.oq_last_error()
+    if _no_gpu():   # side by side, or in place: past the checks, where the runtime refuses the launch
+        assert rope(qo=4 * P - 1024) == 3 and rope(qo=P, ko=2 * P) == 3 and append(qo=P) == 3
