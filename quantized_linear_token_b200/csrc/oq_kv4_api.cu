@@ -2,6 +2,7 @@
 // include/orbitquant.h): argument checks, the handle and dispatch.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 #include <new>
@@ -21,6 +22,7 @@ oq_status unsupported(const char* who, const char* what) {
   return fail(OQ_ERR_UNSUPPORTED, std::string(who) + ": " + what);
 }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+constexpr int64_t MOST_BYTES = (int64_t)1 << 60;   // of an array: sums and products of addresses stay within 64 bits
 size_t size_of(int32_t dtype) { return dtype == OQ_DTYPE_F32 ? 4 : 2; }
 bool known(int32_t dtype) { return dtype == OQ_DTYPE_F32 || dtype == OQ_DTYPE_BF16; }
 
@@ -67,6 +69,7 @@ oq_status check_qk(const QkIn& a) {
     return invalid(a.who, "gains and table must be 16-byte aligned, positions 4-byte");
   if (a.table) {
     if (a.table_rows < 1) return invalid(a.who, "the table must have a row");
+    if (a.table_rows > MOST_BYTES / 4 / std::max(a.rot, 1)) return unsupported(a.who, "the table is too large");
     if (a.rot <= 0 || a.rot > a.D || a.rot % (a.flags & OQ_QK_INTERLEAVED ? 8 : 16))
       return unsupported(a.who, "rotated channels must be a multiple of 8 (interleaved) or 16, up to the head's");
   }
@@ -77,7 +80,7 @@ oq_status check_heads(const char* who, const char* name, const void* p, int32_t 
                       int64_t T, int32_t dtype) {
   if (!p || !aligned(p, 16)) return invalid(who, (std::string(name) + " must be a 16-byte aligned pointer").c_str());
   if ((T > 1 && stride < (int64_t)heads * D) || (T > 1 && (stride * (int64_t)size_of(dtype)) % 16) ||
-      stride > ((int64_t)1 << 40))
+      stride > ((int64_t)1 << 40) || (T > 1 && stride > MOST_BYTES / (int64_t)size_of(dtype) / (T - 1)))
     return invalid(who, (std::string(name) + "'s token stride must cover its heads and be a multiple of 16 bytes").c_str());
   return OQ_OK;
 }
@@ -306,7 +309,7 @@ oq_status oq_kv4_read(const oq_kv4* kv, const uint8_t* cache, int64_t pages, con
 }
 
 size_t oq_kv4_attention_workspace_size(const oq_kv4* kv, int64_t T, int32_t B, int32_t max_q, int32_t max_len) {
-  if (!kv || T <= 0 || B <= 0 || max_q <= 0 || max_len < 0) return 0;
+  if (!kv || T <= 0 || T > 0x7FFFFFFF / kv->heads || B <= 0 || max_q <= 0 || max_len < 0) return 0;   // (such calls are refused or empty)
   return kv4_attention_workspace(kv, T, B, max_q, max_len);
 }
 

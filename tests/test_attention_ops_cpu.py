@@ -226,3 +226,18 @@ def test_overlaps_of_one_token(lib, kv, stride):
         assert b"overlap" in lib.oq_last_error()
     if _no_gpu():   # side by side, or in place: past the checks, where the runtime refuses the launch
         assert rope(qo=4 * P - 1024) == 3 and rope(qo=P, ko=2 * P) == 3 and append(qo=P) == 3
+
+
+def test_arrays_beyond_64_bits_are_refused(lib, kv):
+    """Strides and tables whose extents would wrap around: an overlap could go unnoticed."""
+    T, stride = (1 << 31) - 1, 1 << 40
+    assert lib.oq_qk_norm_rope(P, stride, 4, None, 0, 0, 1, T, 128, None, None, 0, 1e-6, None, 0, 0, None, 0, 2 * P, stride, None, 0,
+                               None) == 1
+    assert lib.oq_qk_norm_rope(P, 512, 4, None, 0, 0, 1, 3, 128, None, None, 0, 1e-6, 5 * P, 1 << 61, 128, None, 0, 2 * P, 512, None,
+                               0, None) == 2
+    # 2^22 tokens 2^40 fp32 elements apart: the last one's offset is a multiple of 2^64
+    assert lib.oq_kv4_append(ctypes.byref(kv), None, 0, P, stride, 3 * P, stride, 0, (1 << 22) + 1, None, None, 0, 1e-6, None, 0, 0,
+                             None, 0, None, 64 * P, 8, 5 * P, 4, 6 * P, 7 * P, 2, None) == 1
+    assert b"stride" in lib.oq_last_error()
+    size = lambda T: lib.oq_kv4_attention_workspace_size(ctypes.byref(kv), T, 2, 1, 100000)
+    assert size(1 << 62) == size(1 << 58) == size((1 << 31) // 8) == 0
