@@ -615,13 +615,14 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinP
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (row >= p.rows) return;
-  // tokens of no sequence (before the first, behind the last, past max_q) have no parts
+  // tokens of no sequence (before the first, behind the last, past max_q) have no parts, nor
+  // have those of a sequence that reaches behind the call's arrays
   const int t = (int)(row / p.heads);
   int start = -1;
   for (int b0 = 0; b0 < p.B && start < 0; b0 += 32) {
     const int b = b0 + lane;
     int at = -1;
-    if (b < p.B && p.cu[b] <= t && t < p.cu[b + 1]) at = p.cu[b];
+    if (b < p.B && p.cu[b] <= t && t < p.cu[b + 1] && p.cu[b + 1] <= p.T) at = p.cu[b];
     start = __reduce_max_sync(0xFFFFFFFFu, at);
   }
   if (start < 0 || t - start >= p.max_q) return;

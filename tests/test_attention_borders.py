@@ -126,3 +126,19 @@ def test_hidden_values_do_not_count(env, D, H, KH, n):
             r = slice(s.np_cu[b], s.np_cu[b + 1] - 1)
             want, tol = A.attention(_np(q)[r], K, V, ok, np.float64(np.float32(D ** -0.5)), True, window)
             assert (np.abs(y[r] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("n", [2, 60])
+def test_a_sequence_behind_the_arrays_has_no_output_in_parts(env, n):
+    """Its tokens have no parts to join: what the workspace held before does not become its result."""
+    torch, B = env
+    rng = np.random.default_rng(43)
+    kv = B.oq_kv4_create(1, 1, 128)
+    s = Streams(torch, rng, kv, [n, n], [3000, 2000])
+    q = torch.from_numpy(rng.standard_normal((2 * n - 1, 1, 128)).astype(np.float32)).cuda().bfloat16()
+    need = B.oq_kv4_attention_workspace_size(kv, 2 * n - 1, 2, n, 3000)
+    assert need > 0
+    w = torch.ones(need // 4, device="cuda")
+    y = torch.full((2 * n - 1, 1, 128), 3.0, device="cuda", dtype=torch.bfloat16)
+    B.oq_kv4_attention(kv, q, *s.view, n, max_len=3000, y=y, workspace=w)
+    assert (y[n:] == 3).all() and not (y[:n] == 3).all()
