@@ -637,7 +637,7 @@ oq_status oq_kv4_attention(const oq_kv4* kv, const void* q, int64_t q_stride, in
                            const int32_t* page_table, int32_t table_width, const int32_t* cu, const int32_t* lens, int32_t B,
                            int32_t max_q, int32_t max_len, float scale, int32_t flags, int32_t window, void* y,
                            void* workspace, size_t workspace_bytes, void* stream);
-/* Reads and clears the handle's device error word, as oq_poll_error does a layer's. */
+/* Reads and clears the handle's device error word, as oq_poll_error does a layer's, on the handle's device. */
 oq_status oq_kv4_poll_error(const oq_kv4* kv);
 
 /*

@@ -722,9 +722,10 @@ def oq_qk_norm_rope(q, k=None, q_gain=None, k_gain=None, eps: float = 1e-6, tabl
 class Kv4:
     """Owns an oq_kv4* (a shape of attention over a 4-bit cache and its error word)."""
 
-    def __init__(self, handle: int, lib, heads: int, kv_heads: int, head_dim: int):
+    def __init__(self, handle: int, lib, heads: int, kv_heads: int, head_dim: int, device: int):
         self._h = ctypes.c_void_p(handle)
         self._lib = lib
+        self.device = device   # its index
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.groups = (kv_heads * head_dim + 127) // 128
         self.scale = head_dim ** -0.5
@@ -756,7 +757,7 @@ def oq_kv4_create(heads: int, kv_heads: int, head_dim: int) -> Kv4:
     L = load_library()
     h = ctypes.c_void_p()
     _check(L.oq_kv4_create(heads, kv_heads, head_dim, ctypes.byref(h)), "oq_kv4_create")
-    return Kv4(h.value, L, heads, kv_heads, head_dim)
+    return Kv4(h.value, L, heads, kv_heads, head_dim, _torch().cuda.current_device())
 
 
 def oq_kv4_destroy(kv: Kv4) -> None:
@@ -876,7 +877,8 @@ def oq_kv4_attention(kv: Kv4, q, cache, page_table, cu, lens, max_q: int, max_le
 
 
 def oq_kv4_poll_error(kv: Kv4) -> None:
-    _check(load_library().oq_kv4_poll_error(kv.handle), "oq_kv4_poll_error")
+    with _torch().cuda.device(kv.device):
+        _check(load_library().oq_kv4_poll_error(kv.handle), "oq_kv4_poll_error")
 
 
 # ------------------------------------------------------------------ 4-bit weights with group scales

@@ -105,6 +105,11 @@ Rows table_of(const QkIn& a) { return flat(a.table, a.table ? (size_t)a.table_ro
 Rows positions_of(const QkIn& a) { return flat(a.positions, a.positions ? (size_t)a.T * 4 : 0); }
 Rows gain_of(const QkIn& a, const void* g) { return flat(g, g ? (size_t)a.D * size_of(a.gain_dtype) : 0); }
 
+bool on_device(const oq_kv4* kv) {
+  int dev = -1;
+  cudaGetDevice(&dev);
+  return dev == kv->device;
+}
 oq_status check_cache(const char* who, const oq_kv4* kv, const void* cache, int64_t pages, const int32_t* table,
                       int32_t width, const int32_t* cu, const int32_t* lens, int32_t B, KvView* view) {
   if (!kv) return invalid(who, "the handle is null");
@@ -115,9 +120,7 @@ oq_status check_cache(const char* who, const oq_kv4* kv, const void* cache, int6
   if (pages == 0 || pages > 0x7FFFFFFF / KV_ROWS / kv->groups)
     return unsupported(who, "the cache must have a page and at most 2^31 / 272 groups of 128 channels in its pages");
   if (width > 0x7FFFFFFF / KV_PAGE || B > 65535) return unsupported(who, "table_width or B too large");
-  int dev = -1;
-  cudaGetDevice(&dev);
-  if (dev != kv->device) return invalid(who, "the handle was created on another device than the current one");
+  if (!on_device(kv)) return invalid(who, "the handle was created on another device than the current one");
   view->cache = static_cast<uint8_t*>(const_cast<void*>(cache));
   view->pages = pages;
   view->table = table;
@@ -225,6 +228,8 @@ void oq_kv4_destroy(oq_kv4* kv) {
 oq_status oq_kv4_poll_error(const oq_kv4* kv) {
   const char* who = "oq_kv4_poll_error";
   if (!kv) return invalid(who, "the handle is null");
+  // (on another device the calls whose word this is would not be waited for)
+  if (!on_device(kv)) return invalid(who, "the handle was created on another device than the current one");
   int word = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&word, kv->d_error, sizeof(int), cudaMemcpyDeviceToHost);

@@ -241,3 +241,14 @@ def test_arrays_beyond_64_bits_are_refused(lib, kv):
     assert b"stride" in lib.oq_last_error()
     size = lambda T: lib.oq_kv4_attention_workspace_size(ctypes.byref(kv), T, 2, 1, 100000)
     assert size(1 << 62) == size(1 << 58) == size((1 << 31) // 8) == 0
+
+
+def test_calls_from_another_device_are_refused(lib, kv):
+    other = _Handle(8, 2, 128, 2, kv.device + 1, None)
+    h = ctypes.byref(other)
+    for call in (lambda: lib.oq_kv4_poll_error(h),
+                 lambda: lib.oq_kv4_read(h, 64 * P, 8, 5 * P, 4, 6 * P, 7 * P, 2, 3, P, 2 * P, 0, None),
+                 lambda: lib.oq_kv4_attention(h, P, 1024, 3, 64 * P, 8, 5 * P, 4, 6 * P, 7 * P, 2, 2, 300, 0.1, 1, 0, 2 * P, None, 0,
+                                              None)):
+        assert call() == 1
+        assert b"device" in lib.oq_last_error()
