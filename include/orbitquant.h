@@ -590,7 +590,8 @@ oq_status oq_qk_norm_rope(const void* q, int64_t q_stride, int32_t q_heads, cons
  *   q, k, v   device [T, heads or kv_heads, head_dim] of dtype with token strides;
  *             q may be null (with q_out).
  *   q_out     device bf16 [T, heads, head_dim], contiguous; may be q itself where
- *             that is bf16 and contiguous.
+ *             that is bf16 and contiguous.  Rows of no sequence (before cu[0], from
+ *             cu[B] on) stay as they were.
  *   positions null: each token's place in its sequence.
  * The codes of a key are those of its value in exact arithmetic.  Tokens without a
  * page, and those of a sequence whose lens is below its tokens, are not stored.

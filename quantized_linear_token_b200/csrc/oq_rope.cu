@@ -193,7 +193,8 @@ struct RopeGrid {
 // first rows' loads leave before the token's place and its table row are known,
 // and PF rows stay in flight.  Rows out of fp32's range are
 // marked and done in fp64 behind each 32 turns (inside the loop they would cost
-// all rows registers).
+// all rows registers).  place: a token's row of the table, and whether it has one: the
+// rows of a token that has none stay as they are.
 template <typename T, typename OUT, bool INTER, int LANES, typename POS>
 __device__ __forceinline__ void rope_rows(const RopeArgs& p, const RopeGrid& g, int which, int cta, POS&& place) {
   constexpr int PF = sizeof(T) == 2 ? 4 : 2, PAIR = 2, MARKS = 32;
@@ -202,7 +203,7 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& p, const RopeGrid& g, 
   const int sub = cta % g.split * g.per_token + grp % g.per_token, step = g.split * g.per_token;
   const bool in = t < p.T && ch < p.D;
   const int rows = p.heads[which], turns = (rows + step - 1) / step, hop = step * p.D;
-  const int mine = in && sub < rows ? (rows - sub + step - 1) / step : 0;   // this lane's rows
+  int mine = in && sub < rows ? (rows - sub + step - 1) / step : 0;   // this lane's rows
   const T* x0 = static_cast<const T*>(p.x[which]) + t * p.in_stride[which] + sub * p.D + ch;
   OUT* y0 = static_cast<OUT*>(p.out[which]) + t * p.out_stride[which] + sub * p.D + ch;
   Vec8<T> raw[PF];
@@ -216,7 +217,9 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& p, const RopeGrid& g, 
   };
 #pragma unroll
   for (int u = 0; u < PF; ++u) fetch(raw[u]);
-  const int64_t pos = place(t);
+  bool held = true;
+  const int64_t pos = place(t, held);
+  if (!held) mine = 0;
   const Coef<INTER> k = make_coef<INTER>(p, p.gain[which], pos, ch, in);
   const float inv_d = 1.0f / (float)p.D;
   OUT* y = y0;
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(NT, 3) rope_kernel(const __grid_constant__ Rop
   const int last = p.both ? 1 : which, cta = (int)blockIdx.x - (which ? p.g[0].ctas : 0);
 #pragma unroll 1
   for (; which <= last; ++which)
-    rope_rows<T, T, INTER, LANES>(p.a, p.g[which], which, cta, [&](int64_t t) {
+    rope_rows<T, T, INTER, LANES>(p.a, p.g[which], which, cta, [&](int64_t t, bool&) {
       return t >= p.a.T ? (int64_t)0 : p.a.positions ? (int64_t)p.a.positions[t] : t;
     });
 }
@@ -471,7 +474,8 @@ __global__ void __launch_bounds__(ANT, 3) append_kernel(const __grid_constant__ 
   const KvView& kv = p.a.kv;
   dependency_wait();
   if ((int)blockIdx.x < p.g.ctas) {
-    rope_rows<T, __nv_bfloat16, INTER, LANES>(r, p.g, 0, (int)blockIdx.x, [&](int64_t t) {
+    rope_rows<T, __nv_bfloat16, INTER, LANES>(r, p.g, 0, (int)blockIdx.x, [&](int64_t t, bool& held) {
+      held = t >= kv.cu[0] && t < kv.cu[kv.B];   // a token of no sequence has no place
       if (!r.table) return (int64_t)0;
       if (r.positions) return t < r.T ? (int64_t)r.positions[t] : (int64_t)0;
       // the token's sequence: how many of them end at or before it

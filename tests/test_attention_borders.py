@@ -142,3 +142,32 @@ def test_a_sequence_behind_the_arrays_has_no_output_in_parts(env, n):
     y = torch.full((2 * n - 1, 1, 128), 3.0, device="cuda", dtype=torch.bfloat16)
     B.oq_kv4_attention(kv, q, *s.view, n, max_len=3000, y=y, workspace=w)
     assert (y[n:] == 3).all() and not (y[:n] == 3).all()
+
+
+@pytest.mark.parametrize("D,table,dtype", [(128, True, "bf16"), (64, False, "bf16"), (64, True, "fp32")])
+def test_append_leaves_queries_of_no_sequence_alone(env, D, table, dtype):
+    """A padded batch: rows before the first sequence and behind the last, in place and not, the sequences' own as in a
+    call without them."""
+    torch, B = env
+    rng = np.random.default_rng(44)
+    kv = B.oq_kv4_create(4, 2, D)
+    s = Streams(torch, rng, kv, [3, 0, 40], [200, 9, 41])
+    T = s.T + 25
+    x = torch.from_numpy(rng.standard_normal((T, 8, D)).astype(np.float32)).cuda()
+    x = x if dtype == "fp32" else x.bfloat16()
+    q, k, v = x[:, :4].contiguous(), x[:, 4:6], x[:, 6:]
+    t = torch.from_numpy(rng.standard_normal((250, D // 2, 2)).astype(np.float32)).cuda() if table else None
+    pos = torch.from_numpy(rng.integers(0, 250, T).astype(np.int32)).cuda() if table else None
+    rows = slice(2, 2 + s.T)
+    for p in (None, pos):
+        part = B.oq_kv4_append(kv, q[rows], k[rows], v[rows], *s.view, table=t, positions=None if p is None else p[rows].contiguous())
+        cache = s.cache.clone()
+        outs = [torch.full((T, 4, D), 3.0, device="cuda", dtype=torch.bfloat16)]
+        if dtype == "bf16":
+            outs.append(q.clone())
+        for out in outs:
+            before = out.clone()
+            y = B.oq_kv4_append(kv, out if out is not outs[0] else q, k, v, s.cache, s.table, s.cu + 2, s.len, table=t, positions=p,
+                                q_out=out)
+            assert y is out and torch.equal(out[rows], part) and torch.equal(cache, s.cache)
+            assert torch.equal(out[:2], before[:2]) and torch.equal(out[2 + s.T:], before[2 + s.T:])
