@@ -45,7 +45,7 @@ namespace {
 constexpr int TMA_WARP = 4, MMA_WARP = 5, NTHREADS = 6 * 32;
 constexpr int UNIT = 16 * 1024;        // a tile of K or of V, spread to 8-bit containers
 constexpr float LAZY = 8.f;            // log2 of the largest weight relative to the running reference
-constexpr float NONE = -1e30f;         // reference of a query that has seen no token
+constexpr float NONE = -3.4028234e38f; // reference of a query that has seen no token: below every score's
 constexpr float FAR = 4194304.f;       // 2^22: the last bit of a block's power of two is half a unit of log2
 
 // COLS queries; HP heads share a group of 128 channels

@@ -40,7 +40,7 @@ constexpr int DEC_WARP = 8, MMA_WARP = 16, NTHREADS = 20 * 32, DEC_THREADS = 256
 // registers of a thread of each four warps; together the launch's 640 x 96
 constexpr int SOFTMAX_REGS = 136, DECODE_REGS = 80, MMA_REGS = 48;
 static_assert(2 * SOFTMAX_REGS + 2 * DECODE_REGS + MMA_REGS == 5 * 96, "more would wait for good");
-constexpr float LAZY = 8.f, NONE = -1e30f;    // as in oq_kv4_attention.cu
+constexpr float LAZY = 8.f, NONE = -3.4028234e38f;   // as in oq_kv4_attention.cu
 constexpr float FAR = 4194304.f;              // 2^22: the last bit of a reference is half a unit of log2
 
 template <int D>

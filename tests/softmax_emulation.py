@@ -3,7 +3,7 @@
 import numpy as np
 
 F = np.float32
-LAZY, NONE = F(8), F(-1e30)
+LAZY, NONE = F(8), -np.finfo(F).max
 
 
 def fma(a, b, c):

@@ -171,3 +171,11 @@ def test_append_leaves_queries_of_no_sequence_alone(env, D, table, dtype):
                                 q_out=out)
             assert y is out and torch.equal(out[rows], part) and torch.equal(cache, s.cache)
             assert torch.equal(out[:2], before[:2]) and torch.equal(out[2 + s.T:], before[2 + s.T:])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 4, 47, 60])
+@pytest.mark.parametrize("far", [2.0 ** 103 * 1.2, 2.0 ** 110, 2.0 ** 124 * 1.6])
+def test_scores_up_to_the_end_of_fp32(env, D, n, far):
+    """Among them queries all of whose scores are below -10^30."""
+    _far(env, D, n, far)
