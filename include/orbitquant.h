@@ -605,7 +605,8 @@ oq_status oq_qk_norm_rope(const void* q, int64_t q_stride, int32_t q_heads, cons
  *             tokens past it get no output.
  *   max_len   about the longest sequence: how the work is split depends on it,
  *             the values only by rounding.
- *   scale     positive.
+ *   scale     positive; scale log2(e) finite, and so, for a result that is, times
+ *             every score.
  *   flags     OQ_ATTN_CAUSAL: a token sees its sequence up to itself; otherwise
  *             all of it.  window > 0: only tokens less than `window` before it.
  *   y         device bf16 [T, heads, head_dim].  A token that sees nothing gets 0.

@@ -328,7 +328,8 @@ oq_status oq_kv4_attention(const oq_kv4* kv, const void* q, int64_t q_stride, in
   if (st != OQ_OK) return st;
   if (T < 0 || max_q < 0 || max_len < 0 || window < 0)
     return invalid(who, "T, max_q, max_len and window must not be negative");
-  if (!(scale > 0.f) || std::isinf(scale)) return invalid(who, "scale must be positive and finite");
+  if (!(scale > 0.f) || std::isinf(scale * 1.4426950408889634f))
+    return invalid(who, "scale must be positive, and scale log2(e) finite");
   if (flags & ~OQ_ATTN_CAUSAL) return invalid(who, "unknown flags");
   const int group = kv->heads / kv->kv_heads;
   if (T > 0x7FFFFFFF / kv->heads || (int64_t)max_q * group > 0x7FFFFFFF - 64 || kv->kv_heads > 1023)

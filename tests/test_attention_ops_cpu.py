@@ -252,3 +252,10 @@ def test_calls_from_another_device_are_refused(lib, kv):
                                               None)):
         assert call() == 1
         assert b"device" in lib.oq_last_error()
+
+
+def test_a_scale_whose_product_is_infinite_is_refused(lib, kv):
+    """The softmax works in powers of two: an infinite factor would make a score of 0 a NaN."""
+    f = lambda scale: lib.oq_kv4_attention(ctypes.byref(kv), P, 1024, 3, 64 * P, 8, 5 * P, 4, 6 * P, 7 * P, 2, 0, 300, scale, 1, 0,
+                                           2 * P, None, 0, None)
+    assert f(3.3e38) == 1 and f(2.5e38) == 1 and f(2.3e38) == 0 and f(1e-45) == 0
