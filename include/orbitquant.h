@@ -597,7 +597,9 @@ oq_status oq_qk_norm_rope(const void* q, int64_t q_stride, int32_t q_heads, cons
  * page, and those of a sequence whose lens is below its tokens, are not stored.
  *
  * oq_kv4_read -- the values that this call's tokens have in the cache, [T,
- * kv_heads, head_dim] of dtype (exact; NaN where a page is not there).
+ * kv_heads, head_dim] of dtype (exact; NaN where a page is not there).  Rows of
+ * tokens that have no place in the cache stay as they were: those of no sequence, of
+ * one whose lens is below its tokens, and those past 128 table_width.
  *
  * oq_kv4_attention -- y = softmax(scale q K^T + mask) V over the cache:
  *   q         device bf16 [T, heads, head_dim] with a token stride.

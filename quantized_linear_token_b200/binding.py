@@ -786,7 +786,8 @@ def oq_kv4_append(kv: Kv4, q, k, v, cache, page_table, cu, lens, q_gain=None, k_
     """Keys and values [T, kv_heads, D] of new tokens to the cache, with the norm
     and rotation of oq_qk_norm_rope on queries and keys; q [T, heads, D] (or None)
     -> q_out bf16 [T, heads, D].  positions: default, each token's place in its
-    sequence.  See include/orbitquant.h for cache, page_table, cu and lens."""
+    sequence.  Rows of q_out that belong to no sequence are left alone (unset in a
+    new tensor).  See include/orbitquant.h for cache, page_table, cu and lens."""
     torch = _torch()
     if k.dim() != 3 or not k.is_cuda:
         raise ValueError("k must be a CUDA tensor [T, kv_heads, D]")
@@ -816,7 +817,8 @@ def oq_kv4_append(kv: Kv4, q, k, v, cache, page_table, cu, lens, q_gain=None, k_
 
 def oq_kv4_read(kv: Kv4, cache, page_table, cu, lens, T: int, dtype=None, k=None, v=None):
     """The values (fp32 by default, or bf16) that a call's T tokens have in the
-    cache -> (k, v) [T, kv_heads, D]."""
+    cache -> (k, v) [T, kv_heads, D]; NaN where a page is not there.  Rows of tokens
+    without a place in the cache are left alone (unset in new tensors)."""
     torch = _torch()
     device, shape = cache.device, (T, kv.kv_heads, kv.head_dim)
     if device.type != "cuda":
@@ -841,7 +843,8 @@ def oq_kv4_attention(kv: Kv4, q, cache, page_table, cu, lens, max_q: int, max_le
     (CUDA, any token stride) -> y bf16 [T, heads, D].  max_q: the most tokens of a
     sequence in this call; max_len: about the longest sequence (default: what the
     page table holds); scale: default D^-0.5; window: 0, or how many tokens, itself
-    among them, a token sees."""
+    among them, a token sees.  Rows of y that belong to no sequence, or to one's
+    tokens past max_q, are left alone (unset in a new tensor)."""
     torch = _torch()
     if q.dim() != 3 or not q.is_cuda or q.dtype is not torch.bfloat16:
         raise ValueError("q must be a bfloat16 CUDA tensor [T, heads, D]")
