@@ -612,12 +612,15 @@ oq_status oq_qk_norm_rope(const void* q, int64_t q_stride, int32_t q_heads, cons
  *   flags     OQ_ATTN_CAUSAL: a token sees its sequence up to itself; otherwise
  *             all of it.  window > 0: only tokens less than `window` before it.
  *   y         device bf16 [T, heads, head_dim].  A token that sees nothing gets 0.
+ *             Rows of no sequence, or of one that reaches behind T, stay as they were.
  *   workspace device scratch of oq_kv4_attention_workspace_size bytes (may be 0),
  *             256-byte aligned; calls that share it must not overlap.
- * Queries enter exactly, softmax and sums are fp32.  Weights are rounded to 8 bits,
- * as bf16's are; with fewer than 48 queries a key head (max_q heads / kv_heads) also
- * by up to 2^-16 of the largest weight times the largest |V| of 32 neighbouring
- * tokens in 32 channels.  |V| from 2^-90 to 2^90, or 0.  A NaN in a key or value
+ * Softmax and sums are fp32.  Weights are rounded to 8 bits, as bf16's are.  With
+ * fewer than 48 queries a key head (max_q heads / kv_heads) also by up to 2^-16 of the
+ * largest weight times the largest |V| of 32 neighbouring tokens in 32 channels (those
+ * that any query of the call sees; never of others), and queries by up to 2^-22 of the
+ * largest of 32 channels (an element above 2^-14 of that enters exactly); with more,
+ * queries enter exactly.  |V| from 2^-90 to 2^90, or 0.  A NaN in a key or value
  * reaches the queries that see it (in values: their block of 32 channels), an
  * infinite or NaN query its own row.  Results repeat bit for bit.  A bounded wait
  * that runs out is reported by oq_kv4_poll_error.

@@ -6,8 +6,9 @@
 // heads, of one token or several) and walks over tiles of 128 tokens, a page.
 //   S^T [128 tokens x queries]  = K [tokens x 128 channels] q^T      (K's scales: A's)
 //   O^T [128 channels x queries] += V^T [channels x 128 tokens] P    (V's scales: in P)
-// A query in bf16 is split exactly into two e4m3 terms (4 + 4 bits, two MMA
-// columns that are added up).  P is split into two e4m3 terms as well, 8 bits
+// A query in bf16 is split into two e4m3 terms (4 + 4 bits, two MMA columns that are
+// added up): exactly, but for elements below 2^-14 of their 32 channels' largest, which
+// are off by up to 2^-22 of that.  P is split into two e4m3 terms as well, 8 bits
 // as in bf16.  V's scales belong to a token and 32 channels, along M and K both,
 // which no operand scale can say; so P takes them up: four copies of P, each
 // times V's scales of one block of 32 channels, of which only the block's own 32
@@ -330,7 +331,8 @@ __global__ void __launch_bounds__(NTHREADS, (Cfg<COLS, HP>::CTAS)) attention_ker
 #pragma unroll
       for (int o = 1; o <= 4; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
       // largest magnitude in [128, 256): its first term's rounding leaves at most
-      // 8, which the second term holds times 32 to the last bit
+      // 8, which the second term holds times 32 to the last bit, of elements down to
+      // 2^-7; below, its step is 2^-14
       const int e = (int)(m >> 23);
       const uint32_t sc = e == 255 ? 255u : (uint32_t)max(e - 7, 5);
       const float inv = mx_inverse_scale(sc);

@@ -179,3 +179,22 @@ def test_append_leaves_queries_of_no_sequence_alone(env, D, table, dtype):
 def test_scores_up_to_the_end_of_fp32(env, D, n, far):
     """Among them queries all of whose scores are below -10^30."""
     _far(env, D, n, far)
+
+
+@pytest.mark.parametrize("D,H,KH", [(128, 2, 1), (64, 8, 2), (128, 16, 1)])
+def test_small_query_channels_meet_large_keys(env, D, H, KH):
+    """Channels from 2^-10 to 2^-22 of their block's largest, under keys that make up for it."""
+    torch, B = env
+    rng = np.random.default_rng(45)
+    kv = B.oq_kv4_create(H, KH, D)
+    s = Streams(torch, rng, kv, [2, 1], [300, 41])
+    down = 2.0 ** -(10 + np.arange(D) % 13)
+    down[::32] = 1                              # a block's largest
+    up = np.where(down == 1, 2.0 ** -4, 2.0 ** 12)   # (one scale for a block: keys of 2^12 beside keys of 0)
+    for b, m in enumerate(s.lens):
+        for j in range(m):
+            k = rng.standard_normal((KH, D)) * up * (rng.random((KH, D)) < 0.3)
+            A.write_token(s.np_cache, s.pages[b, j // 128], j % 128, k.ravel(), rng.standard_normal(KH * D))
+    s.cache.copy_(torch.from_numpy(s.np_cache))
+    q = torch.from_numpy((rng.uniform(1, 2, (s.T, H, D)) * rng.choice([-1, 1], (s.T, H, D)) * down).astype(np.float32)).cuda().bfloat16()
+    _check_attention(torch, B, kv, s, q)

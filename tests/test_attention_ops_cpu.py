@@ -259,3 +259,13 @@ def test_a_scale_whose_product_is_infinite_is_refused(lib, kv):
     f = lambda scale: lib.oq_kv4_attention(ctypes.byref(kv), P, 1024, 3, 64 * P, 8, 5 * P, 4, 6 * P, 7 * P, 2, 0, 300, scale, 1, 0,
                                            2 * P, None, 0, None)
     assert f(3.3e38) == 1 and f(2.5e38) == 1 and f(2.3e38) == 0 and f(1e-45) == 0
+
+
+def test_small_query_elements_are_off_by_little():
+    """Below 2^-14 of its block's largest an element is off by up to 2^-22 of that."""
+    m = np.arange(128, 256) / 128.0
+    for e in range(-8, -24, -1):
+        y = m * 2.0 ** e
+        hi = R.code_values(R.round_codes(y, 8), 8)
+        lo = R.code_values(R.round_codes((y - hi) * 32, 8), 8) / 32
+        assert np.abs(hi + lo - y).max() <= 128 * 2.0 ** -22
