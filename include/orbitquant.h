@@ -548,8 +548,9 @@ oq_status oq_linear_mx(const oq_layer* layer, const uint8_t* codes, const uint8_
  *   q_out, k_out  as q, k, with token strides of their own; an output may be its
  *                 own input (same pointer and stride).
  * head_dim % 8 == 0 up to 256; rot % 16 == 0 (interleaved: % 8); strides multiples
- * of 16 bytes; pointers 16-byte aligned.  fp32 arithmetic, one rounding at the end;
- * rows whose squares leave fp32's range are formed in fp64.
+ * of 16 bytes; pointers 16-byte aligned.  fp32 arithmetic, one rounding at the end
+ * (channels meet gains before the norm: gains from 2^-60 to 2^60, or 0); rows whose
+ * squares leave fp32's range are formed in fp64.
  */
 enum { OQ_QK_INTERLEAVED = 1, OQ_QK_NO_NORM = 2 };
 oq_status oq_qk_norm_rope(const void* q, int64_t q_stride, int32_t q_heads, const void* k, int64_t k_stride, int32_t k_heads,
@@ -662,10 +663,11 @@ oq_status oq_kv4_poll_error(const oq_kv4* kv);
  * division: without zeros s = bf16(max|w| / 7), c = clamp(round(w / s) + 8); with
  * zeros s = bf16((max(w, 0) - min(w, 0)) / 15), z = round(-min(w, 0) / s), c =
  * clamp(round(w / s) + z), all clamped to 0 .. 15, halves to even.  A group that
- * holds an infinity or a NaN gets scale NaN; one whose scale is 0 reads as zeros.
+ * holds an infinity or a NaN, or whose scale overflows, gets scale NaN; one whose scale
+ * is 0 reads as zeros.
  *
- * oq_linear_w4g -- x [T, d_in], y [T, d_out], each bf16 or fp32.  Products are
- * exact (fp32 tokens too), sums fp32.  Results repeat bit for bit.  A call streams
+ * oq_linear_w4g -- x [T, d_in], y [T, d_out], each bf16 or fp32.  Products (c - z) x
+ * are exact (of fp32 tokens too, down to 2^-110), sums fp32.  Results repeat bit for bit.  A call streams
  * the weights once for 32 tokens (10 in fp32).
  */
 oq_status oq_w4g_prepare(const void* W, int32_t W_dtype, int32_t d_out, int32_t d_in, int32_t group, uint8_t* codes,
