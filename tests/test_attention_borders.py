@@ -198,3 +198,23 @@ def test_small_query_channels_meet_large_keys(env, D, H, KH):
     s.cache.copy_(torch.from_numpy(s.np_cache))
     q = torch.from_numpy((rng.uniform(1, 2, (s.T, H, D)) * rng.choice([-1, 1], (s.T, H, D)) * down).astype(np.float32)).cuda().bfloat16()
     _check_attention(torch, B, kv, s, q)
+
+
+@pytest.mark.parametrize("D,H,KH", [(128, 1, 1), (64, 4, 2), (64, 8, 1), (128, 16, 1), (64, 32, 2), (128, 60, 1), (64, 128, 2)])
+def test_far_queries_beside_others(env, D, H, KH):
+    """Of neighbouring queries one has scores of 10^9, one of 10^30 and one is NaN: the others keep their bounds."""
+    torch, B = env
+    rng = np.random.default_rng(46)
+    kv = B.oq_kv4_create(H, KH, D)
+    s = Streams(torch, rng, kv, [1, 3], [700, 300])
+    for b, m in enumerate(s.lens):
+        for j in range(m):
+            A.write_token(s.np_cache, s.pages[b, j // 128], j % 128, rng.standard_normal(KH * D), rng.standard_normal(KH * D))
+    s.cache.copy_(torch.from_numpy(s.np_cache))
+    q = rng.standard_normal((s.T, H, D)).astype(np.float32)
+    q[0, ::5] *= 1e9
+    q[1:, 2::7] *= 1e30
+    q[2, 1::6] = np.nan
+    q = torch.from_numpy(q).cuda().bfloat16()
+    for window in (0, 100):
+        _check_attention(torch, B, kv, s, q, window=window)
