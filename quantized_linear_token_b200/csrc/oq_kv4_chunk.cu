@@ -8,7 +8,7 @@
 // queries take turns: while the tensor cores do one's P V and next S, the other's
 // four warps form P, a thread a query, no shuffles.  P takes S's place in tensor
 // memory and is the second product's A operand from there.  The reference is moved
-// (and O rescaled) only when a weight exceeds it by 2^8.
+// (and O rescaled) only when a weight exceeds it by 2^8, once a tile at most.
 //
 // Decoding: e2m1's bits s e e m shifted into a bf16's sign, exponent and mantissa are
 // its value times 2^-126, exactly (subnormals too); two products bring in 2^126 and
@@ -16,10 +16,11 @@
 // keys) and tokens (of values) lie permuted within each eight, and q's channels and
 // P's tokens are taken in the same order.
 //
-// Bound: issue slots, those of the softmax (an exponential and about four instructions
-// a score) with those of the decoding.  Measured, 1560 queries over 7800 tokens x 40 heads
-// of 128: 388 us, 640 TFLOP/s (154 us at the rate of a large library product).  Four
-// decoding warps and two passes over S took 448.
+// Bound: a query tile's softmax and the MMAs in turn (S of the next tile waits for P V of this
+// one, since P lies in S's place), with the decoding beside them; no unit is full: issue
+// slots 52 % active, the tensor pipe and the exponential unit 35 %.  Measured, 1560 queries over
+// 7800 tokens x 40 heads of 128: 381 us, 654 TFLOP/s (154 us at the rate of a large
+// library product).  Four decoding warps and two passes over S took 448.
 //
 // Warps: 0-3 and 4-7 the two query tiles, 8-15 decoding, 16 tensor memory and MMAs
 // (17-19 only give up registers).

@@ -14,8 +14,9 @@
 // that small CTAs fill all SMs evenly; warps' and CTAs' sums are added in a fixed
 // order through shared memory.
 //
-// Bound: issue slots of the decoding and the MMAs, at 12 to 24 warps an SM, and the
-// launch.  Measured, bf16 tokens: one token x 13824 inputs x 5120 outputs, groups of 128,
+// Bound: latency that 12 to 24 warps an SM leave exposed (issue slots 46 to 48 % active, the
+// integer pipe half busy; scales, zeros and tokens are awaited before a chunk's first MMA),
+// and the launch.  Measured, bf16 tokens: one token x 13824 inputs x 5120 outputs, groups of 128,
 // 13.3 us (the bytes alone 5.6); 13 tokens x 5120 x 13824, groups of 32 with zeros, 23.5 us
 // (6.5).  A form on the tensor cores that read shared memory (codes as e4m3 subnormals,
 // tokens in two e4m3 terms, 128 rows a CTA) took 19.5 and 52: tiles of 128 rows read 128
@@ -420,7 +421,9 @@ cudaError_t launch_tiles(W4gParams& p, cudaStream_t st) {
   // of 64, 15.3 and 18.6; 8192 -> 28672 31.8 and 33.3, 45.0 and 51.4.  Otherwise 16 rows,
   // whose CTAs read a row to its end: 4096 -> 6144 6.6 us and 7.1, 8.7 and 11.0; but long rows
   // are split, over CTAs of 32 rows and 4 warps: 13824 -> 5120 13.3 and, with 16 rows, 14.0,
-  // 18.9 and 21.9; 4096 -> 4096 6.1 and 5.9, 9.9 and 7.7.
+  // 18.9 and 21.9; 4096 -> 4096 6.1 and 5.9, 9.9 and 7.7.  Between (to 5120, groups of 128, one
+  // token and eight): 6144 7.9 and 8.1, 11.8 and 10.4; 8192 9.0 and 9.2, 13.7 and 12.7; 10240
+  // 10.3 and 10.9, 15.2 and 15.2.
   if (columns <= 8) {
     const int64_t ctas = (p.a.N + ROWS - 1) / ROWS * ((p.a.T + p.per_cta - 1) / p.per_cta);
     if (ctas > Cfg<1, 1, 8>::MIN_CTAS * (int64_t)sms) return launch_one<X, GROUP, ZEROS, 1, 2, 8>(p, st);
