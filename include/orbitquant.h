@@ -575,7 +575,8 @@ oq_status oq_qk_norm_rope(const void* q, int64_t q_stride, int32_t q_heads, cons
  *                 264-271  V scales, byte [token][channel / 32]
  *   page_table  device int32 [B, table_width]: the page of tokens 128 i .. of a
  *               sequence.  An entry outside [0, pages) is a page that is not
- *               there: nothing is written to it, its tokens are not seen.
+ *               there: nothing is written to it, its tokens are not seen.  table_width
+ *               is at most 2^23 (2^30 tokens), B at most 65535.
  *   cu          device int32 [B + 1]: sequence b's tokens in this call are rows
  *               cu[b] .. cu[b + 1] - 1 of q, k, v and y.
  *   lens        device int32 [B]: tokens of the sequence in the cache, this call's

@@ -119,7 +119,8 @@ oq_status check_cache(const char* who, const oq_kv4* kv, const void* cache, int6
     return invalid(who, "page_table, cu and lens must be 4-byte aligned pointers");
   if (pages == 0 || pages > 0x7FFFFFFF / KV_ROWS / kv->groups)
     return unsupported(who, "the cache must have a page and at most 2^31 / 272 groups of 128 channels in its pages");
-  if (width > 0x7FFFFFFF / KV_PAGE || B > 65535) return unsupported(who, "table_width or B too large");
+  // (attention marks tokens that are not there by a place of 2^30)
+  if (width > (1 << 30) / KV_PAGE || B > 65535) return unsupported(who, "at most 2^23 pages a sequence and 65535 sequences");
   if (!on_device(kv)) return invalid(who, "the handle was created on another device than the current one");
   view->cache = static_cast<uint8_t*>(const_cast<void*>(cache));
   view->pages = pages;
@@ -353,7 +354,7 @@ oq_status oq_kv4_attention(const oq_kv4* kv, const void* q, int64_t q_stride, in
   a.D = kv->head_dim;
   a.max_q = max_q;
   a.max_len = max_len;
-  a.window = window < (1 << 30) ? window : 0;   // (a cache has fewer tokens: everything is within it)
+  a.window = window < (1 << 30) ? window : 0;   // (a sequence has no more tokens: everything is within it)
   a.causal = (flags & OQ_ATTN_CAUSAL) != 0;
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;

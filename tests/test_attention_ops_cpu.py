@@ -269,3 +269,11 @@ def test_small_query_elements_are_off_by_little():
         hi = R.code_values(R.round_codes(y, 8), 8)
         lo = R.code_values(R.round_codes((y - hi) * 32, 8), 8) / 32
         assert np.abs(hi + lo - y).max() <= 128 * 2.0 ** -22
+
+
+def test_tables_of_more_than_2_30_tokens_are_refused(lib, kv):
+    """Places from 2^30 on are what attention takes for tokens that are not there, and for no window."""
+    h = ctypes.byref(kv)
+    for w, want in ((1 << 23, 0), ((1 << 23) + 1, 2), ((1 << 24) - 1, 2)):
+        assert lib.oq_kv4_attention(h, P, 1024, 3, 64 * P, 8, 5 * P, w, 6 * P, 7 * P, 2, 0, 300, 0.1, 1, 0, 2 * P, None, 0, None) == want
+        assert lib.oq_kv4_read(h, 64 * P, 8, 5 * P, w, 6 * P, 7 * P, 2, 0, P, 2 * P, 0, None) == want
